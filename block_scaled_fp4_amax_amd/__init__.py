@@ -2,7 +2,8 @@
 block-scaled FP4 quantisation library.
 
 The functions carry the C-ABI names (fp4_quantize, fp4_dequantize, fp4_qdq,
-fp4_cast_transpose, fp4_cast_transpose_grouped and the fp4q_* helpers).  They
+fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_kv_append,
+fp4_kv_read, fp4_attn and the fp4q_* helpers).  They
 only marshal arguments: torch supplies device memory and the current HIP
 stream, every step of the computation runs in the library's HIP kernels.  If
 the library is not built, importing the binding raises; there is no fallback.
@@ -16,7 +17,8 @@ __all__ = [
     "Fp4Error", "Cfg", "Sizes", "make_cfg", "lib", "fp4q_abi_version", "fp4q_status_str", "fp4q_buffer_sizes",
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
-    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "LIB_PATH",
+    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "KVCache", "fp4_kv_append",
+    "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -49,6 +51,19 @@ class Cfg(ct.Structure):
 class Sizes(ct.Structure):
     _fields_ = [(n, ct.c_size_t) for n in ("row_codes", "row_scales", "row_outer", "col_codes", "col_scales",
                                            "col_outer", "y", "residual", "workspace")]
+
+
+class _KvCache(ct.Structure):
+    _fields_ = [(n, ct.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales", "k_outer", "v_outer")] + [
+        ("num_pages", ct.c_int64), ("page_size", ct.c_int32), ("kv_heads", ct.c_int32), ("head_dim", ct.c_int32),
+        ("reserved", ct.c_int32)]
+
+
+class _Attn(ct.Structure):
+    _fields_ = [("q", ct.c_void_p), ("ld_q", ct.c_int64)] + [
+        (n, ct.c_void_p) for n in ("page_table", "kv_lens", "q_starts", "sinks", "out", "lse")] + [
+        ("scale", ct.c_float)] + [(n, ct.c_int32) for n in ("batch", "total_q", "q_heads", "table_cols", "max_q",
+                                                            "max_kv", "causal", "window")]
 
 
 def make_cfg(format="nvfp4", scale_format=None, two_level="none", outer_block_size=0, outer_2d=False,
@@ -120,6 +135,15 @@ def lib():
         L.fp4_mx_scales_tiled.argtypes = [P, I64, I64, P, P]
         L.fp4_mx_project_fp8.restype = ct.c_int
         L.fp4_mx_project_fp8.argtypes = [C, P, I64, I64, I64, P, P, P, P, P, P, P, P, P]
+        KV, AT = ct.POINTER(_KvCache), ct.POINTER(_Attn)
+        L.fp4_kv_append.restype = ct.c_int
+        L.fp4_kv_append.argtypes = [C, KV, P, I64, P, I64, P, I64, P]
+        L.fp4_kv_read.restype = ct.c_int
+        L.fp4_kv_read.argtypes = [C, KV, P, I64, P, P, P]
+        L.fp4q_attn_workspace_bytes.restype = SZ
+        L.fp4q_attn_workspace_bytes.argtypes = [C, KV, AT]
+        L.fp4_attn.restype = ct.c_int
+        L.fp4_attn.argtypes = [C, KV, AT, P, SZ, P]
         if L.fp4q_abi_version() != ABI_VERSION:
             raise ImportError("libfp4q.so ABI %d, binding expects %d" % (L.fp4q_abi_version(), ABI_VERSION))
         _lib = L
@@ -508,6 +532,190 @@ def fp4_mm(a, b, cfg=None, *, out_dtype=None, c=None, stream=None):
     _check(lib().fp4_mm(ct.byref(ccfg), _ptr(ac), _ptr(asc), _ptr(bc), _ptr(bsc), M, N, K, la, _ptr(c),
                         c.stride(0) if M > 1 else N, _stream(stream)), "fp4_mm")
     return c
+
+
+# ------------------------------------------------------------------ the paged 4-bit cache
+def _held_on(t, stream):
+    """A tensor allocated here stays reserved until the work of a caller's
+    stream that uses it is done."""
+    if stream is not None:
+        torch = _torch()
+        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return t
+
+
+def _heads_rows(t, heads, dim, what, dtypes):
+    """Token pitch of a [tokens, heads, dim] tensor whose tokens are whole runs."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError("%s must be [tokens, %d, %d], got %s" % (what, heads, dim, tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise Fp4Error(ERR_DTYPE, "%s dtype %s" % (what, t.dtype))
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError("%s: a token's heads must be contiguous" % what)
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _ints(t, dtype, shape, what, device):
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s must be %s of shape %s, got %s %s" % (what, dtype, list(shape), t.dtype, list(t.shape)))
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be contiguous and on %s" % (what, device))
+
+
+class KVCache:
+    """The paged 4-bit cache of one layer's keys and values (layout and rules
+    in include/fp4q.h): uint8 codes [pages, kv_heads, page_size, head_dim / 2]
+    and scales [pages, kv_heads, page_size, head_dim / 16] (/ 32 for MXFP4), and with
+    cfg two_level "tensorwise", outer_mode 1, the calibrated float32 scales k_outer and v_outer
+    [kv_heads].  The tensors are the caller's; KVCache.empty() allocates them."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, cfg, *, k_outer=None, v_outer=None):
+        torch = _torch()
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, kv_heads, page_size, head_dim / 2]")
+        pages, heads, page, half = k_codes.shape
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, half * 2
+        self.cfg = cfg
+        self.device = k_codes.device
+        shapes = {"k_codes": half, "v_codes": half, "k_scales": half * 2 // _inner(cfg),
+                  "v_scales": half * 2 // _inner(cfg)}
+        for n, t in (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)):
+            want = (pages, heads, page, shapes[n])
+            if tuple(t.shape) != want or t.dtype != torch.uint8 or not t.is_contiguous() or t.device != self.device:
+                raise ValueError("%s must be a contiguous uint8 %s on %s" % (n, list(want), self.device))
+        for n, t in (("k_outer", k_outer), ("v_outer", v_outer)):
+            if t is not None and (tuple(t.shape) != (heads,) or t.dtype != torch.float32 or not t.is_contiguous()
+                                  or t.device != self.device):
+                raise ValueError("%s must be a contiguous float32 [%d] on %s" % (n, heads, self.device))
+        if (k_outer is None) != (v_outer is None) or (k_outer is not None) != (cfg.two_level == TWO_LEVEL["tensorwise"]):
+            raise ValueError("k_outer and v_outer go with cfg two_level 'tensorwise' (outer_mode 1), and only with it")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_outer, self.v_outer = k_outer, v_outer
+        self._c = _KvCache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_outer), _ptr(v_outer),
+                           pages, page, heads, half * 2, 0)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, cfg, *, device="cuda", k_outer=None, v_outer=None):
+        """A cache of zeros."""
+        torch = _torch()
+        codes, scales = ((num_pages, kv_heads, page_size, n) for n in (head_dim // 2, head_dim // _inner(cfg)))
+        z = [torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, scales, codes, scales)]
+        return cls(*z, cfg, k_outer=k_outer, v_outer=v_outer)
+
+
+def fp4_kv_append(cache, k, v, slots, *, stream=None):
+    """Quantises k and v (bf16 or float32 [tokens, kv_heads, head_dim]; views with a
+    token pitch are accepted) into the cache's slots (int64 [tokens], page *
+    page_size + place; a slot outside the cache writes nothing)."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    ld_k = _heads_rows(k, cache.kv_heads, cache.head_dim, "k", types)
+    ld_v = _heads_rows(v, cache.kv_heads, cache.head_dim, "v", types)
+    if k.dtype != v.dtype or k.shape != v.shape or k.device != cache.device or v.device != cache.device:
+        raise ValueError("k and v must agree in shape and dtype and lie on the cache's device")
+    _ints(slots, torch.int64, (k.shape[0],), "slots", cache.device)
+    cfg = _with_dtypes(cache.cfg, _dtype_name(k))
+    _check(lib().fp4_kv_append(ct.byref(cfg), ct.byref(cache._c), _ptr(k), ld_k, _ptr(v), ld_v, _ptr(slots), k.shape[0],
+                               _stream(stream)), "fp4_kv_append")
+
+
+def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
+    """(k, v): bf16 (or float32: dtype) [tokens, kv_heads, head_dim] that the
+    cache holds at slots (int64 [tokens]; zeros for one outside the cache).  `out` may supply
+    the pair."""
+    torch = _torch()
+    n = slots.shape[0] if slots.dim() else 0
+    _ints(slots, torch.int64, (None,), "slots", cache.device)
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if out is None:
+        dtype = dtype if dtype is not None else torch.bfloat16
+        k, v = (_held_on(torch.empty(shape, dtype=dtype, device=cache.device), stream) for _ in "kv")
+    else:
+        k, v = out
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise Fp4Error(ERR_DTYPE, "k dtype %s" % k.dtype)
+    for t in (k, v):
+        if tuple(t.shape) != shape or t.dtype != k.dtype or not t.is_contiguous() or t.device != cache.device:
+            raise ValueError("out must be two contiguous %s tensors of one dtype" % list(shape))
+    cfg = _with_dtypes(cache.cfg, output_dtype=_dtype_name(k))
+    _check(lib().fp4_kv_read(ct.byref(cfg), ct.byref(cache._c), _ptr(slots), n, _ptr(k), _ptr(v), _stream(stream)),
+           "fp4_kv_read")
+    return k, v
+
+
+def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=None, table_cols=None, window=0):
+    """Scratch for fp4_attn calls of this size (None if they need none), to keep
+    between calls.  max_q, max_kv, window and table_cols as in the call; without
+    table_cols, the columns that max_kv needs."""
+    torch = _torch()
+    if max_kv is None and table_cols is None:
+        raise ValueError("give max_kv or table_cols")
+    if table_cols is None:
+        table_cols = -(-int(max_kv) // cache.page_size)
+    a = _Attn(batch=int(batch), total_q=int(total_q), q_heads=int(q_heads), table_cols=int(table_cols),
+              max_q=int(total_q if max_q is None else max_q),
+              max_kv=int(table_cols * cache.page_size if max_kv is None else max_kv), causal=1, window=int(window),
+              scale=1.0, ld_q=int(q_heads) * cache.head_dim, q_starts=16)
+    n = lib().fp4q_attn_workspace_bytes(ct.byref(cache.cfg), ct.byref(cache._c), ct.byref(a))
+    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+
+def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv=None, scale=None, causal=True, window=0,
+             sinks=None, out=None, out_dtype=None, with_lse=False, workspace=None, stream=None):
+    """Attention of q (bf16 [tokens, q_heads, head_dim]) over the cache (see
+    include/fp4q.h for masks, limits and rounding).
+
+    page_table   int32 [batch, cols], kv_lens int32 [batch] on the device.
+    q_starts     int32 [batch + 1]: sequence b's queries are q[q_starts[b]:
+                 q_starts[b + 1]]; None: one query each.
+    max_q, max_kv  bounds of the sequences' query and key counts (default: all of q,
+                 all that the page table can name); tight ones make better launches.
+    scale        of q . k, default head_dim ** -0.5.
+    window       > 0: each query sees at most that many keys, up to its own.
+    sinks        float32 [q_heads]: a logit that joins each row's softmax.
+    Returns out (bf16, or out_dtype float32), or (out, lse) with with_lse."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    T, Hq, D = q.shape
+    ld = _heads_rows(q, Hq, cache.head_dim, "q", (torch.bfloat16,))
+    dev = cache.device
+    if q.device != dev:
+        raise ValueError("q must be on the cache's device")
+    _ints(kv_lens, torch.int32, (None,), "kv_lens", dev)
+    batch = kv_lens.shape[0]
+    _ints(page_table, torch.int32, (batch, None), "page_table", dev)
+    if q_starts is not None:
+        _ints(q_starts, torch.int32, (batch + 1,), "q_starts", dev)
+    elif T != batch:
+        raise ValueError("without q_starts, q holds one query for each of the %d sequences, got %d" % (batch, T))
+    if sinks is not None and (sinks.dtype != torch.float32 or tuple(sinks.shape) != (Hq,) or not sinks.is_contiguous()
+                              or sinks.device != dev):
+        raise ValueError("sinks must be a contiguous float32 [%d] on %s" % (Hq, dev))
+    if out is None:
+        out = _held_on(torch.empty((T, Hq, D), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=dev),
+                       stream)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise Fp4Error(ERR_DTYPE, "out dtype %s" % out.dtype)
+    if tuple(out.shape) != (T, Hq, D) or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous %s on %s" % ([T, Hq, D], dev))
+    lse = _held_on(torch.empty((T, Hq), dtype=torch.float32, device=dev), stream) if with_lse else None
+    cols = page_table.shape[1]
+    if max_q is None:
+        max_q = 1 if q_starts is None else T
+    if max_kv is None:
+        max_kv = cols * cache.page_size
+    a = _Attn(_ptr(q), ld, _ptr(page_table), _ptr(kv_lens), _ptr(q_starts), _ptr(sinks), _ptr(out), _ptr(lse),
+              float(D ** -0.5 if scale is None else scale), batch, T, Hq, cols, int(max_q), int(max_kv),
+              int(bool(causal)), int(window))
+    cfg = cache.cfg if out.dtype == torch.bfloat16 else _with_dtypes(cache.cfg, output_dtype="fp32")
+    need = lib().fp4q_attn_workspace_bytes(ct.byref(cfg), ct.byref(cache._c), ct.byref(a))
+    if need and workspace is None:
+        workspace = _held_on(_empty(need, torch.uint8, dev), stream)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().fp4_attn(ct.byref(cfg), ct.byref(cache._c), ct.byref(a), _ptr(workspace), size, _stream(stream)),
+           "fp4_attn")
+    return (out, lse) if with_lse else out
 
 
 class ErrorFeedback:

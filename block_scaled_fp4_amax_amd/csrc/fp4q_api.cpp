@@ -725,4 +725,179 @@ size_t fp4q_cast_transpose_workspace_bytes(const fp4q_cfg* cfg, int32_t groups, 
     return ct_workspace_bytes(r, with_residual != 0, groups, rows_per_group, cols);
 }
 
+namespace {
+
+// Configuration of a 4-bit cache: RNE rows of one tensor per head, whose FP32
+// scale, if any, is given.
+int resolve_cache(const fp4q_cfg* cfg, const fp4q_kv_cache* c, Resolved& r, KvView& v)
+{
+    const int st = resolve(cfg, r);
+    if (st) return st;
+    if (!c) return FP4Q_ERR_NULL;
+    if (r.sr || r.outer_kind == kOuter1D || r.outer_kind == kOuter2D) return FP4Q_ERR_UNSUPPORTED;
+    if (r.inner2d || (r.outer_kind == kOuterTensor && !r.given)) return FP4Q_ERR_MODE;
+    if (c->num_pages < 0 || c->kv_heads < 1 || c->page_size < kKvGroup || c->page_size % kKvGroup)
+        return FP4Q_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FP4Q_ERR_UNSUPPORTED;
+    if (c->page_size > kKvMaxPage || c->kv_heads > 65535 || c->num_pages > ((int64_t)1 << 31) - 1)
+        return FP4Q_ERR_UNSUPPORTED;
+    if (c->num_pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)) return FP4Q_ERR_NULL;
+    if (r.outer_kind == kOuterTensor && (!c->k_outer || !c->v_outer)) return FP4Q_ERR_NULL;
+    if (misaligned(c->k_codes, 16) || misaligned(c->k_scales, 16) || misaligned(c->v_codes, 16) ||
+        misaligned(c->v_scales, 16) || misaligned(c->k_outer, 4) || misaligned(c->v_outer, 4))
+        return FP4Q_ERR_ALIGN;
+    const bool outer = r.outer_kind == kOuterTensor;
+    v = KvView{c->k_codes, c->k_scales, c->v_codes, c->v_scales, outer ? c->k_outer : nullptr,
+               outer ? c->v_outer : nullptr, c->num_pages, c->page_size, c->kv_heads, c->head_dim};
+    return FP4Q_OK;
+}
+
+constexpr int64_t kMaxKvRows = (int64_t)1 << 27;     // tokens of one append or read
+
+int check_attn(const KvView& kv, const fp4q_attn* a)
+{
+    if (!a) return FP4Q_ERR_NULL;
+    if (a->batch < 0 || a->total_q < 0 || a->table_cols < 0 || a->max_q < 0 || a->max_kv < 0 || a->window < 0)
+        return FP4Q_ERR_SHAPE;
+    if (a->q_heads < 1 || a->q_heads % kv.heads) return FP4Q_ERR_SHAPE;
+    if (!a->q_starts && a->total_q != a->batch) return FP4Q_ERR_SHAPE;
+    if (a->total_q > 1 && a->ld_q < (int64_t)a->q_heads * kv.dim) return FP4Q_ERR_SHAPE;
+    if ((a->causal != 0 && a->causal != 1) || (a->window > 0 && !a->causal)) return FP4Q_ERR_MODE;
+    if (!(a->scale > 0.0f) || a->scale > 3.4028235e38f) return FP4Q_ERR_MODE;
+    if (a->max_kv > kKvMaxTokens || (int64_t)a->table_cols * kv.page_size >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)a->max_q * (a->q_heads / kv.heads);
+    if (rows > ((int64_t)1 << 22) || a->batch > 65535 || (int64_t)a->total_q * a->q_heads >= (int64_t)1 << 31)
+        return FP4Q_ERR_UNSUPPORTED;
+    return FP4Q_OK;
+}
+
+// How a call's keys are split over workgroups, and the scratch that takes.
+struct AttnPlan {
+    int32_t splits, chunk;
+    size_t ml, o;
+};
+
+AttnPlan plan_attn(const KvView& kv, const fp4q_attn* a)
+{
+    const int64_t rows = (int64_t)a->max_q * (a->q_heads / kv.heads);
+    // keys that one tile of rows can see
+    int64_t keys = std::min<int64_t>(a->max_kv, (int64_t)a->table_cols * kv.page_size);
+    if (a->window) keys = std::min<int64_t>(keys, (int64_t)a->window + a->max_q + 32);
+    AttnPlan p{1, 128, 0, 0};
+    if (rows == 0 || a->batch == 0) return p;
+    p.splits = attn_splits(a->batch, kv.heads, rows, keys);
+    p.splits = (int32_t)std::min<int64_t>(p.splits, std::max<int64_t>(1, 65535 / a->batch));
+    p.chunk = (int32_t)((keys + p.splits * 128 - 1) / (p.splits * 128) * 128);
+    if (p.chunk < 128) p.chunk = 128;
+    if (p.splits > 1) {
+        const size_t n = (size_t)p.splits * a->total_q * a->q_heads;
+        p.ml = n * 2 * sizeof(float);
+        p.o = n * kv.dim * sizeof(float);
+    }
+    return p;
+}
+
+}  // namespace
+
+int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k, int64_t ld_k, const void* v,
+                  int64_t ld_v, const int64_t* slots, int64_t tokens, void* stream)
+{
+    Resolved r;
+    KvAppendArgs a;
+    const int st = resolve_cache(cfg, cache, r, a.kv);
+    if (st) return st;
+    const int64_t row = (int64_t)a.kv.heads * a.kv.dim;
+    if (tokens < 0 || (tokens > 1 && (ld_k < row || ld_v < row))) return FP4Q_ERR_SHAPE;
+    if (tokens > kMaxKvRows || ld_k > ((int64_t)1 << 31) || ld_v > ((int64_t)1 << 31)) return FP4Q_ERR_UNSUPPORTED;
+    if (tokens == 0 || a.kv.num_pages == 0) return FP4Q_OK;
+    if (!k || !v || !slots) return FP4Q_ERR_NULL;
+    const int64_t per16 = r.x_f32 ? 4 : 8;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8) ||
+        (tokens > 1 && (ld_k % per16 || ld_v % per16)))
+        return FP4Q_ERR_ALIGN;
+    a.k = k;
+    a.v = v;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.num_slots = a.kv.num_pages * a.kv.page_size;
+    return hip_status(launch_kv_append(r.bias, r.x_f32, a, (hipStream_t)stream));
+}
+
+int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                void* stream)
+{
+    Resolved r;
+    KvReadArgs a;
+    const int st = resolve_cache(cfg, cache, r, a.kv);
+    if (st) return st;
+    if (tokens < 0) return FP4Q_ERR_SHAPE;
+    if (tokens > kMaxKvRows) return FP4Q_ERR_UNSUPPORTED;
+    if (tokens == 0) return FP4Q_OK;
+    if (!k || !v || !slots) return FP4Q_ERR_NULL;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8)) return FP4Q_ERR_ALIGN;
+    a.k = k;
+    a.v = v;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.num_slots = a.kv.num_pages * a.kv.page_size;
+    return hip_status(launch_kv_read(r.bias, r.y_f32, a, (hipStream_t)stream));
+}
+
+size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn)
+{
+    Resolved r;
+    KvView kv;
+    if (resolve_cache(cfg, cache, r, kv) || check_attn(kv, attn)) return 0;
+    const AttnPlan p = plan_attn(kv, attn);
+    return p.ml + p.o;
+}
+
+int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
+             size_t workspace_bytes, void* stream)
+{
+    Resolved r;
+    AttnArgs a;
+    int st = resolve_cache(cfg, cache, r, a.kv);
+    if (st) return st;
+    st = check_attn(a.kv, attn);
+    if (st) return st;
+    if (attn->batch == 0 || attn->total_q == 0 || attn->max_q == 0) return FP4Q_OK;
+    if (!attn->q || !attn->kv_lens || !attn->out || (attn->table_cols > 0 && !attn->page_table))
+        return FP4Q_ERR_NULL;
+    if (misaligned(attn->q, 16) || misaligned(attn->out, 16) || misaligned(attn->page_table, 4) ||
+        misaligned(attn->kv_lens, 4) || misaligned(attn->q_starts, 4) || misaligned(attn->sinks, 4) ||
+        misaligned(attn->lse, 4) || (attn->total_q > 1 && attn->ld_q % 8))
+        return FP4Q_ERR_ALIGN;
+    const AttnPlan p = plan_attn(a.kv, attn);
+    if (p.splits > 1 && (!workspace || workspace_bytes < p.ml + p.o)) return FP4Q_ERR_WORKSPACE;
+    if (p.splits > 1 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
+    a.q = attn->q;
+    a.ld_q = attn->ld_q;
+    a.table = attn->page_table;
+    a.kv_lens = attn->kv_lens;
+    a.q_starts = attn->q_starts;
+    a.sinks = attn->sinks;
+    a.out = attn->out;
+    a.lse = attn->lse;
+    a.part_o = (float*)workspace;
+    a.part_ml = (float*)((char*)workspace + p.o);
+    a.scale = attn->scale;
+    a.batch = attn->batch;
+    a.total_q = attn->total_q;
+    a.q_heads = attn->q_heads;
+    a.group = attn->q_heads / a.kv.heads;
+    a.table_cols = attn->table_cols;
+    a.max_q = attn->max_q;
+    a.max_kv = attn->max_kv;
+    a.causal = attn->causal;
+    a.window = attn->window;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.out_f32 = r.y_f32 ? 1 : 0;
+    a.per_page = make_div((uint32_t)(a.kv.page_size / kKvGroup));
+    return hip_status(launch_attn(r.bias, a, (hipStream_t)stream));
+}
+
 }  // extern "C"

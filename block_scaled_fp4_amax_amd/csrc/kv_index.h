@@ -1,0 +1,116 @@
+// kv_index.h -- index arithmetic of the paged 4-bit cache and of attention
+// over it, shared by the kernels, the host layer and the CPU tests (plain
+// integer functions without device state).
+//
+// The cache holds, for K and for V, codes [num_pages][kv_heads][page_size]
+// [head_dim / 2] and scale bytes [num_pages][kv_heads][page_size][head_dim /
+// block]: a page's rows of one head are contiguous, and each row is laid out as
+// fp4_quantize lays out a row of head_dim values.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define FP4Q_HD __host__ __device__ __forceinline__
+#else
+#define FP4Q_HD inline
+#endif
+
+namespace fp4q {
+
+constexpr int kKvGroup = 16;             // tokens the kernels address together; page_size is a multiple
+constexpr int kKvMaxPage = 4096;         // bounds that keep DivBy exact (see there)
+constexpr int64_t kKvMaxTokens = (int64_t)1 << 27;   // keys of one sequence
+
+// Exact u / d for u < 2^32 / d, by one multiplication: M = ceil(2^32 / d) gives
+// u M / 2^32 = u / d + u e / (d 2^32) with 0 <= e < d, and the excess stays
+// below 1 / d.  Divides a token group's number (below 2^27 / 16) by the groups of a
+// page (at most 256).
+struct DivBy {
+    uint64_t m;
+    uint32_t d;
+};
+
+inline DivBy make_div(uint32_t d) { return DivBy{(((uint64_t)1 << 32) + d - 1) / d, d}; }
+
+FP4Q_HD uint32_t div_by(uint32_t u, const DivBy& k) { return (uint32_t)((u * k.m) >> 32); }
+
+// Row of a slot (= page * page_size + place in the page) of one head: the row
+// number to multiply by the bytes of a row, or -1 for a slot outside the cache.
+FP4Q_HD int64_t kv_row_of_slot(int64_t slot, int64_t num_slots, int32_t page_size, int32_t heads, int32_t head)
+{
+    if (slot < 0 || slot >= num_slots) return -1;
+    const int64_t page = slot / page_size;
+    return (page * heads + head) * page_size + (slot - page * page_size);
+}
+
+// The group of 16 tokens starting at token t of a sequence: its first row and
+// whether it may be read.  Groups at or beyond the end of the keys never read
+// the page table; a page number outside the cache makes its tokens absent.  An
+// absent group reads the cache's first rows (any bytes) and masks them.
+struct KvGroup {
+    int64_t row;
+    bool ok;
+};
+
+FP4Q_HD KvGroup kv_group(const int32_t* table_row, int32_t t, int32_t kv_end, const DivBy& groups_per_page,
+                         int64_t num_pages, int32_t heads, int32_t head)
+{
+    KvGroup g{0, false};
+    if (t < kv_end) {
+        const uint32_t u = (uint32_t)t / kKvGroup;
+        const uint32_t p = div_by(u, groups_per_page);
+        const int32_t page = table_row[p];
+        if (page >= 0 && page < num_pages) {
+            const int32_t page_size = (int32_t)groups_per_page.d * kKvGroup;
+            g.row = ((int64_t)page * heads + head) * page_size + (int64_t)(u - p * groups_per_page.d) * kKvGroup;
+            g.ok = true;
+        }
+    }
+    return g;
+}
+
+// A sequence's keys: its stated length, cut to what the page table can name
+// and to the caller's bound.
+FP4Q_HD int32_t kv_length(int32_t stated, int32_t max_kv, int32_t table_cols, int32_t page_size, int64_t num_pages)
+{
+    int64_t n = stated < 0 ? 0 : stated;
+    if (n > max_kv) n = max_kv;
+    const int64_t cap = (int64_t)table_cols * page_size;
+    if (n > cap) n = cap;
+    return num_pages > 0 ? (int32_t)n : 0;
+}
+
+// Queries of a sequence: rows [first, first + count) of q, cut to the tensor
+// and to the caller's bound.
+struct QueryRange {
+    int32_t first, count;
+};
+
+FP4Q_HD QueryRange query_range(int32_t begin, int32_t end, int32_t total, int32_t max_q)
+{
+    if (begin < 0) begin = 0;
+    if (begin > total) begin = total;
+    if (end < begin) end = begin;
+    if (end > total) end = total;
+    const int32_t n = end - begin;
+    return QueryRange{begin, n < max_q ? n : max_q};
+}
+
+// Keys [lo, hi) that the query at place i of n sees, of kv keys: causal puts the
+// last query on the last key; a window keeps that many keys up to the query's own.
+struct KeyRange {
+    int32_t lo, hi;
+};
+
+FP4Q_HD KeyRange key_range(int32_t i, int32_t n, int32_t kv, int32_t causal, int32_t window)
+{
+    if (!causal) return KeyRange{0, kv};
+    int32_t hi = kv - n + i + 1;
+    if (hi < 0) hi = 0;
+    int32_t lo = window > 0 ? hi - window : 0;
+    if (lo < 0) lo = 0;
+    return KeyRange{lo, hi};
+}
+
+}  // namespace fp4q

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv_index.h"
+
 namespace fp4q {
 
 constexpr int kMaxGroupsPerLaunch = 64;
@@ -209,6 +211,59 @@ hipError_t launch_dequant_nv(int scale_bias, int outer_kind, int outer_transpose
 
 hipError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                              void* y, bool y_f32, hipStream_t s);
+
+// The paged 4-bit cache (layout in kv_index.h); k_outer / v_outer are FP32
+// [heads] or null.
+struct KvView {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    const float *k_outer, *v_outer;
+    int64_t num_pages;
+    int32_t page_size, heads, dim;
+};
+
+struct KvAppendArgs {
+    KvView kv;
+    const void *k, *v;       // bf16 or FP32 [tokens, heads, dim], token pitch ld_k / ld_v elements
+    int64_t ld_k, ld_v;
+    const int64_t* slots;    // [tokens]
+    int64_t tokens, num_slots;
+};
+
+struct KvReadArgs {
+    KvView kv;
+    void *k, *v;             // bf16 or FP32 [tokens, heads, dim]
+    const int64_t* slots;
+    int64_t tokens, num_slots;
+};
+
+// bias: 7 (E4M3), 15 (UE5M3) or 0 (MXFP4)
+hipError_t launch_kv_append(int bias, bool x_f32, const KvAppendArgs& a, hipStream_t s);
+hipError_t launch_kv_read(int bias, bool y_f32, const KvReadArgs& a, hipStream_t s);
+
+struct AttnArgs {
+    KvView kv;
+    const uint16_t* q;       // bf16 [total_q, q_heads, dim], token pitch ld_q
+    int64_t ld_q;
+    const int32_t* table;    // [batch, table_cols]
+    const int32_t* kv_lens;  // [batch]
+    const int32_t* q_starts; // [batch + 1], or null: query b is sequence b's
+    const float* sinks;      // [q_heads] or null
+    void* out;               // bf16 or FP32 [total_q, q_heads, dim]
+    float* lse;              // [total_q, q_heads] or null
+    float* part_o;           // [splits][total_q * q_heads][dim], splits > 1
+    float* part_ml;          // [splits][total_q * q_heads][2]
+    float scale;
+    int32_t batch, total_q, q_heads, group, table_cols, max_q, max_kv, causal, window;
+    int32_t splits, chunk;   // parts of a sequence's keys and the keys of one (a multiple of 128)
+    int32_t out_f32;
+    DivBy per_page;          // 16-token groups of a page
+};
+
+// Rows of queries (query x head of a group) that a workgroup of k_attn takes,
+// and how a call's keys are split.
+int attn_block_rows(int64_t rows);
+int attn_splits(int64_t batch, int32_t kv_heads, int64_t rows, int64_t max_kv);
+hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s);
 
 // partial maxima used by the tensorwise amax pass
 constexpr int kAmaxPartials = 512;

@@ -407,6 +407,106 @@ int fp4_mm(const fp4q_cfg* cfg, const uint8_t* a_codes, const uint8_t* a_scales,
 size_t fp4q_mx_scales_tiled_bytes(int64_t rows, int64_t K);
 int fp4_mx_scales_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* out, void* stream);
 
+/*
+ * The paged 4-bit cache of keys and values, for decoding with attention.
+ *
+ * A cache is num_pages pages of page_size tokens (a multiple of 16, at most
+ * 4096) for kv_heads heads of head_dim values (64, 128 or 256; others:
+ * FP4Q_ERR_UNSUPPORTED).  For K and for V:
+ *   codes   uint8 [num_pages][kv_heads][page_size][head_dim / 2]
+ *   scales  uint8 [num_pages][kv_heads][page_size][head_dim / 16] (/ 32: MXFP4)
+ * each row of head_dim values laid out and quantised as fp4_quantize does a row
+ * (RNE), so a page's rows of one head are contiguous.  cfg gives the format:
+ * two_level NONE, or TENSORWISE with outer_mode 1, where k_outer and v_outer hold one
+ * calibrated FP32 scale per head (finite, >= 0) by which rows are divided before
+ * they are quantised.  STOCHASTIC rounding and OUTER_BLOCK: FP4Q_ERR_UNSUPPORTED;
+ * inner_2d, or TENSORWISE with outer_mode 0: FP4Q_ERR_MODE.  All six buffers are device
+ * pointers (codes and scales 16-byte aligned); the struct itself is read on the
+ * host during the call.
+ *
+ * A token's place is its slot, page * page_size + place in the page.
+ */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    const float *k_outer, *v_outer;   /* FP32 [kv_heads], TENSORWISE only */
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim;
+    int32_t reserved;
+} fp4q_kv_cache;
+
+/*
+ * fp4_kv_append -- quantises new rows of K and V and writes them to their slots.
+ *   k, v    bf16 or FP32 (cfg->input_dtype) [tokens, kv_heads, head_dim] device, each
+ *           with a token pitch of ld_k / ld_v elements (>= kv_heads * head_dim, a whole
+ *           number of 16 bytes; ignored for one token), 16-byte aligned.
+ *   slots   int64 [tokens] device.  A slot below 0 or at or beyond num_pages *
+ *           page_size writes nothing (padding).  A slot named twice in one call
+ *           gets one of the rows, or parts of both.
+ * NaN and infinities are treated as in fp4_quantize.
+ */
+int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k, int64_t ld_k, const void* v,
+                  int64_t ld_v, const int64_t* slots, int64_t tokens, void* stream);
+
+/*
+ * fp4_kv_read -- the values that slots of the cache hold, dequantised as by
+ * fp4_dequantize.
+ *   k, v    bf16 or FP32 (cfg->output_dtype) [tokens, kv_heads, head_dim] device,
+ *           contiguous, 16-byte aligned, written.
+ *   slots   int64 [tokens] device; a slot outside the cache reads as zeros.
+ */
+int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                void* stream);
+
+/* One call of fp4_attn (device pointers; the struct is read during the call). */
+typedef struct {
+    const uint16_t* q;         /* bf16 [total_q, q_heads, head_dim], token pitch ld_q elements
+                                  (>= q_heads * head_dim, % 8 == 0), 16-byte aligned            */
+    int64_t ld_q;
+    const int32_t* page_table; /* [batch, table_cols]: a sequence's pages in order              */
+    const int32_t* kv_lens;    /* [batch]: keys of each sequence (its queries' own included)     */
+    const int32_t* q_starts;   /* [batch + 1]: sequence b's queries are rows q_starts[b] ..
+                                  q_starts[b + 1] - 1 of q.  NULL: one query each, sequence b's
+                                  being row b (total_q == batch)                                */
+    const float* sinks;        /* FP32 [q_heads] or NULL: a logit that joins each row's softmax
+                                  without a value                                              */
+    void* out;                 /* bf16 or FP32 (cfg->output_dtype) [total_q, q_heads, head_dim],
+                                  contiguous, 16-byte aligned, written                         */
+    float* lse;                /* FP32 [total_q, q_heads] or NULL: log of each row's sum of
+                                  exponentials (sink included), written                       */
+    float scale;               /* of q . k, > 0                                                 */
+    int32_t batch, total_q, q_heads, table_cols;
+    int32_t max_q, max_kv;     /* bounds of the sequences' query and key counts: they size the
+                                  launch, and counts beyond them are cut                       */
+    int32_t causal;            /* 1: the last query stands on the last key, each sees the keys
+                                  up to its own; 0: every query sees every key                 */
+    int32_t window;            /* causal only: > 0 keeps the last `window` of those keys         */
+} fp4q_attn;
+
+/*
+ * fp4_attn -- attention of queries over the cache: single tokens, a few tokens,
+ * chunks of prompts, mixed in one call.
+ *   out[i, h] = sum_j softmax_j(scale q[i, h] . k_j) v_j,  head h reading KV head
+ *   h / (q_heads / kv_heads), over the keys that query i sees.
+ * A row that sees no key gives zeros and lse = -infinity (or the sink).  Key counts
+ * are cut to table_cols * page_size; a page number outside the cache makes its keys
+ * absent (page table entries beyond a sequence's keys are not read).  Rows of q that
+ * belong to no sequence are not written.  What unseen keys hold never reaches
+ * a result; an MXFP4 block poisoned by NaN makes the rows that see its key NaN,
+ * as in the products.
+ * K and V enter the products exactly; the weights of V are rounded to bf16 (MXFP4)
+ * or FP16 (NVFP4, AMD-FP4: weights below 2^-14 of a row's largest are then multiples of
+ * 2^-24 of it) before they are multiplied and summed; everything else is binary32.
+ * workspace: fp4q_attn_workspace_bytes() bytes (0 for calls whose keys are not
+ * split), 16-byte aligned.  It needs no initial value and holds nothing between
+ * calls.  The result depends on the split, which depends on batch, max_q, max_kv,
+ * window and the heads alone, so equal calls give equal bits.
+ * Limits (FP4Q_ERR_UNSUPPORTED): max_kv <= 2^27, batch <= 65535, max_q * q_heads /
+ * kv_heads <= 2^22, total_q * q_heads < 2^31.
+ */
+size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn);
+int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
+             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
