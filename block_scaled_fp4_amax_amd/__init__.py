@@ -2,8 +2,8 @@
 block-scaled FP4 quantisation library.
 
 The functions carry the C-ABI names (fp4_quantize, fp4_dequantize, fp4_qdq,
-fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_kv_append,
-fp4_kv_read, fp4_attn and the fp4q_* helpers).  They
+fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_linear,
+fp4_kv_append, fp4_kv_read, fp4_attn and the fp4q_* helpers).  They
 only marshal arguments: torch supplies device memory and the current HIP
 stream, every step of the computation runs in the library's HIP kernels.  If
 the library is not built, importing the binding raises; there is no fallback.
@@ -17,7 +17,7 @@ __all__ = [
     "Fp4Error", "Cfg", "Sizes", "make_cfg", "lib", "fp4q_abi_version", "fp4q_status_str", "fp4q_buffer_sizes",
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
-    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "KVCache", "fp4_kv_append",
+    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "KVCache", "fp4_kv_append",
     "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "LIB_PATH",
 ]
 
@@ -144,6 +144,8 @@ def lib():
         L.fp4q_attn_workspace_bytes.argtypes = [C, KV, AT]
         L.fp4_attn.restype = ct.c_int
         L.fp4_attn.argtypes = [C, KV, AT, P, SZ, P]
+        L.fp4_linear.restype = ct.c_int
+        L.fp4_linear.argtypes = [C, P, I64, I64, P, P, P, ct.c_int32, I64, I64, P, I64, P]
         if L.fp4q_abi_version() != ABI_VERSION:
             raise ImportError("libfp4q.so ABI %d, binding expects %d" % (L.fp4q_abi_version(), ABI_VERSION))
         _lib = L
@@ -532,6 +534,46 @@ def fp4_mm(a, b, cfg=None, *, out_dtype=None, c=None, stream=None):
     _check(lib().fp4_mm(ct.byref(ccfg), _ptr(ac), _ptr(asc), _ptr(bc), _ptr(bsc), M, N, K, la, _ptr(c),
                         c.stride(0) if M > 1 else N, _stream(stream)), "fp4_mm")
     return c
+
+
+def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, stream=None):
+    """y = x @ W^T with bf16 x [M, K] (a view with a row pitch is accepted) and a
+    4-bit W [N, K] given as {"codes", "scales", "outer"} in cfg's format, as fp4_quantize
+    returns it (or the row_* buffers of fp4_cast_transpose under those names).
+
+    The gradient of x is the same product over the columnwise buffers: with
+    w = {"codes": col_codes [K, N / 2], "scales": col_scales, "outer": ...} and dy [M, N] in
+    x's place it returns dy @ W [M, K]; a 2D outer array is passed as it is, with
+    outer_transposed=True.  y is bf16 unless out_dtype (or a given y) is float32."""
+    torch = _torch()
+    codes, scales, outer = w["codes"], w["scales"], w.get("outer")
+    if x.dtype != torch.bfloat16:
+        raise Fp4Error(ERR_DTYPE, "x dtype %s" % x.dtype)
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError("x and the weight's codes must be 2-D")
+    (M, K), N = x.shape, codes.shape[0]
+    if codes.shape[1] * 2 != K:
+        raise ValueError("x and the weight disagree on K (%d vs %d)" % (K, codes.shape[1] * 2))
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError("x rows must be contiguous (stride(1) == 1)")
+    _need(codes, N * K // 2, "codes")
+    _need(scales, N * (K // _inner(cfg)), "scales")
+    if cfg.two_level == TWO_LEVEL["tensorwise"]:
+        _need(outer, 4, "outer")
+    elif cfg.two_level == TWO_LEVEL["outer_block"] and cfg.outer_block_size > 0:
+        _need(outer, 4 * (N // (cfg.outer_block_size if cfg.outer_2d else 1)) * (K // cfg.outer_block_size), "outer")
+    if outer is not None and outer.dtype != torch.float32:
+        raise ValueError("outer must be float32")
+    if y is None:
+        y = _held_on(torch.empty((M, N), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=x.device),
+                     stream)
+    if tuple(y.shape) != (M, N) or (N > 1 and y.stride(1) != 1) or y.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("y must be a bf16 or float32 [%d, %d] view with contiguous rows" % (M, N))
+    ycfg = _with_dtypes(cfg, "bf16", _dtype_name(y))
+    _check(lib().fp4_linear(ct.byref(ycfg), _ptr(x), M, x.stride(0) if M > 1 else K, _ptr(codes), _ptr(scales),
+                            _ptr(outer), int(bool(outer_transposed)), N, K, _ptr(y), y.stride(0) if M > 1 else N,
+                            _stream(stream)), "fp4_linear")
+    return y
 
 
 # ------------------------------------------------------------------ the paged 4-bit cache

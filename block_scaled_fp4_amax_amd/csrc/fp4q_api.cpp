@@ -900,4 +900,52 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     return hip_status(launch_attn(r.bias, a, (hipStream_t)stream));
 }
 
+int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, const uint8_t* codes,
+               const uint8_t* scales, const float* outer, int32_t outer_transposed, int64_t N, int64_t K, void* y,
+               int64_t ld_y, void* stream)
+{
+    Resolved r;
+    int st = resolve(cfg, r);
+    if (st) return st;
+    if (r.x_f32) return FP4Q_ERR_UNSUPPORTED;
+    if (outer_transposed != 0 && outer_transposed != 1) return FP4Q_ERR_MODE;
+    if (outer_transposed && r.outer_kind != kOuter2D && r.outer_kind != kOuterNone && r.outer_kind != kOuterTensor)
+        return FP4Q_ERR_MODE;
+    if (M < 0 || N < 0 || K < 0 || K % 32) return FP4Q_ERR_SHAPE;
+    if (M > 1 && ld_x < K) return FP4Q_ERR_SHAPE;
+    if (M > 1 && ld_y < N) return FP4Q_ERR_SHAPE;
+    if (r.obs && (K % r.obs || (r.outer_kind == kOuter2D && N % r.obs))) return FP4Q_ERR_SHAPE;
+    if ((r.outer_kind == kOuter2D && r.obs != 64) || (r.outer_kind == kOuter1D && r.obs % 64)) return FP4Q_ERR_UNSUPPORTED;
+    if (K > ((int64_t)1 << 22) || M > ((int64_t)1 << 20) || N > ((int64_t)1 << 24)) return FP4Q_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return FP4Q_OK;
+    if (!y || (K > 0 && (!x || !codes || !scales))) return FP4Q_ERR_NULL;
+    if (K > 0 && r.outer_kind != kOuterNone && !outer) return FP4Q_ERR_NULL;
+    if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(outer, 4) || misaligned(y, r.y_f32 ? 4 : 2) ||
+        (M > 1 && K > 0 && ld_x % 8))
+        return FP4Q_ERR_ALIGN;
+    LinearArgs a;
+    a.x = x;
+    a.ld_x = ld_x;
+    a.codes = codes;
+    a.scales = scales;
+    a.outer_kind = K > 0 ? r.outer_kind : kOuterNone;
+    a.outer = r.outer_kind == kOuterNone ? nullptr : outer;
+    a.obs = r.obs;
+    a.outer_n = a.outer_k = 0;
+    if (r.outer_kind == kOuter1D) {
+        a.outer_n = K / r.obs;
+        a.outer_k = 1;
+    } else if (r.outer_kind == kOuter2D) {
+        a.outer_n = outer_transposed ? 1 : K / 64;
+        a.outer_k = outer_transposed ? N / 64 : 1;
+    }
+    a.M = (int32_t)M;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.y_f32 = r.y_f32 ? 1 : 0;
+    a.y = y;
+    a.ld_y = ld_y;
+    return hip_status(launch_linear(r.bias, a, (hipStream_t)stream));
+}
+
 }  // extern "C"

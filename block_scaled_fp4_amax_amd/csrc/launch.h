@@ -265,6 +265,22 @@ int attn_block_rows(int64_t rows);
 int attn_splits(int64_t batch, int32_t kv_heads, int64_t rows, int64_t max_kv);
 hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s);
 
+// y = x W^T with bf16 x [M, ld_x] and a 4-bit W [N, K] (rowwise codes and scale bytes).
+struct LinearArgs {
+    const uint16_t* x;
+    int64_t ld_x;
+    const uint8_t *codes, *scales;
+    const float* outer;        // null, [1], or one per row (or 64 rows) and `obs` values of K
+    int64_t outer_n, outer_k;  // index strides of `outer` per 64 rows (2D) or row (1D), per obs values of K
+    int32_t outer_kind, obs;
+    int32_t M, N, K;
+    int32_t y_f32;
+    void* y;                   // bf16 or FP32 [M, ld_y]
+    int64_t ld_y;
+};
+
+hipError_t launch_linear(int bias, const LinearArgs& a, hipStream_t s);
+
 // partial maxima used by the tensorwise amax pass
 constexpr int kAmaxPartials = 512;
 

@@ -87,4 +87,32 @@ struct Dec {
     }
 };
 
+// Decoding to bf16 for every format, for products whose other operand needs
+// binary32's exponents (activations and gradients of any size): G[m] d has at
+// most six significant bits, so the upper halves of the binary32 products are the
+// bf16 values.
+template <int BIAS>
+struct DecBf16 {
+    // 2^k (MXFP4) or d in binary32: a byte's fields shifted to binary32's read as
+    // d 2^(BIAS - 127), subnormals included
+    static __device__ __forceinline__ float scale(uint32_t byte)
+    {
+        if constexpr (BIAS == 0) return __uint_as_float(byte << 23);
+        return __uint_as_float(byte << 20) * (BIAS == 7 ? 0x1p120f : 0x1p112f);
+    }
+
+    template <int B>
+    static __device__ __forceinline__ uint32_t pair(uint32_t w, float s)
+    {
+        if constexpr (BIAS == 0) return Dec<0>::pair<B>(w, __float_as_uint(s));
+        const auto g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, B);
+        return __builtin_amdgcn_perm(__float_as_uint(g[1] * s), __float_as_uint(g[0] * s), 0x07060302u);
+    }
+
+    static __device__ __forceinline__ uint4 octet(uint32_t w, float s)
+    {
+        return make_uint4(pair<0>(w, s), pair<1>(w, s), pair<2>(w, s), pair<3>(w, s));
+    }
+};
+
 }  // namespace fp4q

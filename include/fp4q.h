@@ -408,6 +408,30 @@ size_t fp4q_mx_scales_tiled_bytes(int64_t rows, int64_t K);
 int fp4_mx_scales_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* out, void* stream);
 
 /*
+ * fp4_linear -- y = x W^T with bf16 activations x [M, K] and a 4-bit weight W [N, K]
+ * in any format, for one token up to a training step's rows.
+ *   x        bf16 [M, ld_x] device (ld_x >= K, % 8 == 0; ignored for one row), 16-byte
+ *            aligned.  cfg->input_dtype FP32: FP4Q_ERR_UNSUPPORTED.
+ *   codes, scales, outer  W's rowwise buffers as fp4_quantize or
+ *            fp4_cast_transpose write them.  The columnwise buffers are the
+ *            rowwise ones of W^T [K, N], so with them (and M, K and N in their
+ *            place) the same call is dx = dy W; a 2D outer array then belongs to the
+ *            transpose and outer_transposed is 1 (as in fp4_dequantize).
+ *   y        bf16 or FP32 (cfg->output_dtype) [M, ld_y] device (ld_y >= N), written.
+ * W enters the products exactly as codes times inner scales, in bf16; sums are
+ * binary32, and an outer scale multiplies the binary32 sum of the values that it
+ * covers: |y - exact| <= (K + K / 64 + 2) 2^-24 sum_k |x_k w_k| (plus y's rounding).
+ * The order of a sum depends on M, N and K alone, so equal calls give equal bits.
+ * Needs K % 32 == 0 (FP4Q_ERR_SHAPE); 1D outer blocks of a multiple of 64 and
+ * 2D ones of 64 (others: FP4Q_ERR_UNSUPPORTED); K <= 2^22, M <= 2^20 and N <= 2^24.
+ * K == 0 writes zeros.  rounding, outer_mode, seed, step and index_base are ignored, and so
+ * is inner_2d (see fp4_dequantize).
+ */
+int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, const uint8_t* codes,
+               const uint8_t* scales, const float* outer, int32_t outer_transposed, int64_t N, int64_t K, void* y,
+               int64_t ld_y, void* stream);
+
+/*
  * The paged 4-bit cache of keys and values, for decoding with attention.
  *
  * A cache is num_pages pages of page_size tokens (a multiple of 16, at most

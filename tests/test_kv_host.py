@@ -142,3 +142,46 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
     with pytest.raises(ValueError, match="tensorwise"):
         fq.KVCache(z(4, 2, 16, 32), z(4, 2, 16, 4), z(4, 2, 16, 32), z(4, 2, 16, 4), cfg, k_outer=torch.ones(2),
                    v_outer=torch.ones(2))
+
+
+def linear(cfg=None, x=FAKE, M=3, ld_x=128, codes=FAKE, scales=FAKE, outer=None, t=0, N=64, K=128, y=FAKE, ld_y=64):
+    cfg = cfg if cfg is not None else fq.make_cfg()
+    return status(fq.lib().fp4_linear(ct.byref(cfg), x, M, ld_x, codes, scales, outer, t, N, K, y, ld_y, None))
+
+
+@no_gpu
+def test_linear_rules():
+    C = fq.make_cfg
+    for kw in (dict(M=-1), dict(N=-1), dict(K=-32), dict(K=48), dict(ld_x=120), dict(ld_y=63)):
+        assert linear(**kw) == fq.ERR_SHAPE, kw
+    one_d, two_d = (C(two_level="outer_block", outer_block_size=n, outer_2d=b) for n, b in ((64, False), (64, True)))
+    assert linear(cfg=one_d, K=96, ld_x=96, outer=FAKE) == fq.ERR_SHAPE
+    assert linear(cfg=two_d, N=32, outer=FAKE) == fq.ERR_SHAPE
+    assert linear(cfg=one_d) == fq.ERR_NULL and linear(cfg=two_d) == fq.ERR_NULL
+    assert linear(cfg=C(two_level="tensorwise")) == fq.ERR_NULL
+    for n, b in ((16, False), (32, False), (128, True)):
+        assert linear(cfg=C(two_level="outer_block", outer_block_size=n, outer_2d=b), N=128, ld_y=128,
+                      outer=FAKE) == fq.ERR_UNSUPPORTED
+    assert linear(cfg=one_d, outer=FAKE, t=1) == fq.ERR_MODE and linear(t=2) == fq.ERR_MODE
+    assert linear(cfg=C(input_dtype="fp32")) == fq.ERR_UNSUPPORTED
+    assert linear(cfg=C(input_dtype="fp16")) == fq.ERR_DTYPE
+    for kw in (dict(M=(1 << 20) + 1), dict(N=(1 << 24) + 1, ld_y=1 << 25), dict(K=(1 << 22) + 32, ld_x=1 << 23)):
+        assert linear(**kw) == fq.ERR_UNSUPPORTED, kw
+    for n in ("x", "codes", "scales", "y"):
+        assert linear(**{n: None}) == fq.ERR_NULL
+    for n in ("x", "codes"):
+        assert linear(**{n: MIS}) == fq.ERR_ALIGN
+    assert linear(y=FAKE + 1) == fq.ERR_ALIGN and linear(ld_x=132) == fq.ERR_ALIGN
+    assert linear(cfg=C(two_level="tensorwise"), outer=FAKE + 2) == fq.ERR_ALIGN
+    assert linear(M=0, x=None, y=None) == fq.OK and linear(N=0, codes=None, y=None) == fq.OK
+
+
+def test_linear_binding_rules():
+    u8 = torch.zeros(4, 16, dtype=torch.uint8)
+    w = {"codes": u8, "scales": u8, "outer": None}
+    with pytest.raises(fq.Fp4Error):
+        fq.fp4_linear(torch.zeros(2, 32), w, fq.make_cfg())
+    with pytest.raises(ValueError, match="disagree on K"):
+        fq.fp4_linear(torch.zeros(2, 64, dtype=torch.bfloat16), w, fq.make_cfg())
+    with pytest.raises(ValueError, match="device tensors"):
+        fq.fp4_linear(torch.zeros(2, 32, dtype=torch.bfloat16), w, fq.make_cfg())
