@@ -771,30 +771,9 @@ int check_attn(const KvView& kv, const fp4q_attn* a)
     return FP4Q_OK;
 }
 
-// How a call's keys are split over workgroups, and the scratch that takes.
-struct AttnPlan {
-    int32_t splits, chunk;
-    size_t ml, o;
-};
-
-AttnPlan plan_attn(const KvView& kv, const fp4q_attn* a)
+AttnPlan plan_of(const KvView& kv, const fp4q_attn* a)
 {
-    const int64_t rows = (int64_t)a->max_q * (a->q_heads / kv.heads);
-    // keys that one tile of rows can see
-    int64_t keys = std::min<int64_t>(a->max_kv, (int64_t)a->table_cols * kv.page_size);
-    if (a->window) keys = std::min<int64_t>(keys, (int64_t)a->window + a->max_q + 32);
-    AttnPlan p{1, 128, 0, 0};
-    if (rows == 0 || a->batch == 0) return p;
-    p.splits = attn_splits(a->batch, kv.heads, rows, keys);
-    p.splits = (int32_t)std::min<int64_t>(p.splits, std::max<int64_t>(1, 65535 / a->batch));
-    p.chunk = (int32_t)((keys + p.splits * 128 - 1) / (p.splits * 128) * 128);
-    if (p.chunk < 128) p.chunk = 128;
-    if (p.splits > 1) {
-        const size_t n = (size_t)p.splits * a->total_q * a->q_heads;
-        p.ml = n * 2 * sizeof(float);
-        p.o = n * kv.dim * sizeof(float);
-    }
-    return p;
+    return plan_attn(kv, a->batch, a->total_q, a->q_heads, a->max_q, a->max_kv, a->table_cols, a->window);
 }
 
 }  // namespace
@@ -850,7 +829,7 @@ size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache
     Resolved r;
     KvView kv;
     if (resolve_cache(cfg, cache, r, kv) || check_attn(kv, attn)) return 0;
-    const AttnPlan p = plan_attn(kv, attn);
+    const AttnPlan p = plan_of(kv, attn);
     return p.ml + p.o;
 }
 
@@ -870,9 +849,9 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
         misaligned(attn->kv_lens, 4) || misaligned(attn->q_starts, 4) || misaligned(attn->sinks, 4) ||
         misaligned(attn->lse, 4) || (attn->total_q > 1 && attn->ld_q % 8))
         return FP4Q_ERR_ALIGN;
-    const AttnPlan p = plan_attn(a.kv, attn);
-    if (p.splits > 1 && (!workspace || workspace_bytes < p.ml + p.o)) return FP4Q_ERR_WORKSPACE;
-    if (p.splits > 1 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
+    const AttnPlan p = plan_of(a.kv, attn);
+    if (p.o > 0 && (!workspace || workspace_bytes < p.ml + p.o)) return FP4Q_ERR_WORKSPACE;
+    if (p.o > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
     a.q = attn->q;
     a.ld_q = attn->ld_q;
     a.table = attn->page_table;
@@ -893,6 +872,8 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     a.max_kv = attn->max_kv;
     a.causal = attn->causal;
     a.window = attn->window;
+    a.slots = p.slots;
+    a.groups = p.groups;
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.out_f32 = r.y_f32 ? 1 : 0;

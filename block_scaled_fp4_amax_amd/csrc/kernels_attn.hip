@@ -43,10 +43,58 @@ namespace fp4q {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kUnit = 128;                               // keys that a workgroup of few rows takes at once
+constexpr int kMinShare = 4;                             // units of a workgroup's share, at least
+constexpr int kFewRows = 32;
+constexpr int kTileRows = 32 * kWaves;                   // rows of a workgroup of k_attn
+constexpr int kMaxSplits = 64;
 constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
 constexpr float kLazy = 8.0f;
+
+// Loads of 16 bytes a lane straight to LDS at a wave-uniform base (lane l's go to base
+// + 16 l), from per-lane addresses or through a descriptor.  They are written out, with the
+// waits below, because the compiler's own waits cannot tell stages apart and would
+// wait for every outstanding load before any read of LDS.  No other instruction
+// here reads m0, so the reserved-register clobber warning is silenced.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_load(const void* p, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(p), "s"(base) : "memory", "m0");
+}
+
+__device__ __forceinline__ void lds_load(rsrc_t r, uint32_t off, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen nt lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Waits until at most N vector-memory operations of the wave are outstanding; no read of
+// LDS moves above it.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    static_assert(N >= 0 && N < 64, "the counter holds 63");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
+}
+
+typedef __attribute__((address_space(3))) unsigned char lds_t;
+
+__device__ __forceinline__ uint32_t lds_address(const lds_t* p)
+{
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
+}
+
+// A group's rows through a buffer descriptor in scalar registers: a lane's offsets are the
+// same for every group, so a load takes no address arithmetic on lanes.
+__device__ __forceinline__ rsrc_t rows_at(const uint8_t* base, int64_t row, int bytes)
+{
+    const uint64_t p = (uint64_t)base + (uint64_t)row * bytes;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+    return make_rsrc((const void*)((uint64_t)hi << 32 | lo));
+}
 
 // The largest of a value over the four lanes of a column (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ float column_max(float v)
@@ -57,62 +105,138 @@ __device__ __forceinline__ float column_max(float v)
     return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
-// The codes and scale bytes of one step, as loaded.
+// The codes and scale bytes of one step in a lane's registers.
 template <int D, int BIAS>
 struct Raw {
     static constexpr int kKW = D / 32;                   // dwords of a quarter row of K
     static constexpr int kVW = D / 16 < 8 ? 1 : D / 128; // dwords of D / 16 codes of V
-    uint32_t k[2][kKW], ks[2], v[8][kVW], vs[8];
+    static constexpr int kSB = D / Dec<BIAS>::kBlock;    // scale bytes of a row
+    // V's scale bytes of a lane's four neighbouring keys: whole rows together where
+    // they fill up to 16 bytes, byte by byte where rows are longer
+    static constexpr int kSW = kSB <= 4 ? kSB : 4;
+    uint32_t k[2][kKW], ks[2], v[8][kVW], vs[2][kSW];
+
+    // V's scale byte of key 4 s + t of the lane; bit: 8 times its block
+    __device__ __forceinline__ uint32_t v_scale(int s, int t, uint32_t bit) const
+    {
+        if constexpr (kSB == 2) return __builtin_amdgcn_ubfe(vs[s][t >> 1], 16 * (t & 1) + bit, 8);
+        else if constexpr (kSB == 4) return __builtin_amdgcn_ubfe(vs[s][t], bit, 8);
+        else return vs[s][t];
+    }
 };
 
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w)
-{
-    if constexpr (N == 1) {
-        w[0] = *(const uint32_t*)p;
-    } else if constexpr (N == 2) {
-        const uint2 u = *(const uint2*)p;
-        w[0] = u.x, w[1] = u.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 u = ((const uint4*)p)[i];
-            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-        }
-    }
-}
-
-template <int N>
-__device__ __forceinline__ uint32_t load_bytes(const uint8_t* p)
-{
-    if constexpr (N == 1) return *p;
-    else if constexpr (N == 2) return *(const uint16_t*)p;
-    else return *(const uint32_t*)p;
-}
-
+// A wave's steps on their way: kDepth stages of LDS, filled by loads that write LDS
+// directly (16 bytes a lane to consecutive places), kDepth - 1 steps ahead of
+// their use.  A stage costs 3, 5 or 9 load instructions and no registers, where
+// loading a lane's own words took 24 instructions and kept one step in flight
+// (4 x 131072 keys, NVFP4, head_dim 128: 102 us; 88 us with work cut evenly).
+//   K codes   [32 keys][D / 2], D = 256 with a row's eight 16-byte chunks at
+//             chunk ^ (key % 8), so that the lanes of a read spread over the banks;
+//   V codes   [2][16 keys][D / 2], key 4 q + t of a group of 16 at place 4 t + q,
+//             so that one read of the wave is contiguous;
+//   K scales, V scales  [32 keys][D / block].
 template <int D, int BIAS>
-__device__ __forceinline__ void load_step(const KvView& kv, const KvGroup (&g)[2], int lane, Raw<D, BIAS>& r)
-{
-    constexpr int B = Dec<BIAS>::kBlock;
-    constexpr int KB = D / 4 / B > 0 ? D / 4 / B : 1;    // scale bytes of a quarter row of K
-    const int m = lane & 15, q = lane >> 4;
+struct Ring {
+    static constexpr int B = Dec<BIAS>::kBlock;
+    static constexpr int kDepth = D == 256 ? 2 : 4;
+    static constexpr int kCodes = 32 * D / 2, kScales = 32 * D / B;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kWave = kDepth * kStage;
+    static constexpr int kLoads = D == 64 ? 3 : D == 128 ? 5 : 9;
+
+    lds_t* mem;                                          // the wave's stages
+    const uint8_t *k_codes, *v_codes;
+    uint64_t scales;                                     // the lane's place in the scales of row 0
+    int lane;
+
+    __device__ __forceinline__ Ring(unsigned char* lds, const KvView& kv, int lane)
+        : mem((lds_t*)lds), k_codes(kv.k_codes), v_codes(kv.v_codes), lane(lane)
+    {
+        const uint64_t ks = (uint64_t)kv.k_scales, vs = (uint64_t)kv.v_scales;
+        scales = ks + (lane / (D / B) & 2 ? vs - ks : 0) + (lane % (D / B)) * 16;
+    }
+
+    __device__ __forceinline__ void issue(int slot, const KvGroup (&g)[2])
+    {
+        const uint32_t to = lds_address(mem + slot * kStage);
+        if constexpr (D == 64) {
+            // a group of 16 keys is 512 bytes: lanes 0 .. 31 and 32 .. 63 take one each
+            const int64_t row = g[0].row + (lane < 32 ? 0 : g[1].row - g[0].row);
+            const uint32_t c = lane & 31, place = c >> 1;
+            lds_load(k_codes + row * 32 + c * 16, to);
+            lds_load(v_codes + row * 32 + (4 * (place & 3) + (place >> 2)) * 32 + (c & 1) * 16, to + kCodes);
+        } else {
+            constexpr int kPer = D / 32;                 // 16-byte chunks of a row
+            constexpr int kHalves = D / 128;             // loads of a group
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const uint8_t* kc = kv.k_codes + g[s].row * (D / 2);
-        const uint8_t* ks = kv.k_scales + g[s].row * (D / B);
-        const uint8_t* vc = kv.v_codes + g[s].row * (D / 2);
-        const uint8_t* vs = kv.v_scales + g[s].row * (D / B);
-        load_words<Raw<D, BIAS>::kKW>(kc + m * (D / 2) + q * (D / 8), r.k[s]);
-        r.ks[s] = load_bytes<KB>(ks + m * (D / B) + q * (D / 4) / B);
+            for (int s = 0; s < 2; ++s) {
+                const rsrc_t kc = rows_at(k_codes, g[s].row, D / 2), vc = rows_at(v_codes, g[s].row, D / 2);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const uint8_t* p = vc + (4 * q + t) * (D / 2) + m * (D / 32);
-            if constexpr (D == 64) r.v[4 * s + t][0] = *(const uint16_t*)p;
-            else load_words<Raw<D, BIAS>::kVW>(p, r.v[4 * s + t]);
-            r.vs[4 * s + t] = vs[(4 * q + t) * (D / B) + m * (D / 16) / B];
+                for (int h = 0; h < kHalves; ++h) {
+                    const uint32_t place = h * (64 / kPer) + lane / kPer, c = lane % kPer;
+                    const uint32_t at = to + (s * kHalves + h) * 1024;
+                    lds_load(kc, place * (D / 2) + (D == 256 ? c ^ (place & 7) : c) * 16, at);
+                    lds_load(vc, (4 * (place & 3) + (place >> 2)) * (D / 2) + c * 16, at + kCodes);
+                }
+            }
+        }
+        // scales: D / B chunks of 16 bytes for each of K's and V's two groups
+        if (lane < 4 * (D / B)) {
+            const int64_t row = g[0].row + (lane / (D / B) & 1 ? g[1].row - g[0].row : 0);
+            lds_load((const void*)(scales + (uint64_t)row * (D / B)), to + 2 * kCodes);
         }
     }
-}
+
+    __device__ __forceinline__ void read(int slot, Raw<D, BIAS>& r) const
+    {
+        constexpr int KB = D / 4 / B > 0 ? D / 4 / B : 1;    // scale bytes of a quarter row of K
+        const uint32_t m = lane & 15, q = (uint32_t)lane >> 4;
+        const lds_t* k = mem + slot * kStage;
+        const lds_t *v = k + kCodes, *ks = v + kCodes, *vs = ks + kScales;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const lds_t* kr = k + (16 * s + m) * (D / 2);
+            if constexpr (D == 256) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) words<4>(kr + ((2 * q + j) ^ (m & 7)) * 16, r.k[s] + 4 * j);
+            } else {
+                words<D / 32>(kr + q * (D / 8), r.k[s]);
+            }
+            r.ks[s] = bytes<KB>(ks + (16 * s + m) * (D / B) + q * (D / 4) / B);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const lds_t* p = v + (16 * s + 4 * t + q) * (D / 2) + m * (D / 32);
+                if constexpr (D == 64) r.v[4 * s + t][0] = bytes<2>(p);
+                else words<D / 128>(p, r.v[4 * s + t]);
+                if constexpr (D / B > 4) r.vs[s][t] = bytes<1>(vs + (16 * s + 4 * q + t) * (D / B) + m * (D / 16) / B);
+            }
+            if constexpr (D / B <= 4) words<D / B>(vs + (16 * s + 4 * q) * (D / B), r.vs[s]);
+        }
+    }
+
+private:
+    template <int N>
+    static __device__ __forceinline__ void words(const lds_t* p, uint32_t* w)
+    {
+        if constexpr (N == 1) {
+            w[0] = *(const __attribute__((address_space(3))) uint32_t*)p;
+        } else if constexpr (N == 2) {
+            const u32x2_t u = *(const __attribute__((address_space(3))) u32x2_t*)p;
+            w[0] = u[0], w[1] = u[1];
+        } else {
+            const u32x4_t u = *(const __attribute__((address_space(3))) u32x4_t*)p;
+            w[0] = u[0], w[1] = u[1], w[2] = u[2], w[3] = u[3];
+        }
+    }
+
+    template <int N>
+    static __device__ __forceinline__ uint32_t bytes(const lds_t* p)
+    {
+        if constexpr (N == 1) return *p;
+        else if constexpr (N == 2) return *(const __attribute__((address_space(3))) uint16_t*)p;
+        else return *(const __attribute__((address_space(3))) uint32_t*)p;
+    }
+};
 
 // Rounds a row's head_dim / 4 values of q held by a lane to FP16 after scaling the row to
 // [2^14, 2^15) by a power of two; returns what scores are multiplied by to undo it.
@@ -188,23 +312,40 @@ __device__ __forceinline__ float finish_row(float m, float l, const float* sinks
     return f / l;
 }
 
+// A joined row: lane l holds values (D / 64) l + 0 .. D / 64 - 1.
+template <int D>
+__device__ __forceinline__ void write_joined(const AttnArgs& a, int64_t row, int qh, float m, float l,
+                                             const float (&acc)[D / 64], float unshift, int lane)
+{
+    constexpr int N = D / 64;
+    float lse;
+    const float f = finish_row(m, l, a.sinks, qh, lse) * unshift * (a.kv.v_outer ? a.kv.v_outer[qh / a.group] : 1.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float y = l == 0.0f ? 0.0f : acc[i] * f;
+        if (a.out_f32) ((float*)a.out)[row * D + lane * N + i] = y;
+        else ((uint16_t*)a.out)[row * D + lane * N + i] = (uint16_t)f32_to_bf16(y);
+    }
+    if (a.lse && lane == 0) a.lse[row] = lse;
+}
+
 // MXFP4 keys some rows see and others do not, with a poisoned block of V: 0 times
 // its NaN would reach the rows that do not see the key.  Such blocks are cleared,
 // and the product of (block is poisoned) with (row sees the key) says which
 // outputs become NaN.  All of a lane's values of V lie in one block.
-template <int ND, int QT, class R>
-__device__ __forceinline__ void poison_seen(R& raw, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][ND], uint4 ones)
+template <int ND, int QT>
+__device__ __forceinline__ void poison_seen(uint32_t (&vs)[8], const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][ND], uint4 ones)
 {
     bool any = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) any |= raw.vs[j] == 0xFFu;
+    for (int j = 0; j < 8; ++j) any |= vs[j] == 0xFFu;
     if (!__any(any)) return;
     uint32_t bad[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        bad[j] = (raw.vs[2 * j] == 0xFFu ? ones.x & 0xFFFFu : 0u) | (raw.vs[2 * j + 1] == 0xFFu ? ones.x & 0xFFFF0000u : 0u);
+        bad[j] = (vs[2 * j] == 0xFFu ? ones.x & 0xFFFFu : 0u) | (vs[2 * j + 1] == 0xFFu ? ones.x & 0xFFFF0000u : 0u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) raw.vs[j] = raw.vs[j] == 0xFFu ? 0u : raw.vs[j];
+    for (int j = 0; j < 8; ++j) vs[j] = vs[j] == 0xFFu ? 0u : vs[j];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         uint32_t seen[4];
@@ -222,249 +363,530 @@ __device__ __forceinline__ void poison_seen(R& raw, const f32x4_t (&sc)[QT][2], 
     }
 }
 
+// The rows of a wave: their queries, what scores are multiplied by, the keys that each
+// sees (first / last: the tile's first and last rows'), and where results go.
 template <int D, int BIAS, int QT>
-__global__ __launch_bounds__(64 * kWaves, D == 256 && QT == 2 ? 1 : 2) void k_attn(AttnArgs a)
+struct Rows {
+    uint4 q[QT][D / 32];
+    float c[QT];
+    KeyRange see[QT], first, last;
+    int64_t out[QT];                                     // token * q_heads + head, -1: no row
+
+    __device__ __forceinline__ void load(const AttnArgs& a, const QueryRange& qr, int kv, int head, int row0, int lane)
+    {
+        using X = Dec<BIAS>;
+        const int col = lane & 15, quarter = lane >> 4;
+        const int rows = qr.count * a.group;
+        first = key_range(min(row0, rows - 1) / a.group, qr.count, kv, a.causal, a.window);
+        last = key_range((min(row0 + 16 * QT, rows) - 1) / a.group, qr.count, kv, a.causal, a.window);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            const int r = row0 + 16 * t + col;
+            const bool live = r < rows;
+            const int i = live ? r / a.group : 0, g = live ? r - i * a.group : 0;
+            see[t] = key_range(i, qr.count, kv, a.causal, a.window);
+            out[t] = live ? (int64_t)(qr.first + i) * a.q_heads + head * a.group + g : -1;
+            const uint16_t* p =
+                a.q + (int64_t)(qr.first + i) * a.ld_q + (int64_t)(head * a.group + g) * D + quarter * (D / 4);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) q[t][k] = live ? ((const uint4*)p)[k] : make_uint4(0, 0, 0, 0);
+            c[t] = a.scale * kLog2e * X::kUnshift;
+            if constexpr (!X::kBf16) {
+                c[t] *= q_to_f16<D / 32>(q[t]);
+                if (a.kv.k_outer) c[t] *= a.kv.k_outer[head];
+            }
+            c[t] = fmaxf(c[t], 1.17549435e-38f);         // 0 would turn a masked score into NaN
+        }
+    }
+};
+
+// What a wave has summed.
+template <int D, int QT>
+struct Sums {
+    f32x4_t o[QT][D / 16], l[QT];
+    float m[QT];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            m[t] = kNoMax;
+            l[t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) o[t][n] = f32x4_t{0, 0, 0, 0};
+        }
+    }
+
+    // o[n][r] is the value d = (D / 4) quarter + (D / 16) r + n of the lane's row
+};
+
+// One step: 32 keys from `at`, their bytes in `raw`; bits 0 and 1 of `groups` say which of its
+// two groups are.
+template <int D, int BIAS, int QT>
+__device__ __forceinline__ void attend_step(const Raw<D, BIAS>& raw, uint32_t groups, int at, int end, const Rows<D, BIAS, QT>& rows, int lane,
+                                            Sums<D, QT>& sum)
 {
     using X = Dec<BIAS>;
     constexpr int NK = D / 32;                           // products of a step's scores
     constexpr int ND = D / 16;                           // products of a step's outputs (values of V in a lane)
-    constexpr int kRows = 16 * QT;
-    constexpr int kLine = QT * (D / 4 + 2);              // floats of a lane's partial result
-    __shared__ float join[2][kLine][64];
+    const int col = lane & 15, quarter = lane >> 4;
+    const uint4 ones = make_uint4(X::kOnes, X::kOnes, X::kOnes, X::kOnes);
+    // scores: S^T[key, row], keys 16 s + 4 quarter + r
+    f32x4_t sc[QT][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        uint4 kf8[NK];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            constexpr int per = X::kBlock / 8;           // words of a block
+            const uint32_t byte = D / 4 <= X::kBlock ? raw.ks[s] : (raw.ks[s] >> (8 * (i / per))) & 0xFFu;
+            kf8[i] = X::octet(raw.k[s][i], X::scale(byte));
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            sc[t][s] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < NK; ++i) sc[t][s] = X::mfma(kf8[i], rows.q[t][i], sc[t][s]);
+        }
+    }
 
+    // A step whose keys are not all seen by all rows: scores of unseen keys are
+    // -infinity, and the scales of keys beyond the end (whose bytes may be
+    // anything, NaN among them) are cleared so that 0 times V is 0.
+    uint32_t vs[8];
+    const uint32_t vbit = 8 * (col * ND / X::kBlock);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vs[j] = raw.v_scale(j >> 2, j & 3, vbit);
+    const bool whole = groups == 3 && at >= rows.last.lo && at + kStep <= rows.first.hi && at + kStep <= end;
+    if (!whole) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = at + 16 * s + 4 * quarter + r;
+                const bool there = (groups >> s & 1) && key < end;
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    if (!there || key < rows.see[t].lo || key >= rows.see[t].hi) sc[t][s][r] = -__builtin_inff();
+                if (!there) vs[4 * s + r] = 0;
+            }
+        if constexpr (BIAS == 0) poison_seen<ND, QT>(vs, sc, sum.o, ones);
+    }
+
+    // running maximum, P
+    uint4 p[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
+                          fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
+        top *= rows.c[t];
+        if (__any(top > sum.m[t] + kLazy)) {
+            const float mn = fmaxf(sum.m[t], column_max(top));
+            const float f = __builtin_amdgcn_exp2f(sum.m[t] - mn);
+            sum.m[t] = mn;
+            sum.l[t] *= f;
+#pragma unroll
+            for (int n = 0; n < ND; ++n) sum.o[t][n] *= f;
+        }
+        float e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][k >> 2][k & 3], rows.c[t], -sum.m[t]));
+        p[t] = make_uint4(X::round2(e[0], e[1]), X::round2(e[2], e[3]), X::round2(e[4], e[5]), X::round2(e[6], e[7]));
+        sum.l[t] = X::mfma(ones, p[t], sum.l[t]);
+    }
+
+    // O^T += V^T P^T, two values of head_dim (one byte of codes) at a time
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vs[j] = X::scale(vs[j]);
+    auto two = [&](auto byte_c) {
+        constexpr int y = decltype(byte_c)::value;
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = X::template pair<(y & 3)>(raw.v[j][y >> 2], vs[j]);
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            lo[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x05040100u);
+            hi[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x07060302u);
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            sum.o[t][2 * y] = X::mfma(make_uint4(lo[0], lo[1], lo[2], lo[3]), p[t], sum.o[t][2 * y]);
+            sum.o[t][2 * y + 1] = X::mfma(make_uint4(hi[0], hi[1], hi[2], hi[3]), p[t], sum.o[t][2 * y + 1]);
+        }
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    if constexpr (ND > 4) {
+        two(std::integral_constant<int, 2>{});
+        two(std::integral_constant<int, 3>{});
+    }
+    if constexpr (ND > 8) {
+        two(std::integral_constant<int, 4>{});
+        two(std::integral_constant<int, 5>{});
+        two(std::integral_constant<int, 6>{});
+        two(std::integral_constant<int, 7>{});
+    }
+}
+
+// Steps at, at + stride, ... before end, through the wave's ring.  The rows of the next
+// 64 steps are looked up together, a step a lane: a scalar look-up in each step would
+// be waited for with the step's LDS reads, which count on the same counter.
+template <int D, int BIAS, int QT>
+__device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* lds, const int32_t* table, int head, int at,
+                                       int end, int stride, const Rows<D, BIAS, QT>& rows, int lane, Sums<D, QT>& sum)
+{
+    using R = Ring<D, BIAS>;
+    if (at >= end) return;
+    R ring(lds, a.kv, lane);
+    uint32_t groups = 0;                                 // two bits for each step under way, the next one's lowest
+    int next = at, slot = 0, known = 64;                 // the step to issue, its stage, its lane of `row`
+    int64_t row[2];                                      // of a step's groups, -1: absent
+    auto issue = [&](int behind) {
+        if (known == 64) {
+            known = 0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const KvGroup g = kv_group(table, next + lane * stride + kKvGroup * s, end, a.per_page, a.kv.num_pages,
+                                           a.kv.heads, head);
+                row[s] = g.ok ? g.row : -1;
+            }
+        }
+        KvGroup g[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)row[s], known);
+            const int32_t hi = __builtin_amdgcn_readlane((int32_t)(row[s] >> 32), known);
+            g[s].ok = hi >= 0;
+            g[s].row = hi >= 0 ? (int64_t)hi << 32 | lo : 0;
+        }
+        ++known;
+        ring.issue(slot, g);
+        groups |= (uint32_t)(g[0].ok | g[1].ok << 1) << (2 * behind);
+        slot = (slot + 1) % R::kDepth;
+        next += stride;
+    };
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i)
+        if (next < end) issue(i);
+    for (int now = 0; at < end; at += stride, now = (now + 1) % R::kDepth, groups >>= 2) {
+        if (next < end) {
+            issue(R::kDepth - 1);
+            wait_loads<(R::kDepth - 1) * R::kLoads>();
+        } else {
+            wait_loads<0>();
+        }
+        Raw<D, BIAS> raw;
+        ring.read(now, raw);
+        attend_step<D, BIAS, QT>(raw, groups & 3, at, end, rows, lane, sum);
+    }
+}
+
+// Joins the four waves' sums of the same rows into wave 0's, in a fixed order: 2 and 3
+// into 0 and 1, then 1 into 0.
+template <int D, int QT>
+struct JoinLds {
+    float w[2][QT * (D / 4 + 2)][64];
+};
+
+// LDS of a workgroup: the waves' rings, and after them in time the join.
+template <int D, int BIAS, int QT>
+constexpr int lds_bytes()
+{
+    constexpr int ring = kWaves * Ring<D, BIAS>::kWave, join = (int)sizeof(JoinLds<D, QT>);
+    return ring > join ? ring : join;
+}
+
+template <int D, int QT>
+__device__ __forceinline__ void join_waves(JoinLds<D, QT>& lds, int wave, int lane, Sums<D, QT>& sum)
+{
+    __syncthreads();                                     // every wave is done with its ring
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+            float(*w)[64] = lds.w[wave - half];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                w[t * (D / 4 + 2)][lane] = sum.m[t];
+                w[t * (D / 4 + 2) + 1][lane] = sum.l[t][0];
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) w[t * (D / 4 + 2) + 2 + 4 * n + r][lane] = sum.o[t][n][r];
+            }
+        }
+        __syncthreads();
+        if (wave < half) {
+            float(*w)[64] = lds.w[wave];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                const float mo = w[t * (D / 4 + 2)][lane], mn = fmaxf(sum.m[t], mo);
+                const float f = __builtin_amdgcn_exp2f(sum.m[t] - mn), g = __builtin_amdgcn_exp2f(mo - mn);
+                sum.m[t] = mn;
+                sum.l[t][0] = sum.l[t][0] * f + w[t * (D / 4 + 2) + 1][lane] * g;
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        sum.o[t][n][r] = sum.o[t][n][r] * f + w[t * (D / 4 + 2) + 2 + 4 * n + r][lane] * g;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Final results of a wave's rows.
+template <int D, int BIAS, int QT>
+__device__ __forceinline__ void write_rows(const AttnArgs& a, const Rows<D, BIAS, QT>& rows, const Sums<D, QT>& sum,
+                                           int head, int lane)
+{
+    const float unshift = Dec<BIAS>::kUnshift * (a.kv.v_outer ? a.kv.v_outer[head] : 1.0f);
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int64_t row = rows.out[t];
+        if (row < 0) continue;
+        float lse, y[D / 4];
+        const float l = sum.l[t][0];
+        const float f = finish_row(sum.m[t], l, a.sinks, (int)(row % a.q_heads), lse) * unshift;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) y[D / 16 * r + n] = l == 0.0f ? 0.0f : sum.o[t][n][r] * f;
+        store_row<D>(a.out, a.out_f32 != 0, row, lane >> 4, y);
+        if (a.lse && lane < 16) a.lse[row] = lse;
+    }
+}
+
+// Partial results of a wave's rows: row t * 16 + column (or its place in the output) from
+// `first` of the scratch.
+template <int D, int BIAS, int QT>
+__device__ __forceinline__ void write_parts(const AttnArgs& a, const Rows<D, BIAS, QT>& rows, const Sums<D, QT>& sum,
+                                            int64_t first, bool by_output, int lane)
+{
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        if (rows.out[t] < 0) continue;
+        const int64_t row = first + (by_output ? rows.out[t] : 16 * t + (lane & 15));
+        const float l = sum.l[t][0];
+        if (lane < 16) *(float2*)(a.part_ml + row * 2) = make_float2(sum.m[t], l);
+        if (l == 0.0f) continue;
+        float y[D / 4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) y[D / 16 * r + n] = sum.o[t][n][r];
+        store_row<D>(a.part_o, true, row, lane >> 4, y);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// All rows of a sequence and KV head fit one wave, and the four waves of a workgroup take
+// every fourth step of them.  A unit is 128 keys of one sequence and head; the keys of each are
+// cut into parts of at most `share` units, one a workgroup, with the share chosen on the device
+// (the lengths are there) so that the parts of all sequences fill the chip about once.  k_attn_few_join
+// joins the parts.  Fixed parts of the longest sequence's keys left the chip
+// unevenly loaded (48 sequences up to 8192 keys: ...).
+struct Seq {
+    int first_q, queries, kv;
+    int lo, hi;                                          // keys of all rows, from the step of the first
+    int units;                                           // of one head, 0: no queries
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b)
+{
+    const QueryRange qr = queries_of(a, b);
+    Seq s;
+    s.first_q = qr.first;
+    s.queries = qr.count;
+    s.kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
+    s.lo = key_range(0, qr.count, s.kv, a.causal, a.window).lo / kStep * kStep;
+    s.hi = max(key_range(qr.count - 1, qr.count, s.kv, a.causal, a.window).hi, s.lo);
+    s.units = qr.count == 0 ? 0 : max(1, (s.hi - s.lo + kUnit - 1) / kUnit);
+    return s;
+}
+
+__device__ __forceinline__ Seq seq_of_lane(const Seq& s, int lane)
+{
+    const auto r = [lane](int v) { return __builtin_amdgcn_readlane(v, lane); };
+    return Seq{r(s.first_q), r(s.queries), r(s.kv), r(s.lo), r(s.hi), r(s.units)};
+}
+
+// Sequence b0 + lane, or none.
+__device__ __forceinline__ Seq seq_of_chunk(const AttnArgs& a, int b0, int lane)
+{
+    return b0 + lane < a.batch ? seq_of(a, b0 + lane) : Seq{0, 0, 0, 0, 0, 0};
+}
+
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ int lane_sums(int v)
+{
+    const auto add = [&v](int moved) { v += moved; };
+    add(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // from 1, 2, 4, 8 lanes below in rows of 16
+    add(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, v, kDppBcast15, 0xA, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0, v, kDppBcast31, 0xC, 0xF, false));
+    return v;
+}
+
+// Units of a part: with `slots` workgroups at once and half a part lost a sequence.
+__device__ __forceinline__ int share_of(int total, const AttnArgs& a)
+{
+    const int per_head = max(1, a.slots / a.kv.heads);
+    const int parts = max(per_head - a.batch / 2, (per_head + 3) / 4);
+    return max((total + parts - 1) / parts, kMinShare);
+}
+
+__device__ __forceinline__ int parts_of(int units, int share) { return (units + share - 1) / share; }
+
+template <int D, int BIAS, int QT>
+__global__ __launch_bounds__(64 * kWaves, QT == 1 && D == 64 ? 4 : D == 256 && QT == 2 ? 1 : 2) void k_attn_few(AttnArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int col = lane & 15, quarter = lane >> 4;
+    const int head = (int)blockIdx.x % a.kv.heads, place = (int)blockIdx.x / a.kv.heads;
+    int seq = place, part = 0, parts = 1;
+    Seq q;
+    if (a.slots == 0) {                                  // one workgroup a sequence and head
+        q = seq_of(a, seq);
+        if (q.units == 0) return;
+    } else {
+        // lane l holds sequence b0 + l of 64 at a time
+        Seq mine = seq_of_chunk(a, 0, lane);
+        int total = __builtin_amdgcn_readlane(lane_sums(mine.units), 63);
+        for (int b = 64; b < a.batch; b += 64)
+            total += __builtin_amdgcn_readlane(lane_sums(seq_of_chunk(a, b, lane).units), 63);
+        const int share = share_of(total, a);
+        int b0 = 0, before = 0;                          // parts of a head before chunk b0
+        while (true) {
+            const int n = parts_of(mine.units, share), upto = lane_sums(n);
+            const uint64_t past = __ballot(before + upto > place);
+            if (past) {
+                const int j = __ffsll((unsigned long long)past) - 1;
+                seq = b0 + j;
+                parts = __builtin_amdgcn_readlane(n, j);
+                part = place - before - (__builtin_amdgcn_readlane(upto, j) - parts);
+                q = seq_of_lane(mine, j);
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, 63);
+            b0 += 64;
+            if (b0 >= a.batch) return;                   // more workgroups than parts
+            mine = seq_of_chunk(a, b0, lane);
+        }
+    }
+    const int from = (int)((int64_t)q.units * part / parts), to = (int)((int64_t)q.units * (part + 1) / parts);
+    Rows<D, BIAS, QT> rows;
+    Sums<D, QT> sum;
+    rows.load(a, QueryRange{q.first_q, q.queries}, q.kv, head, 0, lane);
+    sum.clear();
+    attend<D, BIAS, QT>(a, smem + wave * Ring<D, BIAS>::kWave, a.table + (int64_t)seq * a.table_cols, head,
+                        q.lo + from * kUnit + wave * kStep, min(q.hi, q.lo + to * kUnit), kUnit, rows, lane, sum);
+    join_waves<D, QT>(*reinterpret_cast<JoinLds<D, QT>*>(smem), wave, lane, sum);
+    if (wave != 0) return;
+    if (parts == 1) write_rows<D, BIAS, QT>(a, rows, sum, head, lane);
+    else write_parts<D, BIAS, QT>(a, rows, sum, (int64_t)blockIdx.x * (16 * QT), false, lane);
+}
+
+// Joins the parts of one row a wave.
+template <int D, int QT>
+__global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift)
+{
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = (int)blockIdx.x * 4 + wave;          // of a sequence and head
+    const int head = (int)blockIdx.y, seq = (int)blockIdx.z;
+    const QueryRange qr = queries_of(a, seq);
+    if (row >= qr.count * a.group) return;
+    int total = 0;
+    Seq mine = seq_of_chunk(a, 0, lane);
+    total = __builtin_amdgcn_readlane(lane_sums(mine.units), 63);
+    for (int b = 64; b < a.batch; b += 64)
+        total += __builtin_amdgcn_readlane(lane_sums(seq_of_chunk(a, b, lane).units), 63);
+    const int share = share_of(total, a);
+    int first = 0;                                       // parts of a head before this sequence's
+    for (int b0 = 0; b0 + 64 <= seq; b0 += 64) {
+        first += __builtin_amdgcn_readlane(lane_sums(parts_of(mine.units, share)), 63);
+        mine = seq_of_chunk(a, b0 + 64, lane);
+    }
+    const int n = parts_of(mine.units, share), upto = lane_sums(n);
+    const int parts = __builtin_amdgcn_readlane(n, seq & 63);
+    first += __builtin_amdgcn_readlane(upto, seq & 63) - parts;
+    if (parts <= 1) return;
+    const auto part_row = [&](int p) { return ((int64_t)(first + p) * a.kv.heads + head) * (16 * QT) + row; };
+    constexpr int N = D / 64;
+    float acc[N] = {}, l = 0.0f, top = kNoMax;
+    for (int p0 = 0; p0 < parts; p0 += 64) {
+        const float2 ml = p0 + lane < parts ? *(const float2*)(a.part_ml + part_row(p0 + lane) * 2) : make_float2(0.0f, 0.0f);
+        const float mn = fmaxf(top, group_max<64>(ml.y != 0.0f ? ml.x : kNoMax));
+        const float f = __builtin_amdgcn_exp2f(top - mn), w = ml.y != 0.0f ? __builtin_amdgcn_exp2f(ml.x - mn) : 0.0f;
+        top = mn;
+        float part_l = ml.y * w;
+#pragma unroll
+        for (int i = 1; i < 64; i <<= 1) part_l += __shfl_xor(part_l, i, 64);
+        l = l * f + part_l;
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] *= f;
+        const uint64_t used = __ballot(ml.y != 0.0f);    // parts without a key were not written
+        const int here = min(64, parts - p0);
+        for (int j0 = 0; j0 < here; j0 += 8) {
+            float v[8][N];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool on = (used >> (j0 + j)) & 1;
+                const float* p = a.part_o + part_row(p0 + j0 + j) * D + lane * N;
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[j][i] = on ? p[i] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float g = __shfl(w, j0 + j, 64);
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(v[j][i], g, acc[i]);
+            }
+        }
+    }
+    const int i = row / a.group, qh = head * a.group + row - i * a.group;
+    write_joined<D>(a, (int64_t)(qr.first + i) * a.q_heads + qh, qh, top, l, acc, unshift, lane);
+}
+
+// ---------------------------------------------------------------- many rows
+// Each wave has rows of its own and takes every step of their keys; a sequence whose rows fit one
+// wave is shared by the four as above.  Few workgroups split the keys `splits` ways.
+template <int D, int BIAS>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn(AttnArgs a)
+{
+    constexpr int QT = 2, kRows = 16 * QT;
+    extern __shared__ __align__(16) unsigned char smem[];
+    JoinLds<D, QT>& lds = *reinterpret_cast<JoinLds<D, QT>*>(smem);
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int head = (int)blockIdx.x;
     const int b = (int)blockIdx.z % a.batch, split = (int)blockIdx.z / a.batch;
     const QueryRange qr = queries_of(a, b);
     const int kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
-    const int rows = qr.count * a.group;
-    if (rows == 0) return;
-    // Rows that fit one wave are shared by the four (each takes every fourth step);
-    // otherwise each wave has rows of its own and takes every step.
-    const bool shared = rows <= kRows;
+    const int count = qr.count * a.group;
+    if (count == 0) return;
+    const bool shared = count <= kRows;
     const int row0 = shared ? 0 : ((int)blockIdx.y * kWaves + wave) * kRows;
-    if (shared ? blockIdx.y > 0 : (int)blockIdx.y * kWaves * kRows >= rows) return;
-
-    // keys of this wave's rows: those of its first and last query
-    const bool idle = row0 >= rows;
-    const int first_q = min(row0, rows - 1) / a.group, last_q = (min(row0 + kRows, rows) - 1) / a.group;
-    const KeyRange kf = key_range(first_q, qr.count, kv, a.causal, a.window);
-    const KeyRange kl = key_range(last_q, qr.count, kv, a.causal, a.window);
-    const int base = kf.lo / kStep * kStep;
-    const int begin = base + split * a.chunk;
-    const int end = idle ? 0 : min(kl.hi, begin + a.chunk);
-
-    uint4 q[QT][NK];
-    float c[QT];
-    KeyRange see[QT];
-    int64_t out_row[QT];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const int r = row0 + 16 * t + col;
-        const bool live = r < rows;
-        const int i = live ? r / a.group : 0, g = live ? r - i * a.group : 0;
-        see[t] = key_range(i, qr.count, kv, a.causal, a.window);
-        out_row[t] = live ? (int64_t)(qr.first + i) * a.q_heads + head * a.group + g : -1;
-        const uint16_t* p = a.q + (int64_t)(qr.first + i) * a.ld_q + (int64_t)(head * a.group + g) * D + quarter * (D / 4);
-#pragma unroll
-        for (int k = 0; k < NK; ++k) q[t][k] = live ? ((const uint4*)p)[k] : make_uint4(0, 0, 0, 0);
-        c[t] = a.scale * kLog2e * X::kUnshift;
-        if constexpr (!X::kBf16) {
-            c[t] *= q_to_f16<NK>(q[t]);
-            if (a.kv.k_outer) c[t] *= a.kv.k_outer[head];
-        }
-        c[t] = fmaxf(c[t], 1.17549435e-38f);             // 0 would turn a masked score into NaN
-    }
-
-    f32x4_t o[QT][ND], l[QT];
-    float m[QT];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        m[t] = kNoMax;
-        l[t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int n = 0; n < ND; ++n) o[t][n] = f32x4_t{0, 0, 0, 0};
-    }
-
-    const int32_t* table = a.table + (int64_t)b * a.table_cols;
-    const int stride = shared ? kWaves * kStep : kStep;
-    int at = begin + (shared ? wave * kStep : 0);
-    KvGroup grp[2];
-    Raw<D, BIAS> cur;
-    const uint4 ones = make_uint4(X::kOnes, X::kOnes, X::kOnes, X::kOnes);
-    auto fetch = [&](int t0, KvGroup (&g)[2], Raw<D, BIAS>& r) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            g[s] = kv_group(table, t0 + 16 * s, end, a.per_page, a.kv.num_pages, a.kv.heads, head);
-        load_step<D, BIAS>(a.kv, g, lane, r);
-    };
-    if (at < end) fetch(at, grp, cur);
-    for (; at < end; at += stride) {
-        Raw<D, BIAS> nxt;
-        KvGroup grp_n[2];
-        fetch(at + stride, grp_n, nxt);                  // past the end: the cache's first rows, unused
-
-        // scores: S^T[key, row], keys 16 s + 4 quarter + r
-        f32x4_t sc[QT][2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            uint4 kf8[NK];
-#pragma unroll
-            for (int i = 0; i < NK; ++i) {
-                constexpr int per = X::kBlock / 8;       // words of a block
-                const uint32_t byte = D / 4 <= X::kBlock ? cur.ks[s] : (cur.ks[s] >> (8 * (i / per))) & 0xFFu;
-                kf8[i] = X::octet(cur.k[s][i], X::scale(byte));
-            }
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                sc[t][s] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < NK; ++i) sc[t][s] = X::mfma(kf8[i], q[t][i], sc[t][s]);
-            }
-        }
-
-        // A step whose keys are not all seen by all rows: scores of unseen keys are
-        // -infinity, and the scales of keys beyond the end (whose bytes may be
-        // anything, NaN among them) are cleared so that 0 times V is 0.
-        const bool whole = grp[0].ok && grp[1].ok && at >= kl.lo && at + kStep <= kf.hi && at + kStep <= end;
-        if (!whole) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int key = at + 16 * s + 4 * quarter + r;
-                    const bool there = grp[s].ok && key < end;
-#pragma unroll
-                    for (int t = 0; t < QT; ++t)
-                        if (!there || key < see[t].lo || key >= see[t].hi) sc[t][s][r] = -__builtin_inff();
-                    if (!there) cur.vs[4 * s + r] = 0;
-                }
-            if constexpr (BIAS == 0) poison_seen<ND, QT>(cur, sc, o, ones);
-        }
-
-        // running maximum, P
-        uint4 p[QT];
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
-                              fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-            top *= c[t];
-            if (__any(top > m[t] + kLazy)) {
-                const float mn = fmaxf(m[t], column_max(top));
-                const float f = __builtin_amdgcn_exp2f(m[t] - mn);
-                m[t] = mn;
-                l[t] *= f;
-#pragma unroll
-                for (int n = 0; n < ND; ++n) o[t][n] *= f;
-            }
-            float e[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][k >> 2][k & 3], c[t], -m[t]));
-            p[t] = make_uint4(X::round2(e[0], e[1]), X::round2(e[2], e[3]), X::round2(e[4], e[5]), X::round2(e[6], e[7]));
-            l[t] = X::mfma(ones, p[t], l[t]);
-        }
-
-        // O^T += V^T P^T, two values of head_dim (one byte of codes) at a time
-        uint32_t vs[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vs[j] = X::scale(cur.vs[j]);
-        auto two = [&](auto byte_c) {
-            constexpr int y = decltype(byte_c)::value;
-            uint32_t u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = X::template pair<(y & 3)>(cur.v[j][y >> 2], vs[j]);
-            uint32_t lo[4], hi[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x05040100u);
-                hi[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x07060302u);
-            }
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                o[t][2 * y] = X::mfma(make_uint4(lo[0], lo[1], lo[2], lo[3]), p[t], o[t][2 * y]);
-                o[t][2 * y + 1] = X::mfma(make_uint4(hi[0], hi[1], hi[2], hi[3]), p[t], o[t][2 * y + 1]);
-            }
-        };
-        two(std::integral_constant<int, 0>{});
-        two(std::integral_constant<int, 1>{});
-        if constexpr (ND > 4) {
-            two(std::integral_constant<int, 2>{});
-            two(std::integral_constant<int, 3>{});
-        }
-        if constexpr (ND > 8) {
-            two(std::integral_constant<int, 4>{});
-            two(std::integral_constant<int, 5>{});
-            two(std::integral_constant<int, 6>{});
-            two(std::integral_constant<int, 7>{});
-        }
-        cur = nxt;
-        grp[0] = grp_n[0];
-        grp[1] = grp_n[1];
-    }
-
-    // This lane's part of a row: d = (D / 4) quarter + ND r + n from o[n][r].
-    float res[QT][D / 4], lsum[QT];
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        lsum[t] = l[t][0];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int n = 0; n < ND; ++n) res[t][ND * r + n] = o[t][n][r];
-    }
-
+    if (shared ? blockIdx.y > 0 : (int)blockIdx.y * kWaves * kRows >= count) return;
+    Rows<D, BIAS, QT> rows;
+    Sums<D, QT> sum;
+    rows.load(a, qr, kv, head, row0, lane);
+    sum.clear();
+    const int begin = rows.first.lo / kStep * kStep + split * a.chunk;
+    const int end = row0 >= count ? 0 : min(rows.last.hi, begin + a.chunk);
+    attend<D, BIAS, QT>(a, smem + wave * Ring<D, BIAS>::kWave, a.table + (int64_t)b * a.table_cols, head, begin + (shared ? wave * kStep : 0), end,
+                        shared ? kUnit : kStep, rows, lane, sum);
     if (shared) {
-        // join the four waves: 2 and 3 into 0 and 1, then 1 into 0
-#pragma unroll
-        for (int half = 2; half >= 1; half >>= 1) {
-            if (wave >= half && wave < 2 * half) {
-                float(*w)[64] = join[wave - half];
-#pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    w[t * (D / 4 + 2)][lane] = m[t];
-                    w[t * (D / 4 + 2) + 1][lane] = lsum[t];
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) w[t * (D / 4 + 2) + 2 + i][lane] = res[t][i];
-                }
-            }
-            __syncthreads();
-            if (wave < half) {
-                float(*w)[64] = join[wave];
-#pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    const float mo = w[t * (D / 4 + 2)][lane], mn = fmaxf(m[t], mo);
-                    const float f = __builtin_amdgcn_exp2f(m[t] - mn), g = __builtin_amdgcn_exp2f(mo - mn);
-                    m[t] = mn;
-                    lsum[t] = lsum[t] * f + w[t * (D / 4 + 2) + 1][lane] * g;
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) res[t][i] = res[t][i] * f + w[t * (D / 4 + 2) + 2 + i][lane] * g;
-                }
-            }
-            __syncthreads();
-        }
+        join_waves<D, QT>(lds, wave, lane, sum);
         if (wave != 0) return;
     }
-
-    const float unshift = X::kUnshift * (a.kv.v_outer ? a.kv.v_outer[head] : 1.0f);
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        if (out_row[t] < 0) continue;
-        if (a.splits > 1) {
-            const int64_t row = (int64_t)split * a.total_q * a.q_heads + out_row[t];
-            if (quarter == 0) *(float2*)(a.part_ml + row * 2) = make_float2(m[t], lsum[t]);
-            if (lsum[t] != 0.0f) store_row<D>(a.part_o, true, row, quarter, res[t]);
-        } else {
-            const int qh = head * a.group + (int)((out_row[t] - (int64_t)head * a.group) % a.q_heads);
-            float lse;
-            const float f = finish_row(m[t], lsum[t], a.sinks, qh, lse) * unshift;
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) res[t][i] = lsum[t] == 0.0f ? 0.0f : res[t][i] * f;
-            store_row<D>(a.out, a.out_f32 != 0, out_row[t], quarter, res[t]);
-            if (a.lse && quarter == 0) a.lse[out_row[t]] = lse;
-        }
-    }
+    if (a.splits > 1) write_parts<D, BIAS, QT>(a, rows, sum, (int64_t)split * a.total_q * a.q_heads, true, lane);
+    else write_rows<D, BIAS, QT>(a, rows, sum, head, lane);
 }
 
 // Joins the splits of one row a wave: row r of sequence b's.
@@ -483,48 +905,77 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, float unshift)
         mine |= token >= r.first && token < r.first + r.count;
     }
     if (!__any(mine)) return;
-    float top = kNoMax;
-    for (int s = lane; s < a.splits; s += 64) {
-        const float2 ml = *(const float2*)(a.part_ml + (s * rows + row) * 2);
-        if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-    }
-    top = group_max<64>(top);
+    // lane s holds split s's (m, l); a row's reference is the largest m of those that saw a key
+    static_assert(kMaxSplits <= 64, "a lane for each split");
+    const float2 ml = lane < a.splits ? *(const float2*)(a.part_ml + (lane * rows + row) * 2) : make_float2(0.0f, 0.0f);
+    const float top = group_max<64>(ml.y != 0.0f ? ml.x : kNoMax);
+    const float w = ml.y != 0.0f ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f;
+    float l = ml.y * w;
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i, 64);
     constexpr int N = D / 64;
-    float acc[N] = {}, l = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 ml = *(const float2*)(a.part_ml + (s * rows + row) * 2);
-        if (ml.y == 0.0f) continue;
-        const float f = __builtin_amdgcn_exp2f(ml.x - top);
-        l += ml.y * f;
-        const float* p = a.part_o + (s * rows + row) * D + lane * N;
+    float acc[N] = {};
+    const uint64_t used = __ballot(ml.y != 0.0f);
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+        float p[8][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += p[i] * f;
-    }
-    float lse;
-    const bool none = l == 0.0f;
-    float f = finish_row(top, l, a.sinks, qh, lse) * unshift;
-    if (a.kv.v_outer) f *= a.kv.v_outer[qh / a.group];
+        for (int j = 0; j < 8; ++j) {                    // parts without a key were not written
+            const bool on = (used >> (s0 + j)) & 1;
+            const float* q = a.part_o + ((s0 + j) * rows + row) * D + lane * N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float y = none ? 0.0f : acc[i] * f;
-        if (a.out_f32) ((float*)a.out)[row * D + lane * N + i] = y;
-        else ((uint16_t*)a.out)[row * D + lane * N + i] = (uint16_t)f32_to_bf16(y);
+            for (int i = 0; i < N; ++i) p[j][i] = on ? q[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = __shfl(w, s0 + j, 64);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(p[j][i], f, acc[i]);
+        }
     }
-    if (a.lse && lane == 0) a.lse[row] = lse;
+    write_joined<D>(a, row, qh, top, l, acc, unshift, lane);
+}
+
+// A kernel's LDS limit is a property of the function: raised once, outside any launch.
+template <int D, int BIAS, int QT, bool FEW>
+hipError_t allow_lds()
+{
+    constexpr int n = lds_bytes<D, BIAS, QT>();
+    const void* f = nullptr;
+    if constexpr (FEW) f = reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>);
+    else f = reinterpret_cast<const void*>(k_attn<D, BIAS>);
+    static const hipError_t st = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, n);
+    return st;
+}
+
+template <int D, int BIAS, int QT>
+hipError_t launch_few(const AttnArgs& a, hipStream_t s)
+{
+    const hipError_t st = allow_lds<D, BIAS, QT, true>();
+    if (st != hipSuccess) return st;
+    hipLaunchKernelGGL((k_attn_few<D, BIAS, QT>), dim3((uint32_t)a.groups), dim3(64 * kWaves), (lds_bytes<D, BIAS, QT>()), s, a);
+    if (a.slots)
+        hipLaunchKernelGGL((k_attn_few_join<D, QT>),
+                           dim3((uint32_t)((a.max_q * a.group + 3) / 4), (uint32_t)a.kv.heads, (uint32_t)a.batch), dim3(256),
+                           0, s, a, Dec<BIAS>::kUnshift);
+    return hipGetLastError();
 }
 
 template <int D, int BIAS>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
 {
     const int64_t rows = (int64_t)a.max_q * a.group;
-    const int block = attn_block_rows(rows);
-    const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + block - 1) / block), (uint32_t)(a.batch * a.splits));
-    if (rows <= 16) hipLaunchKernelGGL((k_attn<D, BIAS, 1>), grid, dim3(64 * kWaves), 0, s, a);
-    else hipLaunchKernelGGL((k_attn<D, BIAS, 2>), grid, dim3(64 * kWaves), 0, s, a);
-    hipError_t st = hipGetLastError();
-    if (st != hipSuccess || a.splits == 1) return st;
-    const int64_t all = (int64_t)a.total_q * a.q_heads;
-    hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
+    if (rows <= 16) return launch_few<D, BIAS, 1>(a, s);
+    if (rows <= kFewRows) return launch_few<D, BIAS, 2>(a, s);
+    const hipError_t st = allow_lds<D, BIAS, 2, false>();
+    if (st != hipSuccess) return st;
+    {
+        const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
+        hipLaunchKernelGGL((k_attn<D, BIAS>), grid, dim3(64 * kWaves), (lds_bytes<D, BIAS, 2>()), s, a);
+        if (a.splits > 1) {
+            const int64_t all = (int64_t)a.total_q * a.q_heads;
+            hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
+        }
+    }
     return hipGetLastError();
 }
 
@@ -538,17 +989,49 @@ hipError_t launch_bias(const AttnArgs& a, hipStream_t s)
 
 }  // namespace
 
-int attn_block_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 32 * kWaves; }
-
-int attn_splits(int64_t batch, int32_t kv_heads, int64_t rows, int64_t max_kv)
+AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_heads, int64_t max_q, int64_t max_kv,
+                   int64_t table_cols, int64_t window)
 {
-    const int block = attn_block_rows(rows);
-    const int64_t blocks = batch * kv_heads * ((rows + block - 1) / block);
-    int64_t want = (1024 + blocks - 1) / blocks;
-    const int64_t most = (max_kv + 511) / 512;           // at least four steps for each wave
-    if (want > most) want = most;
-    if (want > 64) want = 64;
-    return want < 1 ? 1 : (int)want;
+    AttnPlan p{1, 1 << 30, 0, 0, 0, 0};
+    const int64_t rows = max_q * (q_heads / kv.heads);
+    if (rows == 0 || batch == 0) return p;
+    // keys that one tile of rows can see
+    int64_t keys = max_kv < table_cols * kv.page_size ? max_kv : table_cols * kv.page_size;
+    if (window && window + max_q + kStep < keys) keys = window + max_q + kStep;
+    const int64_t heads = batch * kv.heads;
+    if (rows <= kFewRows) {
+        // Workgroups that the chip holds at once: 4 a compute unit (head_dim 64; 3 with two
+        // tiles of rows), 2 (128) or 2 and 1 (256) by their LDS and registers.  Keys are not cut where
+        // every sequence is short or the heads alone fill the chip twice.
+        const bool one = rows <= 16;
+        const int64_t slots = 256 * (kv.dim == 64 ? (one ? 4 : 3) : kv.dim == 128 || one ? 2 : 1);
+        p.groups = (int32_t)heads;
+        if (keys <= kUnit * kMinShare || heads >= 2 * slots) return p;
+        // no share makes more parts than these: a part is a share, or the last of its sequence
+        const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
+        int64_t parts = per_head + batch;
+        const int64_t most = batch * ((keys / kUnit + 2) / kMinShare + 1);
+        if (parts > most) parts = most;
+        p.slots = (int32_t)slots;
+        p.groups = (int32_t)(parts * kv.heads);
+        const size_t n = (size_t)p.groups * (rows <= 16 ? 16 : 32);
+        p.ml = n * 2 * sizeof(float);
+        p.o = n * kv.dim * sizeof(float);
+        return p;
+    }
+    // Tiles of rows fill the chip by themselves or split the keys until they do once.
+    const int64_t blocks = heads * ((rows + kTileRows - 1) / kTileRows);
+    int64_t want = 256 / blocks;
+    if (want > keys / 512) want = keys / 512;
+    if (want > kMaxSplits) want = kMaxSplits;
+    if (want > 65535 / batch) want = 65535 / batch;
+    if (want <= 1) return p;
+    p.splits = (int32_t)want;
+    p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);
+    const size_t n = (size_t)want * total_q * q_heads;
+    p.ml = n * 2 * sizeof(float);
+    p.o = n * kv.dim * sizeof(float);
+    return p;
 }
 
 hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s)

@@ -250,19 +250,24 @@ struct AttnArgs {
     const float* sinks;      // [q_heads] or null
     void* out;               // bf16 or FP32 [total_q, q_heads, dim]
     float* lse;              // [total_q, q_heads] or null
-    float* part_o;           // [splits][total_q * q_heads][dim], splits > 1
-    float* part_ml;          // [splits][total_q * q_heads][2]
+    float* part_o;           // rows of partial results [dim]: [groups][2][16 or 32], or
+    float* part_ml;          // [splits][total_q * q_heads]; their (m, l)
     float scale;
     int32_t batch, total_q, q_heads, group, table_cols, max_q, max_kv, causal, window;
-    int32_t splits, chunk;   // parts of a sequence's keys and the keys of one (a multiple of 128)
+    int32_t slots, groups;   // few rows: workgroups that the chip holds (0: keys are not cut), workgroups
+    int32_t splits, chunk;   // many rows: parts of a sequence's keys and the keys of one (a multiple of 128)
     int32_t out_f32;
     DivBy per_page;          // 16-token groups of a page
 };
 
-// Rows of queries (query x head of a group) that a workgroup of k_attn takes,
-// and how a call's keys are split.
-int attn_block_rows(int64_t rows);
-int attn_splits(int64_t batch, int32_t kv_heads, int64_t rows, int64_t max_kv);
+// How a call's keys are shared (fields as above) and the bytes of its partial results.
+struct AttnPlan {
+    int32_t splits, chunk, slots, groups;
+    size_t ml, o;
+};
+
+AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_heads, int64_t max_q, int64_t max_kv,
+                   int64_t table_cols, int64_t window);
 hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s);
 
 // y = x W^T with bf16 x [M, ld_x] and a 4-bit W [N, K] (rowwise codes and scale bytes).

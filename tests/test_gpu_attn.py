@@ -110,7 +110,8 @@ def test_single_tokens(fmt, D):
     """Lengths from none to several steps, around every tile border."""
     lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 513]
     s = Setup(fmt, D, 2, 4, 16, lens, [1] * len(lens), outer=fmt != "mxfp4").device()
-    out, lse = s.check()
+    s.check()
+    out, lse = s.check(max_q=1)
     assert not out[0].any() and torch.isinf(lse[0]).all()
     again, _ = s.run(q_starts=None)
     assert torch.equal(out, again)
