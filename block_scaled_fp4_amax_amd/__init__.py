@@ -564,19 +564,28 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, str
         _need(outer, 4 * (N // (cfg.outer_block_size if cfg.outer_2d else 1)) * (K // cfg.outer_block_size), "outer")
     if outer is not None and outer.dtype != torch.float32:
         raise ValueError("outer must be float32")
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("fp4q takes device tensors; got one on %s" % dev)
+    if codes.device != dev or scales.device != dev or (outer is not None and outer.device != dev):
+        raise ValueError("x and the weight must be on one device")
     if y is None:
-        y = _held_on(torch.empty((M, N), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=x.device),
-                     stream)
-    if tuple(y.shape) != (M, N) or (N > 1 and y.stride(1) != 1) or y.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("y must be a bf16 or float32 [%d, %d] view with contiguous rows" % (M, N))
+        y = _held_on(torch.empty((M, N), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=dev), stream)
+    elif tuple(y.shape) != (M, N) or (N > 1 and y.stride(1) != 1) or y.device != dev:
+        raise ValueError("y must be a [%d, %d] view with contiguous rows on %s" % (M, N, dev))
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise Fp4Error(ERR_DTYPE, "y dtype %s" % y.dtype)
     ycfg = _with_dtypes(cfg, "bf16", _dtype_name(y))
-    _check(lib().fp4_linear(ct.byref(ycfg), _ptr(x), M, x.stride(0) if M > 1 else K, _ptr(codes), _ptr(scales),
-                            _ptr(outer), int(bool(outer_transposed)), N, K, _ptr(y), y.stride(0) if M > 1 else N,
-                            _stream(stream)), "fp4_linear")
+    _check(lib().fp4_linear(ct.byref(ycfg), x.data_ptr(), M, x.stride(0) if M > 1 else K, codes.data_ptr(),
+                            scales.data_ptr(), None if outer is None else outer.data_ptr(), 1 if outer_transposed else 0, N,
+                            K, y.data_ptr(), y.stride(0) if M > 1 else N, _raw_stream(stream, dev)), "fp4_linear")
     return y
 
 
 # ------------------------------------------------------------------ the paged 4-bit cache
+# Single tokens make these calls every few microseconds, so they are marshalled with what costs
+# least: plain addresses (checked to be on the cache's device), configurations and structures
+# built once for a cache, and the stream's raw handle.
 def _held_on(t, stream):
     """A tensor allocated here stays reserved until the work of a caller's
     stream that uses it is done."""
@@ -586,20 +595,31 @@ def _held_on(t, stream):
     return t
 
 
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _heads_rows(t, heads, dim, what, dtypes):
     """Token pitch of a [tokens, heads, dim] tensor whose tokens are whole runs."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
-        raise ValueError("%s must be [tokens, %d, %d], got %s" % (what, heads, dim, tuple(t.shape)))
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError("%s must be [tokens, %d, %d], got %s" % (what, heads, dim, tuple(shape)))
     if t.dtype not in dtypes:
         raise Fp4Error(ERR_DTYPE, "%s dtype %s" % (what, t.dtype))
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    s0, s1, s2 = t.stride()
+    if shape[0] and (s2 != 1 or (heads > 1 and s1 != dim)):
         raise ValueError("%s: a token's heads must be contiguous" % what)
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return s0 if shape[0] > 1 else heads * dim
 
 
-def _ints(t, dtype, shape, what, device):
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError("%s must be %s of shape %s, got %s %s" % (what, dtype, list(shape), t.dtype, list(t.shape)))
+def _ints(t, dtype, rows, cols, what, device):
+    """t: [rows] (cols None) or [rows, any], rows None: any."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != (1 if cols is None else 2) or (rows is not None and shape[0] != rows):
+        raise ValueError("%s must be %s [%s%s], got %s %s" % (what, dtype, "n" if rows is None else rows,
+                                                              "" if cols is None else ", cols", t.dtype, list(shape)))
     if not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be contiguous and on %s" % (what, device))
 
@@ -617,8 +637,10 @@ class KVCache:
             raise ValueError("codes must be [pages, kv_heads, page_size, head_dim / 2]")
         pages, heads, page, half = k_codes.shape
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, half * 2
-        self.cfg = cfg
+        self.cfg = Cfg.from_buffer_copy(cfg)
         self.device = k_codes.device
+        self._by_dtype = {torch.bfloat16: ct.byref(_with_dtypes(cfg, "bf16", "bf16")),
+                          torch.float32: ct.byref(_with_dtypes(cfg, "fp32", "fp32"))}
         shapes = {"k_codes": half, "v_codes": half, "k_scales": half * 2 // _inner(cfg),
                   "v_scales": half * 2 // _inner(cfg)}
         for n, t in (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales)):
@@ -635,6 +657,7 @@ class KVCache:
         self.k_outer, self.v_outer = k_outer, v_outer
         self._c = _KvCache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_outer), _ptr(v_outer),
                            pages, page, heads, half * 2, 0)
+        self._ref = ct.byref(self._c)
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, cfg, *, device="cuda", k_outer=None, v_outer=None):
@@ -649,38 +672,38 @@ def fp4_kv_append(cache, k, v, slots, *, stream=None):
     """Quantises k and v (bf16 or float32 [tokens, kv_heads, head_dim]; views with a
     token pitch are accepted) into the cache's slots (int64 [tokens], page *
     page_size + place; a slot outside the cache writes nothing)."""
-    torch = _torch()
+    torch, dev = _torch(), cache.device
     types = (torch.bfloat16, torch.float32)
     ld_k = _heads_rows(k, cache.kv_heads, cache.head_dim, "k", types)
     ld_v = _heads_rows(v, cache.kv_heads, cache.head_dim, "v", types)
-    if k.dtype != v.dtype or k.shape != v.shape or k.device != cache.device or v.device != cache.device:
+    n = k.shape[0]
+    if k.dtype != v.dtype or v.shape[0] != n or k.device != dev or v.device != dev:
         raise ValueError("k and v must agree in shape and dtype and lie on the cache's device")
-    _ints(slots, torch.int64, (k.shape[0],), "slots", cache.device)
-    cfg = _with_dtypes(cache.cfg, _dtype_name(k))
-    _check(lib().fp4_kv_append(ct.byref(cfg), ct.byref(cache._c), _ptr(k), ld_k, _ptr(v), ld_v, _ptr(slots), k.shape[0],
-                               _stream(stream)), "fp4_kv_append")
+    _ints(slots, torch.int64, n, None, "slots", dev)
+    _check(lib().fp4_kv_append(cache._by_dtype[k.dtype], cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
+                               slots.data_ptr(), n, _raw_stream(stream, dev)), "fp4_kv_append")
 
 
 def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
     """(k, v): bf16 (or float32: dtype) [tokens, kv_heads, head_dim] that the
     cache holds at slots (int64 [tokens]; zeros for one outside the cache).  `out` may supply
     the pair."""
-    torch = _torch()
+    torch, dev = _torch(), cache.device
     n = slots.shape[0] if slots.dim() else 0
-    _ints(slots, torch.int64, (None,), "slots", cache.device)
+    _ints(slots, torch.int64, None, None, "slots", dev)
     shape = (n, cache.kv_heads, cache.head_dim)
     if out is None:
         dtype = dtype if dtype is not None else torch.bfloat16
-        k, v = (_held_on(torch.empty(shape, dtype=dtype, device=cache.device), stream) for _ in "kv")
+        k, v = (_held_on(torch.empty(shape, dtype=dtype, device=dev), stream) for _ in "kv")
     else:
         k, v = out
-    if k.dtype not in (torch.bfloat16, torch.float32):
+        for t in (k, v):
+            if tuple(t.shape) != shape or t.dtype != k.dtype or not t.is_contiguous() or t.device != dev:
+                raise ValueError("out must be two contiguous %s tensors of one dtype" % list(shape))
+    cfg = cache._by_dtype.get(k.dtype)
+    if cfg is None:
         raise Fp4Error(ERR_DTYPE, "k dtype %s" % k.dtype)
-    for t in (k, v):
-        if tuple(t.shape) != shape or t.dtype != k.dtype or not t.is_contiguous() or t.device != cache.device:
-            raise ValueError("out must be two contiguous %s tensors of one dtype" % list(shape))
-    cfg = _with_dtypes(cache.cfg, output_dtype=_dtype_name(k))
-    _check(lib().fp4_kv_read(ct.byref(cfg), ct.byref(cache._c), _ptr(slots), n, _ptr(k), _ptr(v), _stream(stream)),
+    _check(lib().fp4_kv_read(cfg, cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
            "fp4_kv_read")
     return k, v
 
@@ -698,7 +721,7 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
               max_q=int(total_q if max_q is None else max_q),
               max_kv=int(table_cols * cache.page_size if max_kv is None else max_kv), causal=1, window=int(window),
               scale=1.0, ld_q=int(q_heads) * cache.head_dim, q_starts=16)
-    n = lib().fp4q_attn_workspace_bytes(ct.byref(cache.cfg), ct.byref(cache._c), ct.byref(a))
+    n = lib().fp4q_attn_workspace_bytes(ct.byref(cache.cfg), cache._ref, ct.byref(a))
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
 
@@ -724,11 +747,11 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     dev = cache.device
     if q.device != dev:
         raise ValueError("q must be on the cache's device")
-    _ints(kv_lens, torch.int32, (None,), "kv_lens", dev)
+    _ints(kv_lens, torch.int32, None, None, "kv_lens", dev)
     batch = kv_lens.shape[0]
-    _ints(page_table, torch.int32, (batch, None), "page_table", dev)
+    _ints(page_table, torch.int32, batch, True, "page_table", dev)
     if q_starts is not None:
-        _ints(q_starts, torch.int32, (batch + 1,), "q_starts", dev)
+        _ints(q_starts, torch.int32, batch + 1, None, "q_starts", dev)
     elif T != batch:
         raise ValueError("without q_starts, q holds one query for each of the %d sequences, got %d" % (batch, T))
     if sinks is not None and (sinks.dtype != torch.float32 or tuple(sinks.shape) != (Hq,) or not sinks.is_contiguous()
@@ -737,26 +760,30 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     if out is None:
         out = _held_on(torch.empty((T, Hq, D), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=dev),
                        stream)
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise Fp4Error(ERR_DTYPE, "out dtype %s" % out.dtype)
-    if tuple(out.shape) != (T, Hq, D) or not out.is_contiguous() or out.device != dev:
+    elif tuple(out.shape) != (T, Hq, D) or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous %s on %s" % ([T, Hq, D], dev))
+    cfg = cache._by_dtype.get(out.dtype)
+    if cfg is None:
+        raise Fp4Error(ERR_DTYPE, "out dtype %s" % out.dtype)
     lse = _held_on(torch.empty((T, Hq), dtype=torch.float32, device=dev), stream) if with_lse else None
     cols = page_table.shape[1]
     if max_q is None:
         max_q = 1 if q_starts is None else T
     if max_kv is None:
         max_kv = cols * cache.page_size
-    a = _Attn(_ptr(q), ld, _ptr(page_table), _ptr(kv_lens), _ptr(q_starts), _ptr(sinks), _ptr(out), _ptr(lse),
-              float(D ** -0.5 if scale is None else scale), batch, T, Hq, cols, int(max_q), int(max_kv),
-              int(bool(causal)), int(window))
-    cfg = cache.cfg if out.dtype == torch.bfloat16 else _with_dtypes(cache.cfg, output_dtype="fp32")
-    need = lib().fp4q_attn_workspace_bytes(ct.byref(cfg), ct.byref(cache._c), ct.byref(a))
-    if need and workspace is None:
-        workspace = _held_on(_empty(need, torch.uint8, dev), stream)
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().fp4_attn(ct.byref(cfg), ct.byref(cache._c), ct.byref(a), _ptr(workspace), size, _stream(stream)),
-           "fp4_attn")
+    a = ct.byref(_Attn(q.data_ptr(), ld, page_table.data_ptr(), kv_lens.data_ptr(),
+                       None if q_starts is None else q_starts.data_ptr(), None if sinks is None else sinks.data_ptr(),
+                       out.data_ptr(), None if lse is None else lse.data_ptr(),
+                       D ** -0.5 if scale is None else scale, batch, T, Hq, cols, max_q, max_kv, 1 if causal else 0,
+                       window))
+    if workspace is None:
+        need = lib().fp4q_attn_workspace_bytes(cfg, cache._ref, a)
+        if need:
+            workspace = _held_on(_empty(need, torch.uint8, dev), stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
+    _check(lib().fp4_attn(cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev)), "fp4_attn")
     return (out, lse) if with_lse else out
 
 
