@@ -17,7 +17,7 @@ __all__ = [
     "Fp4Error", "Cfg", "Sizes", "make_cfg", "lib", "fp4q_abi_version", "fp4q_status_str", "fp4q_buffer_sizes",
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
-    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "KVCache", "fp4_kv_append",
+    "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "fp4q_linear_workspace_bytes", "KVCache", "fp4_kv_append",
     "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "LIB_PATH",
 ]
 
@@ -145,7 +145,9 @@ def lib():
         L.fp4_attn.restype = ct.c_int
         L.fp4_attn.argtypes = [C, KV, AT, P, SZ, P]
         L.fp4_linear.restype = ct.c_int
-        L.fp4_linear.argtypes = [C, P, I64, I64, P, P, P, ct.c_int32, I64, I64, P, I64, P]
+        L.fp4_linear.argtypes = [C, P, I64, I64, P, P, P, ct.c_int32, I64, I64, P, I64, P, SZ, P]
+        L.fp4q_linear_workspace_bytes.restype = SZ
+        L.fp4q_linear_workspace_bytes.argtypes = [I64, I64, I64]
         if L.fp4q_abi_version() != ABI_VERSION:
             raise ImportError("libfp4q.so ABI %d, binding expects %d" % (L.fp4q_abi_version(), ABI_VERSION))
         _lib = L
@@ -536,7 +538,11 @@ def fp4_mm(a, b, cfg=None, *, out_dtype=None, c=None, stream=None):
     return c
 
 
-def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, stream=None):
+def fp4q_linear_workspace_bytes(M, N, K):
+    return lib().fp4q_linear_workspace_bytes(int(M), int(N), int(K))
+
+
+def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, workspace=None, stream=None):
     """y = x @ W^T with bf16 x [M, K] (a view with a row pitch is accepted) and a
     4-bit W [N, K] given as {"codes", "scales", "outer"} in cfg's format, as fp4_quantize
     returns it (or the row_* buffers of fp4_cast_transpose under those names).
@@ -544,7 +550,9 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, str
     The gradient of x is the same product over the columnwise buffers: with
     w = {"codes": col_codes [K, N / 2], "scales": col_scales, "outer": ...} and dy [M, N] in
     x's place it returns dy @ W [M, K]; a 2D outer array is passed as it is, with
-    outer_transposed=True.  y is bf16 unless out_dtype (or a given y) is float32."""
+    outer_transposed=True.  y is bf16 unless out_dtype (or a given y) is float32.
+    workspace: a tensor of at least fp4q_linear_workspace_bytes(M, N, K) bytes, else one is
+    allocated where it is needed."""
     torch = _torch()
     codes, scales, outer = w["codes"], w["scales"], w.get("outer")
     if x.dtype != torch.bfloat16:
@@ -575,10 +583,17 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, str
         raise ValueError("y must be a [%d, %d] view with contiguous rows on %s" % (M, N, dev))
     if y.dtype not in (torch.bfloat16, torch.float32):
         raise Fp4Error(ERR_DTYPE, "y dtype %s" % y.dtype)
+    if workspace is None:
+        need = lib().fp4q_linear_workspace_bytes(M, N, K)
+        if need:
+            workspace = _held_on(_empty(need, torch.uint8, dev), stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % dev)
+    size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
     ycfg = _with_dtypes(cfg, "bf16", _dtype_name(y))
     _check(lib().fp4_linear(ct.byref(ycfg), x.data_ptr(), M, x.stride(0) if M > 1 else K, codes.data_ptr(),
                             scales.data_ptr(), None if outer is None else outer.data_ptr(), 1 if outer_transposed else 0, N,
-                            K, y.data_ptr(), y.stride(0) if M > 1 else N, _raw_stream(stream, dev)), "fp4_linear")
+                            K, y.data_ptr(), y.stride(0) if M > 1 else N, scratch, size, _raw_stream(stream, dev)), "fp4_linear")
     return y
 
 

@@ -881,32 +881,43 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     return hip_status(launch_attn(r.bias, a, (hipStream_t)stream));
 }
 
+size_t fp4q_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M > ((int64_t)1 << 20) || N > ((int64_t)1 << 24) || K > ((int64_t)1 << 22)) return 0;
+    return plan_linear(M, N, K).bytes;
+}
+
 int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, const uint8_t* codes,
                const uint8_t* scales, const float* outer, int32_t outer_transposed, int64_t N, int64_t K, void* y,
-               int64_t ld_y, void* stream)
+               int64_t ld_y, void* workspace, size_t workspace_bytes, void* stream)
 {
     Resolved r;
     int st = resolve(cfg, r);
     if (st) return st;
     if (r.x_f32) return FP4Q_ERR_UNSUPPORTED;
     if (outer_transposed != 0 && outer_transposed != 1) return FP4Q_ERR_MODE;
-    if (outer_transposed && r.outer_kind != kOuter2D && r.outer_kind != kOuterNone && r.outer_kind != kOuterTensor)
-        return FP4Q_ERR_MODE;
+    if (outer_transposed && r.outer_kind == kOuter1D) return FP4Q_ERR_MODE;
     if (M < 0 || N < 0 || K < 0 || K % 32) return FP4Q_ERR_SHAPE;
-    if (M > 1 && ld_x < K) return FP4Q_ERR_SHAPE;
-    if (M > 1 && ld_y < N) return FP4Q_ERR_SHAPE;
+    if (M > 1 && (ld_x < K || ld_y < N)) return FP4Q_ERR_SHAPE;
     if (r.obs && (K % r.obs || (r.outer_kind == kOuter2D && N % r.obs))) return FP4Q_ERR_SHAPE;
     if ((r.outer_kind == kOuter2D && r.obs != 64) || (r.outer_kind == kOuter1D && r.obs % 64)) return FP4Q_ERR_UNSUPPORTED;
     if (K > ((int64_t)1 << 22) || M > ((int64_t)1 << 20) || N > ((int64_t)1 << 24)) return FP4Q_ERR_UNSUPPORTED;
+    // 32-bit byte offsets within a tile of x (64 rows) and within the outer scales
+    if (M > 1 && ld_x > ((int64_t)1 << 23)) return FP4Q_ERR_UNSUPPORTED;
+    if ((r.outer_kind == kOuter1D ? N * (K / r.obs) : r.outer_kind == kOuter2D ? (N / 64) * (K / 64) : 0) >= (int64_t)1 << 29)
+        return FP4Q_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return FP4Q_OK;
     if (!y || (K > 0 && (!x || !codes || !scales))) return FP4Q_ERR_NULL;
     if (K > 0 && r.outer_kind != kOuterNone && !outer) return FP4Q_ERR_NULL;
-    if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(outer, 4) || misaligned(y, r.y_f32 ? 4 : 2) ||
-        (M > 1 && K > 0 && ld_x % 8))
+    if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(outer, 4) ||
+        misaligned(y, r.y_f32 ? 4 : 2) || (M > 1 && K > 0 && ld_x % 8))
         return FP4Q_ERR_ALIGN;
+    const LinearPlan p = plan_linear(M, N, K);
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return FP4Q_ERR_WORKSPACE;
+    if (p.bytes > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
     LinearArgs a;
     a.x = x;
-    a.ld_x = ld_x;
+    a.ld_x = M > 1 ? ld_x : 0;
     a.codes = codes;
     a.scales = scales;
     a.outer_kind = K > 0 ? r.outer_kind : kOuterNone;
@@ -926,6 +937,10 @@ int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, 
     a.y_f32 = r.y_f32 ? 1 : 0;
     a.y = y;
     a.ld_y = ld_y;
+    a.y_vec = !misaligned(y, r.y_f32 ? 16 : 8) && (M == 1 || ld_y % 4 == 0) ? 1 : 0;
+    a.splits = p.splits;
+    a.parts = p.bytes > 0 ? (float*)workspace : nullptr;
+    a.parts_ld = p.ld;
     return hip_status(launch_linear(r.bias, a, (hipStream_t)stream));
 }
 

@@ -36,6 +36,7 @@
 #include "fp4q_device.h"
 #include "kv_index.h"
 #include "launch.h"
+#include "lds_load.h"
 #include "mfma16.h"
 
 namespace fp4q {
@@ -52,40 +53,6 @@ constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
 constexpr float kLazy = 8.0f;
-
-// Loads of 16 bytes a lane straight to LDS at a wave-uniform base (lane l's go to base
-// + 16 l), from per-lane addresses or through a descriptor.  They are written out, with the
-// waits below, because the compiler's own waits cannot tell stages apart and would
-// wait for every outstanding load before any read of LDS.  No other instruction
-// here reads m0, so the reserved-register clobber warning is silenced.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_load(const void* p, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(p), "s"(base) : "memory", "m0");
-}
-
-__device__ __forceinline__ void lds_load(rsrc_t r, uint32_t off, uint32_t base)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen nt lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// Waits until at most N vector-memory operations of the wave are outstanding; no read of
-// LDS moves above it.
-template <int N>
-__device__ __forceinline__ void wait_loads()
-{
-    static_assert(N >= 0 && N < 64, "the counter holds 63");
-    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
-}
-
-typedef __attribute__((address_space(3))) unsigned char lds_t;
-
-__device__ __forceinline__ uint32_t lds_address(const lds_t* p)
-{
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
-}
 
 // A group's rows through a buffer descriptor in scalar registers: a lane's offsets are the
 // same for every group, so a load takes no address arithmetic on lanes.

@@ -14,6 +14,7 @@
 // are joined through LDS in a fixed order.
 #include "fp4q_device.h"
 #include "launch.h"
+#include "lds_load.h"
 #include "mfma16.h"
 
 namespace fp4q {
@@ -23,6 +24,31 @@ namespace {
 // Outer scales inside the sum: none (or one for the tensor, applied to y), per
 // 64 rows (2D) or per row (1D).
 enum { kInnerOnly = 0, kPerTile = 1, kPerRow = 2 };
+
+// Values c .. c + 3 of row r of y.
+__device__ __forceinline__ void store4(const LinearArgs& a, int64_t r, int c, f32x4_t v)
+{
+    const int64_t at = r * a.ld_y + c;
+    if (a.y_f32) {
+        float* y = (float*)a.y + at;
+        if (a.y_vec && c + 4 <= a.N) {
+            *(f32x4_t*)y = v;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < a.N) y[i] = v[i];
+    } else {
+        uint16_t* y = (uint16_t*)a.y + at;
+        if (a.y_vec && c + 4 <= a.N) {
+            *(uint2*)y = make_uint2(Dec<0>::round2(v[0], v[1]), Dec<0>::round2(v[2], v[3]));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < a.N) y[i] = (uint16_t)Dec<0>::round2(v[i], 0.0f);
+    }
+}
 
 constexpr int kPair = 128;                               // values of K of a pair of steps
 
@@ -154,35 +180,234 @@ __global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
         if (!live[m]) continue;
-        const int64_t at = (int64_t)(m0 + 16 * m + row) * a.ld_y;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = n0 + 16 * n + 4 * quarter + r;
-                const float v = acc[m][n][r] * whole;
-                if (c >= a.N) continue;
-                if (a.y_f32) ((float*)a.y)[at + c] = v;
-                else ((uint16_t*)a.y)[at + c] = (uint16_t)f32_to_bf16(v);
-            }
+        for (int n = 0; n < NT; ++n) store4(a, m0 + 16 * m + row, n0 + 16 * n + 4 * quarter, acc[m][n] * whole);
     }
 }
 
-template <int BIAS, int MT, int NT, int OUTER>
-void launch_tile(const LinearArgs& a, hipStream_t s)
+// ---------------------------------------------------------------- tiles
+// Larger work: a workgroup of eight waves takes 16 MT rows of x and 128 rows of W, 128
+// values of K at a time through a ring of LDS stages filled by direct loads:
+//   x       [16 MT][128] bf16, a row's sixteen 16-byte chunks at chunk ^ (row % 16),
+//   codes   [128][64 bytes], a row's four chunks at chunk ^ (row / 2 % 2 * 2),
+//   scales  [128][8 or 4], a word each (rows of scale bytes have any alignment: 90 bytes for
+//           MXFP4 and K = 2880), outer scales [2][128] FP32 (per 64 values of K).
+// Wave w takes W's rows 32 (w % 4) .. + 31 and the stage's 64 values of K from 64 (w / 4);
+// the two halves join through LDS.  So x is read from the caches once for 128 rows of W and
+// a row of W is decoded once for 16 MT rows of x.  Few tiles: the stages are split
+// over workgroups, whose binary32 sums k_linear_join adds in order.
+constexpr int kTileN = 128, kStageK = 128;
+constexpr int64_t kSmallWeight = (int64_t)1 << 24;
+
+template <int BIAS, int MT, bool OUTER>
+struct Tile {
+    static constexpr int B = Dec<BIAS>::kBlock;
+    static constexpr int kX = 16 * MT * kStageK * 2, kC = kTileN * kStageK / 2, kS = kTileN * kStageK / B * 4;
+    static constexpr int kO = OUTER ? 2 * kTileN * 4 : 0;
+    static constexpr int kStage = kX + kC + kS + kO;
+    static constexpr int kDepth = MT == 4 ? 3 : MT == 2 ? 4 : 5;
+    static constexpr int kXLoads = MT >= 2 ? MT / 2 : 1;   // of a wave; MT 1: four waves take none
+    static constexpr int kSLoads = kTileN * kStageK / B / 512;
+    static constexpr int kLds = kDepth * kStage;
+};
+
+template <int BIAS, int MT, bool OUTER>
+__global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
 {
-    constexpr int KS = MT * NT >= 8 ? 4 : 8;
-    const dim3 grid((uint32_t)((a.N + 16 * NT - 1) / (16 * NT)), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL((k_linear<BIAS, MT, NT, OUTER, KS>), grid, dim3(64 * KS), 0, s, a);
+    using T = Tile<BIAS, MT, OUTER>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    lds_t* const lds = (lds_t*)smem;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wn = wave & 3, half = wave >> 2;
+    const int row = lane & 15, quarter = lane >> 4;
+    const int n0 = (int)blockIdx.x * kTileN, m0 = (int)blockIdx.y * (16 * MT);
+    const int stages = (a.K + kStageK - 1) / kStageK;
+    const int s0 = (int)((int64_t)stages * blockIdx.z / gridDim.z), s1 = (int)((int64_t)stages * (blockIdx.z + 1) / gridDim.z);
+
+    // Descriptors from the tile's first rows; rows beyond M or N repeat the last one
+    // (their results are not stored), values beyond K load as zeros.
+    const rsrc_t xr = make_rsrc(a.x + (int64_t)m0 * a.ld_x), cr = make_rsrc(a.codes + (int64_t)n0 * (a.K / 2));
+    const rsrc_t sr = make_rsrc(a.scales + (int64_t)n0 * (a.K / T::B));
+    const int last_m = a.M - 1 - m0, last_n = a.N - 1 - n0;
+
+    auto issue = [&](int s, int slot) {
+        const uint32_t to = lds_address(lds + slot * T::kStage);
+        const int k0 = s * kStageK;
+#pragma unroll
+        for (int j = 0; j < T::kXLoads; ++j) {           // four rows of x a load
+            const int piece = wave * T::kXLoads + j;
+            const int r = 4 * piece + (lane >> 4), c = (lane & 15) ^ (r & 15);
+            const int k = k0 + 8 * c;
+            const uint32_t off = k < a.K ? (uint32_t)(min(r, last_m) * (int)a.ld_x + k) * 2 : kOff;
+            if (MT > 1 || wave < 4) lds_load_kept(xr, off, to + piece * 1024);
+        }
+        {                                                // sixteen rows of codes a load
+            const int r = 16 * wave + (lane >> 2), c = (lane & 3) ^ (r & 2);
+            const int k = k0 + 32 * c;
+            lds_load(cr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / 2) + k / 2) : kOff, to + T::kX + wave * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < T::kSLoads; ++j) {           // eight or sixteen rows of scales a load
+            constexpr int kPer = kStageK / T::B;
+            const int piece = wave * T::kSLoads + j;
+            const int r = piece * (64 / kPer) + lane / kPer, k = k0 + lane % kPer * T::B;
+            lds_load1(sr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / T::B) + k / T::B) : kOff,
+                      to + T::kX + T::kC + piece * 256);
+        }
+        if constexpr (OUTER) {                           // the wave's own 32 rows and half
+            const int r = 32 * wn + lane, k = k0 + 64 * half;
+            const int64_t n = min(n0 + r, a.N - 1);
+            const uint32_t at = (uint32_t)((a.outer_kind == kOuter2D ? n >> 6 : n) * a.outer_n + k / a.obs * a.outer_k) * 4;
+            if (lane < 32)
+                lds_load4(make_rsrc(a.outer), k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + (half * kTileN + 32 * wn) * 4);
+        }
+    };
+    constexpr int kLoads = T::kXLoads + 1 + T::kSLoads + (OUTER ? 1 : 0);
+    // waves that load no x wait for one load less a stage
+    const auto wait_stage = [&](bool more) {
+        if (!more) wait_loads<0>();
+        else if (MT == 1 && wave >= 4) wait_loads<(T::kDepth - 2) * (kLoads - 1)>();
+        else wait_loads<(T::kDepth - 2) * kLoads>();
+    };
+
+    f32x4_t acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4_t{0, 0, 0, 0};
+
+#pragma unroll
+    for (int i = 0; i < T::kDepth - 1; ++i)
+        if (s0 + i < s1) issue(s0 + i, i);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        // this wave's loads of the stage have landed; the barrier makes everybody's visible, and
+        // says that the stage before, whose place is filled next, has been read
+        wait_stage(s + T::kDepth - 2 < s1);
+        lds_barrier();
+        const int free = slot == 0 ? T::kDepth - 1 : slot - 1;
+        if (s + T::kDepth - 1 < s1) issue(s + T::kDepth - 1, free);
+        const lds_t* const x = lds + slot * T::kStage;
+        const lds_t* const c = x + T::kX;
+        slot = slot + 1 == T::kDepth ? 0 : slot + 1;
+
+        uint4 w[2][2];
+        f32x4_t so[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int r = 32 * wn + 16 * n + row;
+            const int chunk = (2 * half + (quarter >> 1)) ^ (r & 2);
+            const u32x2_t code = *(const __attribute__((address_space(3))) u32x2_t*)(c + r * 64 + chunk * 16 + (quarter & 1) * 8);
+            const float sc = DecBf16<BIAS>::scale(
+                *(const __attribute__((address_space(3))) uint32_t*)(c + T::kC +
+                                                                      (r * (kStageK / T::B) + (64 * half + 16 * quarter) / T::B) * 4));
+            w[n][0] = DecBf16<BIAS>::octet(code[0], sc);
+            w[n][1] = DecBf16<BIAS>::octet(code[1], sc);
+            if constexpr (OUTER)
+                so[n] = *(const __attribute__((address_space(3))) f32x4_t*)(c + T::kC + T::kS +
+                                                                             (half * kTileN + 32 * wn + 16 * n + 4 * quarter) * 4);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint4 v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int chunk = (8 * half + 2 * quarter + i) ^ row;
+                const u32x4_t u = *(const __attribute__((address_space(3))) u32x4_t*)(x + (16 * m + row) * 256 + chunk * 16);
+                v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                f32x4_t p = OUTER ? f32x4_t{0, 0, 0, 0} : acc[m][n];
+                p = Dec<0>::mfma(w[n][0], v[0], p);
+                p = Dec<0>::mfma(w[n][1], v[1], p);
+                if constexpr (OUTER) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[m][n][r] = __builtin_fmaf(p[r], so[n][r], acc[m][n][r]);
+                } else {
+                    acc[m][n] = p;
+                }
+            }
+        }
+    }
+
+    // the second half of K joins the first
+    __syncthreads();
+    float* const join = reinterpret_cast<float*>(smem) + wn * (MT * 8 * 64) + lane;
+    if (half == 1) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) join[(m * 8 + i) * 64] = acc[m][i >> 2][i & 3];
+    }
+    __syncthreads();
+    if (half == 1) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] += join[(m * 8 + i) * 64];
+
+    const float whole = a.outer_kind == kOuterTensor && a.parts == nullptr ? a.outer[0] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int64_t r = m0 + 16 * m + row;
+        if (r >= a.M) continue;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int c = n0 + 32 * wn + 16 * n + 4 * quarter;
+            if (a.parts) {
+                *(float4*)(a.parts + (blockIdx.z * (int64_t)a.M + r) * a.parts_ld + c) =
+                    make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] *= whole;
+            store4(a, r, c, acc[m][n]);
+        }
+    }
+}
+
+// Adds the splits' sums in order: four values of a row a lane.
+__global__ __launch_bounds__(256) void k_linear_join(LinearArgs a)
+{
+    const int64_t quads = a.parts_ld / 4;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= quads * a.M) return;
+    const int64_t r = at / quads;
+    const int c = (int)(at - r * quads) * 4;
+    const float* p = a.parts + r * a.parts_ld + c;
+    f32x4_t sum = {0, 0, 0, 0};
+    for (int s = 0; s < a.splits; ++s) sum += *(const f32x4_t*)(p + s * (int64_t)a.M * a.parts_ld);
+    if (a.outer_kind == kOuterTensor) sum *= a.outer[0];
+    store4(a, r, c, sum);
+}
+
+template <int BIAS, int MT, bool OUTER>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t s)
+{
+    using T = Tile<BIAS, MT, OUTER>;
+    static_assert(T::kLds >= 4 * MT * 8 * 64 * 4, "the halves join in the ring's place");
+    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_linear_tile<BIAS, MT, OUTER>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    if (allowed != hipSuccess) return allowed;
+    const dim3 grid((uint32_t)((a.N + kTileN - 1) / kTileN), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)), (uint32_t)a.splits);
+    hipLaunchKernelGGL((k_linear_tile<BIAS, MT, OUTER>), grid, dim3(512), T::kLds, s, a);
+    if (a.parts) {
+        const int64_t quads = a.parts_ld / 4 * a.M;
+        hipLaunchKernelGGL(k_linear_join, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
 }
 
 template <int BIAS, int OUTER>
 hipError_t launch_outer(const LinearArgs& a, hipStream_t s)
 {
-    if (a.M <= 16) launch_tile<BIAS, 1, 1, OUTER>(a, s);
-    else if (a.M <= 32) launch_tile<BIAS, 2, 2, OUTER>(a, s);
-    else launch_tile<BIAS, 4, 2, OUTER>(a, s);
-    return hipGetLastError();
+    if (a.splits == 0) {
+        hipLaunchKernelGGL((k_linear<BIAS, 1, 1, OUTER, 8>), dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)),
+                           dim3(512), 0, s, a);
+        return hipGetLastError();
+    }
+    if (a.M <= 16) return launch_tile<BIAS, 1, OUTER != kInnerOnly>(a, s);
+    if (a.M <= 32) return launch_tile<BIAS, 2, OUTER != kInnerOnly>(a, s);
+    return launch_tile<BIAS, 4, OUTER != kInnerOnly>(a, s);
 }
 
 template <int BIAS>
@@ -196,6 +421,24 @@ hipError_t launch_bias(const LinearArgs& a, hipStream_t s)
 }
 
 }  // namespace
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K)
+{
+    LinearPlan p{0, 0, 0};
+    // small weights under few rows: one launch without parts
+    if (M <= 16 && N * K <= kSmallWeight) return p;
+    const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int64_t blocks = (N + kTileN - 1) / kTileN * ((M + rows - 1) / rows);
+    const int64_t stages = (K + kStageK - 1) / kStageK;
+    int64_t want = 512 / blocks;                         // two workgroups a compute unit
+    if (want > stages / 4) want = stages / 4;
+    p.splits = want < 1 ? 1 : (int32_t)want;
+    if (p.splits > 1) {
+        p.ld = (N + kTileN - 1) / kTileN * kTileN;
+        p.bytes = (size_t)p.splits * M * p.ld * sizeof(float);
+    }
+    return p;
+}
 
 hipError_t launch_linear(int bias, const LinearArgs& a, hipStream_t s)
 {

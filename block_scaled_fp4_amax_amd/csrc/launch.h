@@ -282,8 +282,19 @@ struct LinearArgs {
     int32_t y_f32;
     void* y;                   // bf16 or FP32 [M, ld_y]
     int64_t ld_y;
+    int32_t y_vec;             // 1: four values of y at a multiple of four are aligned together
+    int32_t splits;            // 0: small weights; else parts of K over workgroups
+    float* parts;              // FP32 [splits][M][parts_ld], null with one part
+    int64_t parts_ld;
 };
 
+struct LinearPlan {
+    int32_t splits;
+    int64_t ld;
+    size_t bytes;
+};
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(int bias, const LinearArgs& a, hipStream_t s);
 
 // partial maxima used by the tensorwise amax pass

@@ -418,18 +418,21 @@ int fp4_mx_scales_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t*
  *            place) the same call is dx = dy W; a 2D outer array then belongs to the
  *            transpose and outer_transposed is 1 (as in fp4_dequantize).
  *   y        bf16 or FP32 (cfg->output_dtype) [M, ld_y] device (ld_y >= N), written.
+ *   workspace  fp4q_linear_workspace_bytes() bytes (0 unless K is split over
+ *            workgroups), 16-byte aligned; no initial value, nothing kept.
  * W enters the products exactly as codes times inner scales, in bf16; sums are
  * binary32, and an outer scale multiplies the binary32 sum of the values that it
  * covers: |y - exact| <= (K + K / 64 + 2) 2^-24 sum_k |x_k w_k| (plus y's rounding).
  * The order of a sum depends on M, N and K alone, so equal calls give equal bits.
  * Needs K % 32 == 0 (FP4Q_ERR_SHAPE); 1D outer blocks of a multiple of 64 and
- * 2D ones of 64 (others: FP4Q_ERR_UNSUPPORTED); K <= 2^22, M <= 2^20 and N <= 2^24.
- * K == 0 writes zeros.  rounding, outer_mode, seed, step and index_base are ignored, and so
+ * 2D ones of 64 (others: FP4Q_ERR_UNSUPPORTED); K <= 2^22, M <= 2^20, N <= 2^24,
+ * ld_x <= 2^23 and fewer than 2^29 outer scales.  K == 0 writes zeros.  rounding, outer_mode, seed, step and index_base are ignored, and so
  * is inner_2d (see fp4_dequantize).
  */
+size_t fp4q_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, const uint8_t* codes,
                const uint8_t* scales, const float* outer, int32_t outer_transposed, int64_t N, int64_t K, void* y,
-               int64_t ld_y, void* stream);
+               int64_t ld_y, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The paged 4-bit cache of keys and values, for decoding with attention.

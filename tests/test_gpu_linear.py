@@ -100,6 +100,22 @@ def test_long_rows(M):
         check(fq.fp4_linear(x.cuda(), w, cfg, out_dtype=torch.float32), x, wd, 14592)
 
 
+@pytest.mark.parametrize("M", [1, 16, 31, 64, 100])
+@pytest.mark.parametrize("fmt,kind", [("mxfp4", "none"), ("nvfp4", "2d"), ("nvfp4", "1d128"), ("amdfp4", "tensor")])
+def test_large_weights(fmt, kind, M):
+    """Weights that are cut into tiles and split along K, with tails of N and K."""
+    rng = np.random.default_rng(M)
+    N, K = (4224, 4096 + 128) if kind in ("2d", "1d128") else (4201, 4096 + 96)
+    w, wd, cfg = weight(rng, fmt, kind, N, K)
+    x = activations(rng, M, K)
+    y = fq.fp4_linear(x.cuda(), w, cfg, out_dtype=torch.float32)
+    check(y, x, wd, K)
+    need = fq.fp4q_linear_workspace_bytes(M, N, K)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(fq.fp4_linear(x.cuda(), w, cfg, out_dtype=torch.float32, workspace=ws), y)
+
+
 def test_pitched_views_and_untouched_padding():
     rng = np.random.default_rng(1)
     w, wd, cfg = weight(rng, "nvfp4", "none", 50, 96)

@@ -144,9 +144,10 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
                    v_outer=torch.ones(2))
 
 
-def linear(cfg=None, x=FAKE, M=3, ld_x=128, codes=FAKE, scales=FAKE, outer=None, t=0, N=64, K=128, y=FAKE, ld_y=64):
+def linear(cfg=None, x=FAKE, M=3, ld_x=128, codes=FAKE, scales=FAKE, outer=None, t=0, N=64, K=128, y=FAKE, ld_y=64, ws=None, wsb=0):
     cfg = cfg if cfg is not None else fq.make_cfg()
-    return status(fq.lib().fp4_linear(ct.byref(cfg), x, M, ld_x, codes, scales, outer, t, N, K, y, ld_y, None))
+    return status(fq.lib().fp4_linear(ct.byref(cfg), x, M, ld_x, codes, scales, outer, t, N, K, y, ld_y, ws, wsb,
+                                         None))
 
 
 @no_gpu
@@ -173,6 +174,12 @@ def test_linear_rules():
         assert linear(**{n: MIS}) == fq.ERR_ALIGN
     assert linear(y=FAKE + 1) == fq.ERR_ALIGN and linear(ld_x=132) == fq.ERR_ALIGN
     assert linear(cfg=C(two_level="tensorwise"), outer=FAKE + 2) == fq.ERR_ALIGN
+    assert linear(ld_x=(1 << 23) + 8) == fq.ERR_UNSUPPORTED
+    big = dict(M=40, N=256, K=8192, ld_x=8192, ld_y=256)
+    need = fq.fp4q_linear_workspace_bytes(40, 256, 8192)
+    assert need > 0 and linear(**big) == fq.ERR_WORKSPACE and linear(ws=FAKE, wsb=need - 1, **big) == fq.ERR_WORKSPACE
+    assert linear(ws=MIS, wsb=need, **big) == fq.ERR_ALIGN
+    assert fq.fp4q_linear_workspace_bytes(-1, 256, 8192) == 0
     assert linear(M=0, x=None, y=None) == fq.OK and linear(N=0, codes=None, y=None) == fq.OK
 
 
