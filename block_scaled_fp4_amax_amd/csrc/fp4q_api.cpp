@@ -910,7 +910,7 @@ int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, 
     if (!y || (K > 0 && (!x || !codes || !scales))) return FP4Q_ERR_NULL;
     if (K > 0 && r.outer_kind != kOuterNone && !outer) return FP4Q_ERR_NULL;
     if (misaligned(x, 16) || misaligned(codes, 16) || misaligned(outer, 4) ||
-        misaligned(y, r.y_f32 ? 4 : 2) || (M > 1 && K > 0 && ld_x % 8))
+        (r.fmt != FP4Q_MXFP4 && misaligned(scales, 2)) || misaligned(y, r.y_f32 ? 4 : 2) || (M > 1 && K > 0 && ld_x % 8))
         return FP4Q_ERR_ALIGN;
     const LinearPlan p = plan_linear(M, N, K);
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return FP4Q_ERR_WORKSPACE;

@@ -21,6 +21,8 @@ namespace fp4q {
 
 namespace {
 
+#define LDS_PTR(t) __attribute__((address_space(3))) t*
+
 // Outer scales inside the sum: none (or one for the tensor, applied to y), per
 // 64 rows (2D) or per row (1D).
 enum { kInnerOnly = 0, kPerTile = 1, kPerRow = 2 };
@@ -50,6 +52,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t r, int c, f3
     }
 }
 
+constexpr int64_t kSmallWeight = (int64_t)1 << 24;
 constexpr int kPair = 128;                               // values of K of a pair of steps
 
 template <int BIAS, int NT>
@@ -186,29 +189,34 @@ __global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
 }
 
 // ---------------------------------------------------------------- tiles
-// Larger work: a workgroup of eight waves takes 16 MT rows of x and 128 rows of W, 128
+// Larger work: a workgroup of eight waves takes 16 MT rows of x and 32 kWN rows of W, 256
 // values of K at a time through a ring of LDS stages filled by direct loads:
-//   x       [16 MT][128] bf16, a row's sixteen 16-byte chunks at chunk ^ (row % 16),
-//   codes   [128][64 bytes], a row's four chunks at chunk ^ (row / 2 % 2 * 2),
-//   scales  [128][8 or 4], a word each (rows of scale bytes have any alignment: 90 bytes for
-//           MXFP4 and K = 2880), outer scales [2][128] FP32 (per 64 values of K).
-// Wave w takes W's rows 32 (w % 4) .. + 31 and the stage's 64 values of K from 64 (w / 4);
-// the two halves join through LDS.  So x is read from the caches once for 128 rows of W and
-// a row of W is decoded once for 16 MT rows of x.  Few tiles: the stages are split
-// over workgroups, whose binary32 sums k_linear_join adds in order.
-constexpr int kTileN = 128, kStageK = 128;
-constexpr int64_t kSmallWeight = (int64_t)1 << 24;
+//   x       [16 MT][256] bf16, a row's 32 chunks of 16 bytes at chunk ^ (row % 16),
+//   codes   [32 kWN][128 bytes], a row's eight chunks at chunk ^ (row / 2 % 4 * 2),
+//   scales  [32 kWN][8], a word for 32 values of K (one byte of MXFP4, two of the
+//           others: rows of scale bytes have no better alignment, 90 bytes for
+//           MXFP4 and K = 2880),
+//   outer scales [4][32 kWN] FP32, per 64 values of K.
+// Wave w takes W's rows 32 (w % kWN) .. + 31 and the (w / kWN)-th part of the stage's K;
+// the parts join through LDS.  So a workgroup reads x from the caches once for
+// 32 kWN rows of W, and a row of W is decoded once for 16 MT rows of x: with eight tiles the
+// matrix instructions take as long as the decoding.  Few tiles: the stages are split over
+// workgroups, whose binary32 sums k_linear_join adds in order.
+constexpr int kStageK = 256;
 
 template <int BIAS, int MT, bool OUTER>
 struct Tile {
     static constexpr int B = Dec<BIAS>::kBlock;
-    static constexpr int kX = 16 * MT * kStageK * 2, kC = kTileN * kStageK / 2, kS = kTileN * kStageK / B * 4;
-    static constexpr int kO = OUTER ? 2 * kTileN * 4 : 0;
+    static constexpr int kWN = MT == 8 ? 2 : 4, kWK = 8 / kWN;   // waves along W's rows and along K
+    static constexpr int kN = 32 * kWN;
+    static constexpr int kSteps = kStageK / kWK / 64;    // of 64 values of K, of a wave and stage
+    static constexpr int kX = 16 * MT * kStageK * 2, kC = kN * kStageK / 2, kS = kN * 8 * 4, kO = OUTER ? 4 * kN * 4 : 0;
     static constexpr int kStage = kX + kC + kS + kO;
-    static constexpr int kDepth = MT == 4 ? 3 : MT == 2 ? 4 : 5;
-    static constexpr int kXLoads = MT >= 2 ? MT / 2 : 1;   // of a wave; MT 1: four waves take none
-    static constexpr int kSLoads = kTileN * kStageK / B / 512;
+    // one workgroup fills a compute unit's LDS
+    static constexpr int kDepth = 160 * 1024 / kStage < 4 ? 160 * 1024 / kStage : 4;
     static constexpr int kLds = kDepth * kStage;
+    static constexpr int kLoads = MT + kN / 64 + kN / 64 + (OUTER ? 1 : 0);   // of a wave and stage
+    static_assert(kDepth >= 2 && kLds >= (kWK - 1) * kWN * MT * 8 * 64 * 4, "two stages; the parts join in their place");
 };
 
 template <int BIAS, int MT, bool OUTER>
@@ -218,9 +226,9 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
     extern __shared__ __align__(16) unsigned char smem[];
     lds_t* const lds = (lds_t*)smem;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int wn = wave & 3, half = wave >> 2;
+    const int wn = wave % T::kWN, wk = wave / T::kWN;
     const int row = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * kTileN, m0 = (int)blockIdx.y * (16 * MT);
+    const int n0 = (int)blockIdx.x * T::kN, m0 = (int)blockIdx.y * (16 * MT);
     const int stages = (a.K + kStageK - 1) / kStageK;
     const int s0 = (int)((int64_t)stages * blockIdx.z / gridDim.z), s1 = (int)((int64_t)stages * (blockIdx.z + 1) / gridDim.z);
 
@@ -234,40 +242,32 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
         const uint32_t to = lds_address(lds + slot * T::kStage);
         const int k0 = s * kStageK;
 #pragma unroll
-        for (int j = 0; j < T::kXLoads; ++j) {           // four rows of x a load
-            const int piece = wave * T::kXLoads + j;
-            const int r = 4 * piece + (lane >> 4), c = (lane & 15) ^ (r & 15);
-            const int k = k0 + 8 * c;
-            const uint32_t off = k < a.K ? (uint32_t)(min(r, last_m) * (int)a.ld_x + k) * 2 : kOff;
-            if (MT > 1 || wave < 4) lds_load_kept(xr, off, to + piece * 1024);
-        }
-        {                                                // sixteen rows of codes a load
-            const int r = 16 * wave + (lane >> 2), c = (lane & 3) ^ (r & 2);
-            const int k = k0 + 32 * c;
-            lds_load(cr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / 2) + k / 2) : kOff, to + T::kX + wave * 1024);
+        for (int j = 0; j < MT; ++j) {                   // two rows of x a load
+            const int piece = wave * MT + j, r = 2 * piece + (lane >> 5);
+            const int k = k0 + 8 * ((lane & 31) ^ (r & 15));
+            lds_load_kept(xr, k < a.K ? (uint32_t)(min(r, last_m) * (int)a.ld_x + k) * 2 : kOff, to + piece * 1024);
         }
 #pragma unroll
-        for (int j = 0; j < T::kSLoads; ++j) {           // eight or sixteen rows of scales a load
-            constexpr int kPer = kStageK / T::B;
-            const int piece = wave * T::kSLoads + j;
-            const int r = piece * (64 / kPer) + lane / kPer, k = k0 + lane % kPer * T::B;
-            lds_load1(sr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / T::B) + k / T::B) : kOff,
-                      to + T::kX + T::kC + piece * 256);
+        for (int j = 0; j < T::kN / 64; ++j) {           // eight rows of codes a load
+            const int piece = wave * (T::kN / 64) + j, r = 8 * piece + (lane >> 3);
+            const int k = k0 + 32 * ((lane & 7) ^ (r & 6));
+            lds_load_kept(cr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / 2) + k / 2) : kOff, to + T::kX + piece * 1024);
         }
-        if constexpr (OUTER) {                           // the wave's own 32 rows and half
-            const int r = 32 * wn + lane, k = k0 + 64 * half;
+#pragma unroll
+        for (int j = 0; j < T::kN / 64; ++j) {           // eight rows of scales a load
+            const int piece = wave * (T::kN / 64) + j, r = 8 * piece + (lane >> 3), k = k0 + 32 * (lane & 7);
+            const uint32_t off = k < a.K ? (uint32_t)(min(r, last_n) * (a.K / T::B) + k / T::B) : kOff;
+            if constexpr (T::B == 32) lds_load1(sr, off, to + T::kX + T::kC + piece * 256);
+            else lds_load2(sr, off, to + T::kX + T::kC + piece * 256);
+        }
+        if constexpr (OUTER) {                           // 4 kN outer scales over the waves
+            constexpr int kPer = 4 * T::kN / 8;
+            const int i = wave * kPer + lane, r = i % T::kN, k = k0 + 64 * (i / T::kN);
             const int64_t n = min(n0 + r, a.N - 1);
             const uint32_t at = (uint32_t)((a.outer_kind == kOuter2D ? n >> 6 : n) * a.outer_n + k / a.obs * a.outer_k) * 4;
-            if (lane < 32)
-                lds_load4(make_rsrc(a.outer), k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + (half * kTileN + 32 * wn) * 4);
+            if (lane < kPer)
+                lds_load4(make_rsrc(a.outer), k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + wave * (4 * kPer));
         }
-    };
-    constexpr int kLoads = T::kXLoads + 1 + T::kSLoads + (OUTER ? 1 : 0);
-    // waves that load no x wait for one load less a stage
-    const auto wait_stage = [&](bool more) {
-        if (!more) wait_loads<0>();
-        else if (MT == 1 && wave >= 4) wait_loads<(T::kDepth - 2) * (kLoads - 1)>();
-        else wait_loads<(T::kDepth - 2) * kLoads>();
     };
 
     f32x4_t acc[MT][2];
@@ -281,7 +281,8 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
     for (int s = s0; s < s1; ++s) {
         // this wave's loads of the stage have landed; the barrier makes everybody's visible, and
         // says that the stage before, whose place is filled next, has been read
-        wait_stage(s + T::kDepth - 2 < s1);
+        if (s + T::kDepth - 2 < s1) wait_loads<(T::kDepth - 2) * T::kLoads>();
+        else wait_loads<0>();
         lds_barrier();
         const int free = slot == 0 ? T::kDepth - 1 : slot - 1;
         if (s + T::kDepth - 1 < s1) issue(s + T::kDepth - 1, free);
@@ -289,61 +290,67 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
         const lds_t* const c = x + T::kX;
         slot = slot + 1 == T::kDepth ? 0 : slot + 1;
 
-        uint4 w[2][2];
-        f32x4_t so[2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int r = 32 * wn + 16 * n + row;
-            const int chunk = (2 * half + (quarter >> 1)) ^ (r & 2);
-            const u32x2_t code = *(const __attribute__((address_space(3))) u32x2_t*)(c + r * 64 + chunk * 16 + (quarter & 1) * 8);
-            const float sc = DecBf16<BIAS>::scale(
-                *(const __attribute__((address_space(3))) uint32_t*)(c + T::kC +
-                                                                      (r * (kStageK / T::B) + (64 * half + 16 * quarter) / T::B) * 4));
-            w[n][0] = DecBf16<BIAS>::octet(code[0], sc);
-            w[n][1] = DecBf16<BIAS>::octet(code[1], sc);
-            if constexpr (OUTER)
-                so[n] = *(const __attribute__((address_space(3))) f32x4_t*)(c + T::kC + T::kS +
-                                                                             (half * kTileN + 32 * wn + 16 * n + 4 * quarter) * 4);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint4 v[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int chunk = (8 * half + 2 * quarter + i) ^ row;
-                const u32x4_t u = *(const __attribute__((address_space(3))) u32x4_t*)(x + (16 * m + row) * 256 + chunk * 16);
-                v[i] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+        for (int step = 0; step < T::kSteps; ++step) {
+            const int part = wk * T::kSteps + step;      // the stage's 64 values of K from 64 part
+            uint4 w[2][2];
+            f32x4_t so[2];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                f32x4_t p = OUTER ? f32x4_t{0, 0, 0, 0} : acc[m][n];
-                p = Dec<0>::mfma(w[n][0], v[0], p);
-                p = Dec<0>::mfma(w[n][1], v[1], p);
-                if constexpr (OUTER) {
+                const int r = 32 * wn + 16 * n + row;
+                const int chunk = (2 * part + (quarter >> 1)) ^ (r & 6);
+                const u32x2_t code = *(const LDS_PTR(u32x2_t))(c + r * 128 + chunk * 16 + (quarter & 1) * 8);
+                uint32_t byte = *(const LDS_PTR(uint32_t))(c + T::kC + (r * 8 + 2 * part + (quarter >> 1)) * 4);
+                if constexpr (T::B == 16) byte = __builtin_amdgcn_ubfe(byte, 8 * (quarter & 1), 8);
+                const float sc = DecBf16<BIAS>::scale(byte);
+                w[n][0] = DecBf16<BIAS>::octet(code[0], sc);
+                w[n][1] = DecBf16<BIAS>::octet(code[1], sc);
+                if constexpr (OUTER)
+                    so[n] = *(const LDS_PTR(f32x4_t))(c + T::kC + T::kS + (part * T::kN + 32 * wn + 16 * n + 4 * quarter) * 4);
+            }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[m][n][r] = __builtin_fmaf(p[r], so[n][r], acc[m][n][r]);
-                } else {
-                    acc[m][n] = p;
+            for (int m = 0; m < MT; ++m) {
+                uint4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int chunk = (8 * part + 2 * quarter + i) ^ row;
+                    const u32x4_t u = *(const LDS_PTR(u32x4_t))(x + (16 * m + row) * 512 + chunk * 16);
+                    v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    f32x4_t p = OUTER ? f32x4_t{0, 0, 0, 0} : acc[m][n];
+                    p = Dec<0>::mfma(w[n][0], v[0], p);
+                    p = Dec<0>::mfma(w[n][1], v[1], p);
+                    if constexpr (OUTER) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[m][n][r] = __builtin_fmaf(p[r], so[n][r], acc[m][n][r]);
+                    } else {
+                        acc[m][n] = p;
+                    }
                 }
             }
         }
     }
 
-    // the second half of K joins the first
+    // the parts of K join the first in order
     __syncthreads();
-    float* const join = reinterpret_cast<float*>(smem) + wn * (MT * 8 * 64) + lane;
-    if (half == 1) {
+    float* const join = reinterpret_cast<float*>(smem) + lane;
+    if (wk > 0) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) join[(m * 8 + i) * 64] = acc[m][i >> 2][i & 3];
+            for (int i = 0; i < 8; ++i)
+                join[(((wk - 1) * T::kWN + wn) * (MT * 8) + m * 8 + i) * 64] = acc[m][i >> 2][i & 3];
     }
     __syncthreads();
-    if (half == 1) return;
+    if (wk > 0) return;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int p = 0; p < T::kWK - 1; ++p)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] += join[(m * 8 + i) * 64];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[m][i >> 2][i & 3] += join[((p * T::kWN + wn) * (MT * 8) + m * 8 + i) * 64];
 
     const float whole = a.outer_kind == kOuterTensor && a.parts == nullptr ? a.outer[0] : 1.0f;
 #pragma unroll
@@ -384,11 +391,10 @@ template <int BIAS, int MT, bool OUTER>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t s)
 {
     using T = Tile<BIAS, MT, OUTER>;
-    static_assert(T::kLds >= 4 * MT * 8 * 64 * 4, "the halves join in the ring's place");
     static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_linear_tile<BIAS, MT, OUTER>),
                                                           hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (allowed != hipSuccess) return allowed;
-    const dim3 grid((uint32_t)((a.N + kTileN - 1) / kTileN), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)), (uint32_t)a.splits);
+    const dim3 grid((uint32_t)((a.N + T::kN - 1) / T::kN), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)), (uint32_t)a.splits);
     hipLaunchKernelGGL((k_linear_tile<BIAS, MT, OUTER>), grid, dim3(512), T::kLds, s, a);
     if (a.parts) {
         const int64_t quads = a.parts_ld / 4 * a.M;
@@ -407,7 +413,9 @@ hipError_t launch_outer(const LinearArgs& a, hipStream_t s)
     }
     if (a.M <= 16) return launch_tile<BIAS, 1, OUTER != kInnerOnly>(a, s);
     if (a.M <= 32) return launch_tile<BIAS, 2, OUTER != kInnerOnly>(a, s);
-    return launch_tile<BIAS, 4, OUTER != kInnerOnly>(a, s);
+    if (a.M <= 48) return launch_tile<BIAS, 3, OUTER != kInnerOnly>(a, s);
+    if (a.M <= 64) return launch_tile<BIAS, 4, OUTER != kInnerOnly>(a, s);
+    return launch_tile<BIAS, 8, OUTER != kInnerOnly>(a, s);
 }
 
 template <int BIAS>
@@ -427,14 +435,14 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K)
     LinearPlan p{0, 0, 0};
     // small weights under few rows: one launch without parts
     if (M <= 16 && N * K <= kSmallWeight) return p;
-    const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    const int64_t blocks = (N + kTileN - 1) / kTileN * ((M + rows - 1) / rows);
+    const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : M <= 64 ? 64 : 128, cols = M <= 64 ? 128 : 64;
+    const int64_t blocks = (N + cols - 1) / cols * ((M + rows - 1) / rows);
     const int64_t stages = (K + kStageK - 1) / kStageK;
-    int64_t want = 512 / blocks;                         // two workgroups a compute unit
+    int64_t want = 256 / blocks;                         // one workgroup a compute unit
     if (want > stages / 4) want = stages / 4;
     p.splits = want < 1 ? 1 : (int32_t)want;
     if (p.splits > 1) {
-        p.ld = (N + kTileN - 1) / kTileN * kTileN;
+        p.ld = (N + cols - 1) / cols * cols;
         p.bytes = (size_t)p.splits * M * p.ld * sizeof(float);
     }
     return p;

@@ -35,6 +35,12 @@ __device__ __forceinline__ void lds_load1(rsrc_t r, uint32_t off, uint32_t base)
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
 }
 
+// Two bytes a lane (2-byte aligned), lane l's to the word at base + 4 l.
+__device__ __forceinline__ void lds_load2(rsrc_t r, uint32_t off, uint32_t base)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ushort %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+}
+
 // Sixteen bytes a lane through the caches' ordinary policy, for bytes that other workgroups read again.
 __device__ __forceinline__ void lds_load_kept(rsrc_t r, uint32_t off, uint32_t base)
 {

@@ -417,6 +417,7 @@ int fp4_mx_scales_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t*
  *            rowwise ones of W^T [K, N], so with them (and M, K and N in their
  *            place) the same call is dx = dy W; a 2D outer array then belongs to the
  *            transpose and outer_transposed is 1 (as in fp4_dequantize).
+ *            NVFP4 and AMD-FP4 scale bytes 2-byte aligned.
  *   y        bf16 or FP32 (cfg->output_dtype) [M, ld_y] device (ld_y >= N), written.
  *   workspace  fp4q_linear_workspace_bytes() bytes (0 unless K is split over
  *            workgroups), 16-byte aligned; no initial value, nothing kept.

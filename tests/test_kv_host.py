@@ -174,6 +174,7 @@ def test_linear_rules():
         assert linear(**{n: MIS}) == fq.ERR_ALIGN
     assert linear(y=FAKE + 1) == fq.ERR_ALIGN and linear(ld_x=132) == fq.ERR_ALIGN
     assert linear(cfg=C(two_level="tensorwise"), outer=FAKE + 2) == fq.ERR_ALIGN
+    assert linear(scales=FAKE + 1) == fq.ERR_ALIGN
     assert linear(ld_x=(1 << 23) + 8) == fq.ERR_UNSUPPORTED
     big = dict(M=40, N=256, K=8192, ld_x=8192, ld_y=256)
     need = fq.fp4q_linear_workspace_bytes(40, 256, 8192)
