@@ -202,20 +202,26 @@ __global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
 // 32 kWN rows of W, and a row of W is decoded once for 16 MT rows of x: with eight tiles the
 // matrix instructions take as long as the decoding.  Few tiles: the stages are split over
 // workgroups, whose binary32 sums k_linear_join adds in order.
-constexpr int kStageK = 256;
 
 template <int BIAS, int MT, bool OUTER>
 struct Tile {
     static constexpr int B = Dec<BIAS>::kBlock;
-    static constexpr int kWN = MT == 8 ? 2 : 4, kWK = 8 / kWN;   // waves along W's rows and along K
+    static constexpr int kStageK = MT == 8 ? 128 : 256;
+    static constexpr int kWN = 4, kWK = 2;               // waves along W's rows and along K
     static constexpr int kN = 32 * kWN;
     static constexpr int kSteps = kStageK / kWK / 64;    // of 64 values of K, of a wave and stage
-    static constexpr int kX = 16 * MT * kStageK * 2, kC = kN * kStageK / 2, kS = kN * 8 * 4, kO = OUTER ? 4 * kN * 4 : 0;
+    static constexpr int kX = 16 * MT * kStageK * 2, kC = kN * kStageK / 2, kS = kN * kStageK / 8,
+                         kO = OUTER ? kN * kStageK / 16 : 0;
     static constexpr int kStage = kX + kC + kS + kO;
+    // 16-byte chunks of a row of x and of codes (scale words: half of the codes' chunks' values
+    // each, as many), and the loads of a wave and stage
+    static constexpr int kXC = kStageK / 8, kCC = kStageK / 32;
+    static constexpr int kCX = kCC - 2;                  // the bits of a row that move its chunks
+    static constexpr int kXL = 16 * MT * kXC / 512, kCL = kN * kCC / 512;
     // one workgroup fills a compute unit's LDS
     static constexpr int kDepth = 160 * 1024 / kStage < 4 ? 160 * 1024 / kStage : 4;
     static constexpr int kLds = kDepth * kStage;
-    static constexpr int kLoads = MT + kN / 64 + kN / 64 + (OUTER ? 1 : 0);   // of a wave and stage
+    static constexpr int kLoads = kXL + 2 * kCL + (OUTER ? 1 : 0);
     static_assert(kDepth >= 2 && kLds >= (kWK - 1) * kWN * MT * 8 * 64 * 4, "two stages; the parts join in their place");
 };
 
@@ -229,44 +235,59 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
     const int wn = wave % T::kWN, wk = wave / T::kWN;
     const int row = lane & 15, quarter = lane >> 4;
     const int n0 = (int)blockIdx.x * T::kN, m0 = (int)blockIdx.y * (16 * MT);
-    const int stages = (a.K + kStageK - 1) / kStageK;
+    const int stages = (a.K + T::kStageK - 1) / T::kStageK;
     const int s0 = (int)((int64_t)stages * blockIdx.z / gridDim.z), s1 = (int)((int64_t)stages * (blockIdx.z + 1) / gridDim.z);
 
     // Descriptors from the tile's first rows; rows beyond M or N repeat the last one
     // (their results are not stored), values beyond K load as zeros.
     const rsrc_t xr = make_rsrc(a.x + (int64_t)m0 * a.ld_x), cr = make_rsrc(a.codes + (int64_t)n0 * (a.K / 2));
     const rsrc_t sr = make_rsrc(a.scales + (int64_t)n0 * (a.K / T::B));
+    const rsrc_t outr = make_rsrc(a.outer);
     const int last_m = a.M - 1 - m0, last_n = a.N - 1 - n0;
 
+    // A lane's offsets within the first stage.  A later stage adds the same to all lanes, so a
+    // whole stage takes no lane arithmetic.
+    const int xc = lane % T::kXC, cc = lane % T::kCC;
+    uint32_t xo[T::kXL], co[T::kCL], ro[T::kCL];
+    const auto x_row = [&](int j) { return (wave * T::kXL + j) * (64 / T::kXC) + lane / T::kXC; };
+    const auto w_row = [&](int j) { return (wave * T::kCL + j) * (64 / T::kCC) + lane / T::kCC; };
+#pragma unroll
+    for (int j = 0; j < T::kXL; ++j)
+        xo[j] = (uint32_t)(min(x_row(j), last_m) * (int)a.ld_x + 8 * (xc ^ (x_row(j) & 15))) * 2;
+#pragma unroll
+    for (int j = 0; j < T::kCL; ++j) {
+        co[j] = (uint32_t)(min(w_row(j), last_n) * (a.K / 2) + 16 * (cc ^ (w_row(j) & T::kCX)));
+        ro[j] = (uint32_t)(min(w_row(j), last_n) * (a.K / T::B) + cc * (32 / T::B));
+    }
     auto issue = [&](int s, int slot) {
         const uint32_t to = lds_address(lds + slot * T::kStage);
-        const int k0 = s * kStageK;
+        const int k0 = s * T::kStageK;
+        const bool tail = k0 + T::kStageK > a.K;         // values beyond K load as zeros
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {                   // two rows of x a load
-            const int piece = wave * MT + j, r = 2 * piece + (lane >> 5);
-            const int k = k0 + 8 * ((lane & 31) ^ (r & 15));
-            lds_load_kept(xr, k < a.K ? (uint32_t)(min(r, last_m) * (int)a.ld_x + k) * 2 : kOff, to + piece * 1024);
+        for (int j = 0; j < T::kXL; ++j) {
+            uint32_t off = xo[j];
+            if (tail) off = k0 + 8 * (xc ^ (x_row(j) & 15)) < a.K ? off : kOff;
+            lds_load_kept(xr, off, to + (wave * T::kXL + j) * 1024, k0 * 2);
         }
 #pragma unroll
-        for (int j = 0; j < T::kN / 64; ++j) {           // eight rows of codes a load
-            const int piece = wave * (T::kN / 64) + j, r = 8 * piece + (lane >> 3);
-            const int k = k0 + 32 * ((lane & 7) ^ (r & 6));
-            lds_load_kept(cr, k < a.K ? (uint32_t)(min(r, last_n) * (a.K / 2) + k / 2) : kOff, to + T::kX + piece * 1024);
+        for (int j = 0; j < T::kCL; ++j) {
+            const int piece = wave * T::kCL + j;
+            uint32_t off = co[j], at = ro[j];
+            if (tail) {
+                off = k0 + 32 * (cc ^ (w_row(j) & T::kCX)) < a.K ? off : kOff;
+                at = k0 + 32 * cc < a.K ? at : kOff;
+            }
+            lds_load_kept(cr, off, to + T::kX + piece * 1024, k0 / 2);
+            if constexpr (T::B == 32) lds_load1(sr, at, to + T::kX + T::kC + piece * 256, k0 / T::B);
+            else lds_load2(sr, at, to + T::kX + T::kC + piece * 256, k0 / T::B);
         }
-#pragma unroll
-        for (int j = 0; j < T::kN / 64; ++j) {           // eight rows of scales a load
-            const int piece = wave * (T::kN / 64) + j, r = 8 * piece + (lane >> 3), k = k0 + 32 * (lane & 7);
-            const uint32_t off = k < a.K ? (uint32_t)(min(r, last_n) * (a.K / T::B) + k / T::B) : kOff;
-            if constexpr (T::B == 32) lds_load1(sr, off, to + T::kX + T::kC + piece * 256);
-            else lds_load2(sr, off, to + T::kX + T::kC + piece * 256);
-        }
-        if constexpr (OUTER) {                           // 4 kN outer scales over the waves
-            constexpr int kPer = 4 * T::kN / 8;
+        if constexpr (OUTER) {                           // the outer scales over the waves
+            constexpr int kPer = T::kN * T::kStageK / 512;
             const int i = wave * kPer + lane, r = i % T::kN, k = k0 + 64 * (i / T::kN);
-            const int64_t n = min(n0 + r, a.N - 1);
-            const uint32_t at = (uint32_t)((a.outer_kind == kOuter2D ? n >> 6 : n) * a.outer_n + k / a.obs * a.outer_k) * 4;
+            const int n = min(n0 + r, a.N - 1);
+            const uint32_t at = (uint32_t)((a.outer_kind == kOuter2D ? n >> 6 : n) * (int)a.outer_n + k / a.obs * (int)a.outer_k) * 4;
             if (lane < kPer)
-                lds_load4(make_rsrc(a.outer), k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + wave * (4 * kPer));
+                lds_load4(outr, k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + wave * (4 * kPer));
         }
     };
 
@@ -293,35 +314,46 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
 #pragma unroll
         for (int step = 0; step < T::kSteps; ++step) {
             const int part = wk * T::kSteps + step;      // the stage's 64 values of K from 64 part
-            uint4 w[2][2];
+            // all of the step's reads are issued before its arithmetic: W's first, whose decoding
+            // hides the wait for x
+            u32x2_t code[2];
+            uint32_t byte[2];
             f32x4_t so[2];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int r = 32 * wn + 16 * n + row;
-                const int chunk = (2 * part + (quarter >> 1)) ^ (r & 6);
-                const u32x2_t code = *(const LDS_PTR(u32x2_t))(c + r * 128 + chunk * 16 + (quarter & 1) * 8);
-                uint32_t byte = *(const LDS_PTR(uint32_t))(c + T::kC + (r * 8 + 2 * part + (quarter >> 1)) * 4);
-                if constexpr (T::B == 16) byte = __builtin_amdgcn_ubfe(byte, 8 * (quarter & 1), 8);
-                const float sc = DecBf16<BIAS>::scale(byte);
-                w[n][0] = DecBf16<BIAS>::octet(code[0], sc);
-                w[n][1] = DecBf16<BIAS>::octet(code[1], sc);
+                const int chunk = (2 * part + (quarter >> 1)) ^ (r & T::kCX);
+                code[n] = *(const LDS_PTR(u32x2_t))(c + r * (T::kStageK / 2) + chunk * 16 + (quarter & 1) * 8);
+                byte[n] = *(const LDS_PTR(uint32_t))(c + T::kC + (r * T::kCC + 2 * part + (quarter >> 1)) * 4);
                 if constexpr (OUTER)
                     so[n] = *(const LDS_PTR(f32x4_t))(c + T::kC + T::kS + (part * T::kN + 32 * wn + 16 * n + 4 * quarter) * 4);
             }
+            u32x4_t v[MT][2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                uint4 v[2];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int chunk = (8 * part + 2 * quarter + i) ^ row;
-                    const u32x4_t u = *(const LDS_PTR(u32x4_t))(x + (16 * m + row) * 512 + chunk * 16);
-                    v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                    v[m][i] = *(const LDS_PTR(u32x4_t))(x + (16 * m + row) * (T::kStageK * 2) + chunk * 16);
                 }
+            __builtin_amdgcn_sched_barrier(0);
+            uint4 w[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if constexpr (T::B == 16) byte[n] = __builtin_amdgcn_ubfe(byte[n], 8 * (quarter & 1), 8);
+                const float sc = DecBf16<BIAS>::scale(byte[n]);
+                w[n][0] = DecBf16<BIAS>::octet(code[n][0], sc);
+                w[n][1] = DecBf16<BIAS>::octet(code[n][1], sc);
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint4 v0 = make_uint4(v[m][0][0], v[m][0][1], v[m][0][2], v[m][0][3]);
+                const uint4 v1 = make_uint4(v[m][1][0], v[m][1][1], v[m][1][2], v[m][1][3]);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     f32x4_t p = OUTER ? f32x4_t{0, 0, 0, 0} : acc[m][n];
-                    p = Dec<0>::mfma(w[n][0], v[0], p);
-                    p = Dec<0>::mfma(w[n][1], v[1], p);
+                    p = Dec<0>::mfma(w[n][0], v0, p);
+                    p = Dec<0>::mfma(w[n][1], v1, p);
                     if constexpr (OUTER) {
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[m][n][r] = __builtin_fmaf(p[r], so[n][r], acc[m][n][r]);
@@ -345,7 +377,7 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
     }
     __syncthreads();
     if (wk > 0) return;
-#pragma unroll
+#pragma unroll 1
     for (int p = 0; p < T::kWK - 1; ++p)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -435,9 +467,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K)
     LinearPlan p{0, 0, 0};
     // small weights under few rows: one launch without parts
     if (M <= 16 && N * K <= kSmallWeight) return p;
-    const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : M <= 64 ? 64 : 128, cols = M <= 64 ? 128 : 64;
+    const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : M <= 64 ? 64 : 128, cols = 128;
     const int64_t blocks = (N + cols - 1) / cols * ((M + rows - 1) / rows);
-    const int64_t stages = (K + kStageK - 1) / kStageK;
+    const int64_t stages = (K + 255) / 256;
     int64_t want = 256 / blocks;                         // one workgroup a compute unit
     if (want > stages / 4) want = stages / 4;
     p.splits = want < 1 ? 1 : (int32_t)want;

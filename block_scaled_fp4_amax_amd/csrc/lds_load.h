@@ -18,33 +18,43 @@ __device__ __forceinline__ void lds_load(const void* p, uint32_t base)
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(p), "s"(base) : "memory", "m0");
 }
 
-__device__ __forceinline__ void lds_load(rsrc_t r, uint32_t off, uint32_t base)
+__device__ __forceinline__ void lds_load(rsrc_t r, uint32_t off, uint32_t base, uint32_t all = 0)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen nt lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, %3 offen nt lds" :
+                 : "v"(off), "s"(base), "s"(r), "s"(all)
+                 : "memory", "m0");
 }
 
 // Four bytes a lane, lane l's to base + 4 l.
-__device__ __forceinline__ void lds_load4(rsrc_t r, uint32_t off, uint32_t base)
+__device__ __forceinline__ void lds_load4(rsrc_t r, uint32_t off, uint32_t base, uint32_t all = 0)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %0, %2, %3 offen lds" :
+                 : "v"(off), "s"(base), "s"(r), "s"(all)
+                 : "memory", "m0");
 }
 
 // One byte a lane, lane l's to the word at base + 4 l.
-__device__ __forceinline__ void lds_load1(rsrc_t r, uint32_t off, uint32_t base)
+__device__ __forceinline__ void lds_load1(rsrc_t r, uint32_t off, uint32_t base, uint32_t all = 0)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %0, %2, %3 offen lds" :
+                 : "v"(off), "s"(base), "s"(r), "s"(all)
+                 : "memory", "m0");
 }
 
 // Two bytes a lane (2-byte aligned), lane l's to the word at base + 4 l.
-__device__ __forceinline__ void lds_load2(rsrc_t r, uint32_t off, uint32_t base)
+__device__ __forceinline__ void lds_load2(rsrc_t r, uint32_t off, uint32_t base, uint32_t all = 0)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ushort %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_ushort %0, %2, %3 offen lds" :
+                 : "v"(off), "s"(base), "s"(r), "s"(all)
+                 : "memory", "m0");
 }
 
 // Sixteen bytes a lane through the caches' ordinary policy, for bytes that other workgroups read again.
-__device__ __forceinline__ void lds_load_kept(rsrc_t r, uint32_t off, uint32_t base)
+__device__ __forceinline__ void lds_load_kept(rsrc_t r, uint32_t off, uint32_t base, uint32_t all = 0)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds" : : "v"(off), "s"(base), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, %3 offen lds" :
+                 : "v"(off), "s"(base), "s"(r), "s"(all)
+                 : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
