@@ -198,7 +198,8 @@ __global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
 //           MXFP4 and K = 2880),
 //   outer scales [4][32 kWN] FP32, per 64 values of K.
 // Wave w takes W's rows 32 (w % kWN) .. + 31 and the (w / kWN)-th part of the stage's K;
-// the parts join through LDS.  So a workgroup reads x from the caches once for
+// the parts join through LDS.  Waves 0 to 3, one of each SIMD, issue the loads, and the SIMD's
+// other wave computes meanwhile.  So a workgroup reads x from the caches once for
 // 32 kWN rows of W, and a row of W is decoded once for 16 MT rows of x: with eight tiles the
 // matrix instructions take as long as the decoding.  Few tiles: the stages are split over
 // workgroups, whose binary32 sums k_linear_join adds in order.
@@ -217,11 +218,12 @@ struct Tile {
     // each, as many), and the loads of a wave and stage
     static constexpr int kXC = kStageK / 8, kCC = kStageK / 32;
     static constexpr int kCX = kCC - 2;                  // the bits of a row that move its chunks
-    static constexpr int kXL = 16 * MT * kXC / 512, kCL = kN * kCC / 512;
+    static constexpr int kXL = 16 * MT * kXC / 256, kCL = kN * kCC / 256;
     // one workgroup fills a compute unit's LDS
     static constexpr int kDepth = 160 * 1024 / kStage < 4 ? 160 * 1024 / kStage : 4;
     static constexpr int kLds = kDepth * kStage;
-    static constexpr int kLoads = kXL + 2 * kCL + (OUTER ? 1 : 0);
+    static constexpr int kOL = OUTER ? kN * kStageK / 64 / 256 : 0;
+    static constexpr int kLoads = kXL + 2 * kCL + kOL;
     static_assert(kDepth >= 2 && kLds >= (kWK - 1) * kWN * MT * 8 * 64 * 4, "two stages; the parts join in their place");
 };
 
@@ -281,13 +283,12 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
             if constexpr (T::B == 32) lds_load1(sr, at, to + T::kX + T::kC + piece * 256, k0 / T::B);
             else lds_load2(sr, at, to + T::kX + T::kC + piece * 256, k0 / T::B);
         }
-        if constexpr (OUTER) {                           // the outer scales over the waves
-            constexpr int kPer = T::kN * T::kStageK / 512;
-            const int i = wave * kPer + lane, r = i % T::kN, k = k0 + 64 * (i / T::kN);
+#pragma unroll
+        for (int j = 0; j < T::kOL; ++j) {               // outer scales
+            const int i = (wave * T::kOL + j) * 64 + lane, r = i % T::kN, k = k0 + 64 * (i / T::kN);
             const int n = min(n0 + r, a.N - 1);
             const uint32_t at = (uint32_t)((a.outer_kind == kOuter2D ? n >> 6 : n) * (int)a.outer_n + k / a.obs * (int)a.outer_k) * 4;
-            if (lane < kPer)
-                lds_load4(outr, k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + wave * (4 * kPer));
+            lds_load4(outr, k < a.K ? at : kOff, to + T::kX + T::kC + T::kS + (wave * T::kOL + j) * 256);
         }
     };
 
@@ -297,16 +298,16 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
 
 #pragma unroll
     for (int i = 0; i < T::kDepth - 1; ++i)
-        if (s0 + i < s1) issue(s0 + i, i);
+        if (wave < 4 && s0 + i < s1) issue(s0 + i, i);
     int slot = 0;
     for (int s = s0; s < s1; ++s) {
-        // this wave's loads of the stage have landed; the barrier makes everybody's visible, and
+        // a loading wave's part of the stage has landed; the barrier makes everybody's visible, and
         // says that the stage before, whose place is filled next, has been read
         if (s + T::kDepth - 2 < s1) wait_loads<(T::kDepth - 2) * T::kLoads>();
         else wait_loads<0>();
         lds_barrier();
         const int free = slot == 0 ? T::kDepth - 1 : slot - 1;
-        if (s + T::kDepth - 1 < s1) issue(s + T::kDepth - 1, free);
+        if (wave < 4 && s + T::kDepth - 1 < s1) issue(s + T::kDepth - 1, free);
         const lds_t* const x = lds + slot * T::kStage;
         const lds_t* const c = x + T::kX;
         slot = slot + 1 == T::kDepth ? 0 : slot + 1;
