@@ -771,6 +771,8 @@ int check_attn(const KvView& kv, const fp4q_attn* a)
     return FP4Q_OK;
 }
 
+size_t attn_bytes(const AttnPlan& p) { return p.o + p.few_o + p.ml + p.few_ml; }
+
 AttnPlan plan_of(const KvView& kv, const fp4q_attn* a)
 {
     return plan_attn(kv, a->batch, a->total_q, a->q_heads, a->max_q, a->max_kv, a->table_cols, a->window);
@@ -830,7 +832,7 @@ size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache
     KvView kv;
     if (resolve_cache(cfg, cache, r, kv) || check_attn(kv, attn)) return 0;
     const AttnPlan p = plan_of(kv, attn);
-    return p.ml + p.o;
+    return attn_bytes(p);
 }
 
 int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
@@ -850,8 +852,9 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
         misaligned(attn->lse, 4) || (attn->total_q > 1 && attn->ld_q % 8))
         return FP4Q_ERR_ALIGN;
     const AttnPlan p = plan_of(a.kv, attn);
-    if (p.o > 0 && (!workspace || workspace_bytes < p.ml + p.o)) return FP4Q_ERR_WORKSPACE;
-    if (p.o > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
+    const size_t need = attn_bytes(p);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_ERR_WORKSPACE;
+    if (need > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
     a.q = attn->q;
     a.ld_q = attn->ld_q;
     a.table = attn->page_table;
@@ -860,8 +863,11 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     a.sinks = attn->sinks;
     a.out = attn->out;
     a.lse = attn->lse;
-    a.part_o = (float*)workspace;
-    a.part_ml = (float*)((char*)workspace + p.o);
+    char* ws = (char*)workspace;
+    a.part_o = (float*)ws;
+    a.few_o = (float*)(ws + p.o);
+    a.part_ml = (float*)(ws + p.o + p.few_o);
+    a.few_ml = (float*)(ws + p.o + p.few_o + p.ml);
     a.scale = attn->scale;
     a.batch = attn->batch;
     a.total_q = attn->total_q;

@@ -31,6 +31,7 @@
 // Few rows: the four waves of a workgroup take every fourth step of the same rows and
 // join through LDS, and the keys are split over workgroups, whose partial (O, m, l) a
 // second kernel joins (launch_attn).
+#include <algorithm>
 #include <type_traits>
 
 #include "fp4q_device.h"
@@ -47,7 +48,6 @@ constexpr int kWaves = 4;
 constexpr int kUnit = 128;                               // keys that a workgroup of few rows takes at once
 constexpr int kMinShare = 4;                             // units of a workgroup's share, at least
 constexpr int kFewRows = 32;
-constexpr int kTileRows = 32 * kWaves;                   // rows of a workgroup of k_attn
 constexpr int kMaxSplits = 64;
 constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -387,44 +387,36 @@ struct Sums {
     // o[n][r] is the value d = (D / 4) quarter + (D / 16) r + n of the lane's row
 };
 
-// One step: 32 keys from `at`, their bytes in `raw`; bits 0 and 1 of `groups` say which of its
-// two groups are.
-template <int D, int BIAS, int QT>
-__device__ __forceinline__ void attend_step(const Raw<D, BIAS>& raw, uint32_t groups, int at, int end, const Rows<D, BIAS, QT>& rows, int lane,
-                                            Sums<D, QT>& sum)
+// One step: 32 keys from `at`, whose operands `src` gives; bits 0 and 1 of `groups` say which of
+// its two groups of 16 are there.
+template <int D, int BIAS, int QT, class Src>
+__device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, int end, const Rows<D, BIAS, QT>& rows,
+                                            int lane, Sums<D, QT>& sum)
 {
     using X = Dec<BIAS>;
     constexpr int NK = D / 32;                           // products of a step's scores
     constexpr int ND = D / 16;                           // products of a step's outputs (values of V in a lane)
-    const int col = lane & 15, quarter = lane >> 4;
+    const int quarter = lane >> 4;
     const uint4 ones = make_uint4(X::kOnes, X::kOnes, X::kOnes, X::kOnes);
     // scores: S^T[key, row], keys 16 s + 4 quarter + r
     f32x4_t sc[QT][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        uint4 kf8[NK];
+        uint4 kf[NK];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            constexpr int per = X::kBlock / 8;           // words of a block
-            const uint32_t byte = D / 4 <= X::kBlock ? raw.ks[s] : (raw.ks[s] >> (8 * (i / per))) & 0xFFu;
-            kf8[i] = X::octet(raw.k[s][i], X::scale(byte));
-        }
+        for (int i = 0; i < NK; ++i) kf[i] = src.k(s, i);
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             sc[t][s] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < NK; ++i) sc[t][s] = X::mfma(kf8[i], rows.q[t][i], sc[t][s]);
+            for (int i = 0; i < NK; ++i) sc[t][s] = X::mfma(kf[i], rows.q[t][i], sc[t][s]);
         }
     }
 
     // A step whose keys are not all seen by all rows: scores of unseen keys are
-    // -infinity, and the scales of keys beyond the end (whose bytes may be
-    // anything, NaN among them) are cleared so that 0 times V is 0.
-    uint32_t vs[8];
-    const uint32_t vbit = 8 * (col * ND / X::kBlock);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) vs[j] = raw.v_scale(j >> 2, j & 3, vbit);
-    const bool whole = groups == 3 && at >= rows.last.lo && at + kStep <= rows.first.hi && at + kStep <= end;
+    // -infinity.  V of keys that are not there (whose bytes may be anything) is
+    // cleared, so that 0 times it is 0.
+    const bool whole = (groups & 3) == 3 && at >= rows.last.lo && at + kStep <= rows.first.hi && at + kStep <= end;
     if (!whole) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -435,9 +427,9 @@ __device__ __forceinline__ void attend_step(const Raw<D, BIAS>& raw, uint32_t gr
 #pragma unroll
                 for (int t = 0; t < QT; ++t)
                     if (!there || key < rows.see[t].lo || key >= rows.see[t].hi) sc[t][s][r] = -__builtin_inff();
-                if (!there) vs[4 * s + r] = 0;
+                src.keep(4 * s + r, there);
             }
-        if constexpr (BIAS == 0) poison_seen<ND, QT>(vs, sc, sum.o, ones);
+        if constexpr (BIAS == 0) src.poison(groups, sc, sum.o);
     }
 
     // running maximum, P
@@ -464,23 +456,15 @@ __device__ __forceinline__ void attend_step(const Raw<D, BIAS>& raw, uint32_t gr
     }
 
     // O^T += V^T P^T, two values of head_dim (one byte of codes) at a time
-#pragma unroll
-    for (int j = 0; j < 8; ++j) vs[j] = X::scale(vs[j]);
+    src.decode_scales();
     auto two = [&](auto byte_c) {
         constexpr int y = decltype(byte_c)::value;
-        uint32_t u[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = X::template pair<(y & 3)>(raw.v[j][y >> 2], vs[j]);
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            lo[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x05040100u);
-            hi[j] = __builtin_amdgcn_perm(u[2 * j + 1], u[2 * j], 0x07060302u);
-        }
+        uint4 lo, hi;
+        src.template v<y>(lo, hi);
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            sum.o[t][2 * y] = X::mfma(make_uint4(lo[0], lo[1], lo[2], lo[3]), p[t], sum.o[t][2 * y]);
-            sum.o[t][2 * y + 1] = X::mfma(make_uint4(hi[0], hi[1], hi[2], hi[3]), p[t], sum.o[t][2 * y + 1]);
+            sum.o[t][2 * y] = X::mfma(lo, p[t], sum.o[t][2 * y]);
+            sum.o[t][2 * y + 1] = X::mfma(hi, p[t], sum.o[t][2 * y + 1]);
         }
     };
     two(std::integral_constant<int, 0>{});
@@ -496,6 +480,63 @@ __device__ __forceinline__ void attend_step(const Raw<D, BIAS>& raw, uint32_t gr
         two(std::integral_constant<int, 7>{});
     }
 }
+
+// V's operands of two neighbouring values of head_dim (the low and high codes of byte B of each
+// key's word w[j]) for the lane's eight keys, with the keys' decoded scales.
+template <int BIAS, int B>
+__device__ __forceinline__ void decode_v(const uint32_t (&w)[8], const uint32_t (&scale)[8], uint4& lo, uint4& hi)
+{
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = Dec<BIAS>::template pair<B>(w[j], scale[j]);
+    lo = make_uint4(__builtin_amdgcn_perm(u[1], u[0], 0x05040100u), __builtin_amdgcn_perm(u[3], u[2], 0x05040100u),
+                    __builtin_amdgcn_perm(u[5], u[4], 0x05040100u), __builtin_amdgcn_perm(u[7], u[6], 0x05040100u));
+    hi = make_uint4(__builtin_amdgcn_perm(u[1], u[0], 0x07060302u), __builtin_amdgcn_perm(u[3], u[2], 0x07060302u),
+                    __builtin_amdgcn_perm(u[5], u[4], 0x07060302u), __builtin_amdgcn_perm(u[7], u[6], 0x07060302u));
+}
+
+// Operands decoded by the wave that uses them, from the step's bytes.
+template <int D, int BIAS, int QT>
+struct FromRaw {
+    const Raw<D, BIAS>& raw;
+    uint32_t vs[8];
+
+    __device__ __forceinline__ FromRaw(const Raw<D, BIAS>& raw, int lane) : raw(raw)
+    {
+        const uint32_t bit = 8 * ((lane & 15) * (D / 16) / Dec<BIAS>::kBlock);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vs[j] = raw.v_scale(j >> 2, j & 3, bit);
+    }
+
+    __device__ __forceinline__ uint4 k(int s, int i) const
+    {
+        constexpr int per = Dec<BIAS>::kBlock / 8;       // words of a block
+        const uint32_t byte = D / 4 <= Dec<BIAS>::kBlock ? raw.ks[s] : (raw.ks[s] >> (8 * (i / per))) & 0xFFu;
+        return Dec<BIAS>::octet(raw.k[s][i], Dec<BIAS>::scale(byte));
+    }
+
+    __device__ __forceinline__ void keep(int j, bool there) { vs[j] = there ? vs[j] : 0; }
+
+    __device__ __forceinline__ void poison(uint32_t, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
+    {
+        poison_seen<D / 16, QT>(vs, sc, o, make_uint4(Dec<0>::kOnes, Dec<0>::kOnes, Dec<0>::kOnes, Dec<0>::kOnes));
+    }
+
+    __device__ __forceinline__ void decode_scales()
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vs[j] = Dec<BIAS>::scale(vs[j]);
+    }
+
+    template <int Y>
+    __device__ __forceinline__ void v(uint4& lo, uint4& hi) const
+    {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = raw.v[j][Y >> 2];
+        decode_v<BIAS, (Y & 3)>(w, vs, lo, hi);
+    }
+};
 
 // Steps at, at + stride, ... before end, through the wave's ring.  The rows of the next
 // 64 steps are looked up together, a step a lane: a scalar look-up in each step would
@@ -546,7 +587,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* lds, co
         }
         Raw<D, BIAS> raw;
         ring.read(now, raw);
-        attend_step<D, BIAS, QT>(raw, groups & 3, at, end, rows, lane, sum);
+        FromRaw<D, BIAS, QT> src(raw, lane);
+        attend_step<D, BIAS, QT>(src, groups, at, end, rows, lane, sum);
     }
 }
 
@@ -657,7 +699,7 @@ __device__ __forceinline__ void write_parts(const AttnArgs& a, const Rows<D, BIA
 struct Seq {
     int first_q, queries, kv;
     int lo, hi;                                          // keys of all rows, from the step of the first
-    int units;                                           // of one head, 0: no queries
+    int units;                                           // of one head, 0: none here
 };
 
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b)
@@ -669,7 +711,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b)
     s.kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
     s.lo = key_range(0, qr.count, s.kv, a.causal, a.window).lo / kStep * kStep;
     s.hi = max(key_range(qr.count - 1, qr.count, s.kv, a.causal, a.window).hi, s.lo);
-    s.units = qr.count == 0 ? 0 : max(1, (s.hi - s.lo + kUnit - 1) / kUnit);
+    // sequences of more rows are k_attn_tiles'
+    s.units = qr.count == 0 || qr.count * a.group > kFewRows ? 0 : max(1, (s.hi - s.lo + kUnit - 1) / kUnit);
     return s;
 }
 
@@ -821,14 +864,230 @@ __global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift
 }
 
 // ---------------------------------------------------------------- many rows
-// Each wave has rows of its own and takes every step of their keys; a sequence whose rows fit one
-// wave is shared by the four as above.  Few workgroups split the keys `splits` ways.
+// Eight waves take rows of their own and the same keys, 128 (head_dim 256: 64) at a time.  Each wave
+// decodes a part of those keys' K and V once for all into LDS, as whole operands (64 lanes of 16
+// bytes, written and read without bank conflicts), for the next keys while this one's are
+// used; its bytes are loaded another round ahead.  Decoded by each wave for itself the work
+// per 32 rows and keys was 220 vector instructions beside 34 matrix ones (two prompts of
+// 4096 tokens, MXFP4: 305 us).  Few workgroups split the keys `splits` ways.
+template <int D>
+struct Tiles {
+    static constexpr int kWaves = 8;
+    static constexpr int kQT = D == 256 ? 1 : 2;
+    static constexpr int kRows = kWaves * 16 * kQT;
+    static constexpr int kSteps = D == 256 ? 2 : 4;      // of 32 keys, a round
+    static constexpr int kKeys = kSteps * kStep;
+    static constexpr int kFrags = D / 16;                // operands of K, and of V, a step
+    static constexpr int kStepBytes = 2 * kFrags * 1024;
+    static constexpr int kRound = kSteps * kStepBytes;
+    static constexpr int kLds = 2 * kRound + 2 * kSteps * 16;
+};
+
+// Operands from a step's place in LDS.
+template <int D, int BIAS, int QT>
+struct FromLds {
+    const lds_t* mem;                                    // the step's operands, at the lane's 16 bytes
+
+    __device__ __forceinline__ uint4 frag(int n) const
+    {
+        const u32x4_t u = *(const __attribute__((address_space(3))) u32x4_t*)(mem + n * 1024);
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+
+    __device__ __forceinline__ uint4 k(int s, int i) const { return frag(s * (D / 32) + i); }
+    __device__ __forceinline__ void keep(int, bool) {}
+    __device__ __forceinline__ void decode_scales() {}
+
+    // In a step with a poisoned block that some rows do not see: the NaN operands count for the
+    // rows that see their key, and v() gives zeros in their place.
+    bool clean = false;
+    __device__ __forceinline__ void poison(uint32_t groups, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
+    {
+        if (!(groups & 4)) return;
+        clean = true;
+        constexpr uint32_t one = Dec<0>::kOnes & 0xFFFFu;
+#pragma unroll 1
+        for (int n = 0; n < D / 16; ++n) {
+            const uint4 v = frag(D / 16 + n);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t bad[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bad[j] = ((w[j] & 0x7FFFu) > 0x7F80u ? one : 0u) | ((w[j] >> 16 & 0x7FFFu) > 0x7F80u ? one << 16 : 0u);
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                uint32_t seen[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    seen[j] = (sc[t][j >> 1][2 * (j & 1)] != -__builtin_inff() ? one : 0u) |
+                              (sc[t][j >> 1][2 * (j & 1) + 1] != -__builtin_inff() ? one << 16 : 0u);
+                const f32x4_t c = Dec<0>::mfma(make_uint4(bad[0], bad[1], bad[2], bad[3]),
+                                               make_uint4(seen[0], seen[1], seen[2], seen[3]), f32x4_t{0, 0, 0, 0});
+                // o[t][n] with a runtime n: every n is compared, so that o stays in registers
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[t][d][r] = d == n && c[r] > 0.0f ? __builtin_nanf("") : o[t][d][r];
+            }
+        }
+    }
+
+    __device__ __forceinline__ uint4 v_frag(int n) const
+    {
+        uint4 v = frag(D / 16 + n);
+        if constexpr (BIAS == 0) {
+            if (clean) {
+                uint32_t* w = (uint32_t*)&v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = ((w[j] & 0x7FFFu) > 0x7F80u ? 0u : w[j] & 0xFFFFu) |
+                           ((w[j] >> 16 & 0x7FFFu) > 0x7F80u ? 0u : w[j] & 0xFFFF0000u);
+            }
+        }
+        return v;
+    }
+
+    template <int Y>
+    __device__ __forceinline__ void v(uint4& lo, uint4& hi) const
+    {
+        lo = v_frag(2 * Y);
+        hi = v_frag(2 * Y + 1);
+    }
+};
+
+// A wave's part of a round's decoding: K or V of one step (head_dim 256: half of it).
 template <int D, int BIAS>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn(AttnArgs a)
+struct DecodePart {
+    using T = Tiles<D>;
+    static constexpr int B = Dec<BIAS>::kBlock;
+    static constexpr int kHalves = 8 / (2 * T::kSteps);
+    int step, half, lane;
+    bool is_v;
+    const uint8_t *codes, *scales;
+
+    __device__ __forceinline__ DecodePart(const KvView& kv, int wave, int lane) : lane(lane)
+    {
+        step = wave % T::kSteps;
+        is_v = wave / T::kSteps % 2;
+        half = wave / (2 * T::kSteps);
+        codes = is_v ? kv.v_codes : kv.k_codes;
+        scales = is_v ? kv.v_scales : kv.k_scales;
+    }
+
+    struct Bytes {
+        uint32_t w[8], s[8];
+    };
+
+    // row[2]: the rows of the step's groups, -1 where absent (then the cache's first rows)
+    __device__ __forceinline__ void load(const int64_t (&row)[2], Bytes& b) const
+    {
+        const uint32_t m = lane & 15, q = (uint32_t)lane >> 4;
+        if (!is_v) {
+            constexpr int W = D / 32, KB = D / 4 / B > 0 ? D / 4 / B : 1;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (kHalves == 2 && s != half) continue; // uniform
+                const int64_t r = row[s] < 0 ? 0 : row[s];
+                const rsrc_t c = rows_at(codes, r, D / 2), f = rows_at(scales, r, D / B);
+                uint32_t* w = b.w + (kHalves == 2 ? 0 : s * W);
+                const uint32_t at = m * (D / 2) + q * (D / 8);
+                if constexpr (W == 2) {
+                    const u32x2_t u = __builtin_amdgcn_raw_buffer_load_b64(c, at, 0, 0);
+                    w[0] = u[0], w[1] = u[1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i) {
+                        const uint4 u = buf_load16<0>(c, at + 16 * i);
+                        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+                    }
+                }
+                const uint32_t fa = m * (D / B) + q * (D / 4) / B;
+                uint32_t& o = b.s[kHalves == 2 ? 0 : s];
+                if constexpr (KB == 1) o = __builtin_amdgcn_raw_buffer_load_b8(f, fa, 0, 0);
+                else if constexpr (KB == 2) o = __builtin_amdgcn_raw_buffer_load_b16(f, fa, 0, 0);
+                else o = __builtin_amdgcn_raw_buffer_load_b32(f, fa, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int64_t r = row[s] < 0 ? 0 : row[s];
+                const rsrc_t c = rows_at(codes, r, D / 2), f = rows_at(scales, r, D / B);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t at = (4 * q + t) * (D / 2) + m * (D / 32);
+                    if constexpr (D == 64) b.w[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b16(c, at, 0, 0);
+                    else b.w[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b32(c, at + 4 * half, 0, 0);
+                    b.s[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b8(f, (4 * q + t) * (D / B) + m * (D / 16) / B, 0, 0);
+                }
+            }
+        }
+    }
+
+    // Writes the operands of the step at `at` to the round's LDS, and the step's flags: which groups are there,
+    // and (bit 2) whether V has a poisoned block.
+    __device__ __forceinline__ void decode(const int64_t (&row)[2], int at, int kv, Bytes& b, lds_t* round, lds_t* flags) const
+    {
+        using X = Dec<BIAS>;
+        lds_t* to = round + step * T::kStepBytes + lane * 16;
+        const auto put = [&](int n, uint4 v) {
+            *(__attribute__((address_space(3))) u32x4_t*)(to + n * 1024) = u32x4_t{v.x, v.y, v.z, v.w};
+        };
+        if (!is_v) {
+            constexpr int W = D / 32, per = B / 8;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (kHalves == 2 && s != half) continue;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const uint32_t sb = b.s[kHalves == 2 ? 0 : s];
+                    const uint32_t byte = D / 4 <= B ? sb : (sb >> (8 * (i / per))) & 0xFFu;
+                    put(s * W + i, X::octet(b.w[(kHalves == 2 ? 0 : s * W) + i], X::scale(byte)));
+                }
+            }
+            return;
+        }
+        const uint32_t there = (row[0] >= 0 ? 1u : 0u) | (row[1] >= 0 ? 2u : 0u);
+        if (there != 3 || at + kStep > kv) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int key = at + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
+                if (!(there >> (j >> 2) & 1) || key >= kv) b.s[j] = 0;
+            }
+        }
+        uint32_t flag = there;
+        if constexpr (BIAS == 0) {
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bad |= b.s[j] == 0xFFu;
+            flag |= __any(bad) ? 4u : 0u;
+        }
+        if (lane == 0 && half == 0) *(__attribute__((address_space(3))) uint32_t*)(flags + step * 16) = flag;
+        uint32_t sc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sc[j] = X::scale(b.s[j]);
+        const int n0 = D / 16 + 8 * half;
+        uint4 lo, hi;
+        decode_v<BIAS, 0>(b.w, sc, lo, hi);
+        put(n0, lo), put(n0 + 1, hi);
+        decode_v<BIAS, 1>(b.w, sc, lo, hi);
+        put(n0 + 2, lo), put(n0 + 3, hi);
+        if constexpr (D > 64) {
+            decode_v<BIAS, 2>(b.w, sc, lo, hi);
+            put(n0 + 4, lo), put(n0 + 5, hi);
+            decode_v<BIAS, 3>(b.w, sc, lo, hi);
+            put(n0 + 6, lo), put(n0 + 7, hi);
+        }
+    }
+};
+
+template <int D, int BIAS>
+__global__ __launch_bounds__(512) void k_attn_tiles(AttnArgs a)
 {
-    constexpr int QT = 2, kRows = 16 * QT;
+    using T = Tiles<D>;
+    constexpr int QT = T::kQT;
     extern __shared__ __align__(16) unsigned char smem[];
-    JoinLds<D, QT>& lds = *reinterpret_cast<JoinLds<D, QT>*>(smem);
+    lds_t* const lds = (lds_t*)smem;
+    lds_t* const flags = lds + 2 * T::kRound;
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int head = (int)blockIdx.x;
@@ -836,22 +1095,78 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn(AttnArgs
     const QueryRange qr = queries_of(a, b);
     const int kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
     const int count = qr.count * a.group;
-    if (count == 0) return;
-    const bool shared = count <= kRows;
-    const int row0 = shared ? 0 : ((int)blockIdx.y * kWaves + wave) * kRows;
-    if (shared ? blockIdx.y > 0 : (int)blockIdx.y * kWaves * kRows >= count) return;
+    if (count <= kFewRows && a.batch > 1) return;        // k_attn_few's
+    // the last rows, which see the most keys, first
+    const int block = (int)(gridDim.y - 1 - blockIdx.y);
+    if (block * T::kRows >= count) return;
+    const int row0 = block * T::kRows + wave * (16 * QT);
     Rows<D, BIAS, QT> rows;
     Sums<D, QT> sum;
     rows.load(a, qr, kv, head, row0, lane);
     sum.clear();
-    const int begin = rows.first.lo / kStep * kStep + split * a.chunk;
-    const int end = row0 >= count ? 0 : min(rows.last.hi, begin + a.chunk);
-    attend<D, BIAS, QT>(a, smem + wave * Ring<D, BIAS>::kWave, a.table + (int64_t)b * a.table_cols, head, begin + (shared ? wave * kStep : 0), end,
-                        shared ? kUnit : kStep, rows, lane, sum);
-    if (shared) {
-        join_waves<D, QT>(lds, wave, lane, sum);
-        if (wave != 0) return;
+    // keys of the workgroup's rows (this split's part) and of the wave's
+    const KeyRange kf = key_range(block * T::kRows / a.group, qr.count, kv, a.causal, a.window);
+    const KeyRange kl = key_range((min((block + 1) * T::kRows, count) - 1) / a.group, qr.count, kv, a.causal, a.window);
+    const int begin = kf.lo / T::kKeys * T::kKeys + split * a.chunk;
+    const int end = min(kl.hi, begin + a.chunk);
+    const int my_end = row0 < count ? min(rows.last.hi, end) : 0;
+
+    const DecodePart<D, BIAS> part(a.kv, wave, lane);
+    const int32_t* table = a.table + (int64_t)b * a.table_cols;
+    // rows of the part's step in the next 64 rounds, a round a lane
+    int64_t row[2];
+    int known = 64, looked = begin;                      // the next round to look up
+    const auto next_rows = [&](int64_t (&g)[2]) {
+        if (known == 64) {
+            known = 0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const KvGroup k = kv_group(table, looked + lane * T::kKeys + part.step * kStep + kKvGroup * s, kv, a.per_page,
+                                           a.kv.num_pages, a.kv.heads, head);
+                row[s] = k.ok ? k.row : -1;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)row[s], known);
+            const int32_t hi = __builtin_amdgcn_readlane((int32_t)(row[s] >> 32), known);
+            g[s] = (int64_t)hi << 32 | lo;
+        }
+        ++known;
+        looked += T::kKeys;
+    };
+
+    if (begin < end) {                                   // the same for all waves
+        typename DecodePart<D, BIAS>::Bytes now, next;
+        int64_t g0[2], g1[2];
+        next_rows(g0);
+        part.load(g0, now);
+        next_rows(g1);
+        part.load(g1, next);
+        part.decode(g0, begin + part.step * kStep, kv, now, lds, flags);
+        int buf = 0;
+        for (int at = begin; at < end; at += T::kKeys, buf ^= 1) {
+            lds_barrier();                               // this round is decoded, the other one's place is free
+            now = next;
+            g0[0] = g1[0], g0[1] = g1[1];
+            if (at + T::kKeys < end) {
+                next_rows(g1);
+                part.load(g1, next);
+                part.decode(g0, at + T::kKeys + part.step * kStep, kv, now, lds + (buf ^ 1) * T::kRound,
+                            flags + (buf ^ 1) * (T::kSteps * 16));
+            }
+#pragma unroll 1
+            for (int s = 0; s < T::kSteps; ++s) {
+                const int k = at + s * kStep;
+                if (k >= my_end || k + kStep <= rows.first.lo) continue;
+                const uint32_t groups = __builtin_amdgcn_readfirstlane(
+                    *(const __attribute__((address_space(3))) uint32_t*)(flags + buf * (T::kSteps * 16) + s * 16));
+                FromLds<D, BIAS, QT> src{lds + buf * T::kRound + s * T::kStepBytes + lane * 16};
+                attend_step<D, BIAS, QT>(src, groups, k, my_end, rows, lane, sum);
+            }
+        }
     }
+    if (row0 >= count) return;
     if (a.splits > 1) write_parts<D, BIAS, QT>(a, rows, sum, (int64_t)split * a.total_q * a.q_heads, true, lane);
     else write_rows<D, BIAS, QT>(a, rows, sum, head, lane);
 }
@@ -864,12 +1179,12 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, float unshift)
     const int64_t rows = (int64_t)a.total_q * a.q_heads;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (row >= rows) return;
-    // only rows of some sequence have partial results
+    // only rows that k_attn_tiles took have partial results
     const int token = (int)(row / a.q_heads), qh = (int)(row - (int64_t)token * a.q_heads);
     bool mine = false;
     for (int b = lane; b < a.batch; b += 64) {
         const QueryRange r = queries_of(a, b);
-        mine |= token >= r.first && token < r.first + r.count;
+        mine |= token >= r.first && token < r.first + r.count && (a.batch == 1 || r.count * a.group > kFewRows);
     }
     if (!__any(mine)) return;
     // lane s holds split s's (m, l); a row's reference is the largest m of those that saw a key
@@ -903,45 +1218,43 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, float unshift)
 }
 
 // A kernel's LDS limit is a property of the function: raised once, outside any launch.
-template <int D, int BIAS, int QT, bool FEW>
-hipError_t allow_lds()
-{
-    constexpr int n = lds_bytes<D, BIAS, QT>();
-    const void* f = nullptr;
-    if constexpr (FEW) f = reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>);
-    else f = reinterpret_cast<const void*>(k_attn<D, BIAS>);
-    static const hipError_t st = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, n);
-    return st;
-}
-
 template <int D, int BIAS, int QT>
-hipError_t launch_few(const AttnArgs& a, hipStream_t s)
+hipError_t launch_few(AttnArgs a, hipStream_t s)
 {
-    const hipError_t st = allow_lds<D, BIAS, QT, true>();
+    constexpr int lds = lds_bytes<D, BIAS, QT>();
+    static const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (st != hipSuccess) return st;
-    hipLaunchKernelGGL((k_attn_few<D, BIAS, QT>), dim3((uint32_t)a.groups), dim3(64 * kWaves), (lds_bytes<D, BIAS, QT>()), s, a);
-    if (a.slots)
-        hipLaunchKernelGGL((k_attn_few_join<D, QT>),
-                           dim3((uint32_t)((a.max_q * a.group + 3) / 4), (uint32_t)a.kv.heads, (uint32_t)a.batch), dim3(256),
-                           0, s, a, Dec<BIAS>::kUnshift);
+    a.part_o = a.few_o;
+    a.part_ml = a.few_ml;
+    hipLaunchKernelGGL((k_attn_few<D, BIAS, QT>), dim3((uint32_t)a.groups), dim3(64 * kWaves), lds, s, a);
+    if (a.slots) {
+        const int64_t rows = std::min<int64_t>((int64_t)a.max_q * a.group, kFewRows);
+        hipLaunchKernelGGL((k_attn_few_join<D, QT>), dim3((uint32_t)((rows + 3) / 4), (uint32_t)a.kv.heads, (uint32_t)a.batch),
+                           dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
+    }
     return hipGetLastError();
 }
 
 template <int D, int BIAS>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
 {
+    using T = Tiles<D>;
     const int64_t rows = (int64_t)a.max_q * a.group;
     if (rows <= 16) return launch_few<D, BIAS, 1>(a, s);
     if (rows <= kFewRows) return launch_few<D, BIAS, 2>(a, s);
-    const hipError_t st = allow_lds<D, BIAS, 2, false>();
+    if (a.groups) {                                      // a batch may hold sequences of few rows too
+        const hipError_t st = launch_few<D, BIAS, 2>(a, s);
+        if (st != hipSuccess) return st;
+    }
+    static const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tiles<D, BIAS>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (st != hipSuccess) return st;
-    {
-        const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
-        hipLaunchKernelGGL((k_attn<D, BIAS>), grid, dim3(64 * kWaves), (lds_bytes<D, BIAS, 2>()), s, a);
-        if (a.splits > 1) {
-            const int64_t all = (int64_t)a.total_q * a.q_heads;
-            hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
-        }
+    const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + T::kRows - 1) / T::kRows), (uint32_t)(a.batch * a.splits));
+    hipLaunchKernelGGL((k_attn_tiles<D, BIAS>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
+    if (a.splits > 1) {
+        const int64_t all = (int64_t)a.total_q * a.q_heads;
+        hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
     }
     return hipGetLastError();
 }
@@ -956,42 +1269,42 @@ hipError_t launch_bias(const AttnArgs& a, hipStream_t s)
 
 }  // namespace
 
+// Sequences of few rows.
+static void plan_few(AttnPlan& p, const KvView& kv, int64_t batch, int64_t rows, int64_t keys)
+{
+    // Workgroups that the chip holds at once: 4 a compute unit (head_dim 64; 3 with two
+    // tiles of rows), 2 (128) or 2 and 1 (256) by their LDS and registers.  Keys are not cut where
+    // every sequence is short or the heads alone fill the chip twice.
+    const bool one = rows <= 16;
+    const int64_t slots = 256 * (kv.dim == 64 ? (one ? 4 : 3) : kv.dim == 128 || one ? 2 : 1);
+    const int64_t heads = batch * kv.heads;
+    p.groups = (int32_t)heads;
+    if (keys <= kUnit * kMinShare || heads >= 2 * slots) return;
+    // no share makes more parts than these: a part is a share, or the last of its sequence
+    const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
+    const int64_t parts = std::min(per_head + batch, batch * ((keys / kUnit + 2) / kMinShare + 1));
+    p.slots = (int32_t)slots;
+    p.groups = (int32_t)(parts * kv.heads);
+    const size_t n = (size_t)p.groups * (one ? 16 : 32);
+    p.few_ml = n * 2 * sizeof(float);
+    p.few_o = n * kv.dim * sizeof(float);
+}
+
 AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_heads, int64_t max_q, int64_t max_kv,
                    int64_t table_cols, int64_t window)
 {
-    AttnPlan p{1, 1 << 30, 0, 0, 0, 0};
+    AttnPlan p{1, 1 << 30, 0, 0, 0, 0, 0, 0};
     const int64_t rows = max_q * (q_heads / kv.heads);
     if (rows == 0 || batch == 0) return p;
     // keys that one tile of rows can see
-    int64_t keys = max_kv < table_cols * kv.page_size ? max_kv : table_cols * kv.page_size;
-    if (window && window + max_q + kStep < keys) keys = window + max_q + kStep;
-    const int64_t heads = batch * kv.heads;
-    if (rows <= kFewRows) {
-        // Workgroups that the chip holds at once: 4 a compute unit (head_dim 64; 3 with two
-        // tiles of rows), 2 (128) or 2 and 1 (256) by their LDS and registers.  Keys are not cut where
-        // every sequence is short or the heads alone fill the chip twice.
-        const bool one = rows <= 16;
-        const int64_t slots = 256 * (kv.dim == 64 ? (one ? 4 : 3) : kv.dim == 128 || one ? 2 : 1);
-        p.groups = (int32_t)heads;
-        if (keys <= kUnit * kMinShare || heads >= 2 * slots) return p;
-        // no share makes more parts than these: a part is a share, or the last of its sequence
-        const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
-        int64_t parts = per_head + batch;
-        const int64_t most = batch * ((keys / kUnit + 2) / kMinShare + 1);
-        if (parts > most) parts = most;
-        p.slots = (int32_t)slots;
-        p.groups = (int32_t)(parts * kv.heads);
-        const size_t n = (size_t)p.groups * (rows <= 16 ? 16 : 32);
-        p.ml = n * 2 * sizeof(float);
-        p.o = n * kv.dim * sizeof(float);
-        return p;
-    }
+    int64_t keys = std::min(max_kv, table_cols * kv.page_size);
+    if (window) keys = std::min(keys, window + max_q + kStep);
+    if (rows <= kFewRows || batch > 1) plan_few(p, kv, batch, std::min<int64_t>(rows, kFewRows), keys);
+    if (rows <= kFewRows) return p;
     // Tiles of rows fill the chip by themselves or split the keys until they do once.
-    const int64_t blocks = heads * ((rows + kTileRows - 1) / kTileRows);
-    int64_t want = 256 / blocks;
-    if (want > keys / 512) want = keys / 512;
-    if (want > kMaxSplits) want = kMaxSplits;
-    if (want > 65535 / batch) want = 65535 / batch;
+    const int64_t tile = kv.dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows;
+    const int64_t blocks = batch * kv.heads * ((rows + tile - 1) / tile);
+    const int64_t want = std::min({256 / blocks, keys / 512, (int64_t)kMaxSplits, 65535 / batch});
     if (want <= 1) return p;
     p.splits = (int32_t)want;
     p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);

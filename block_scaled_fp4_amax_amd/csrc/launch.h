@@ -250,8 +250,8 @@ struct AttnArgs {
     const float* sinks;      // [q_heads] or null
     void* out;               // bf16 or FP32 [total_q, q_heads, dim]
     float* lse;              // [total_q, q_heads] or null
-    float* part_o;           // rows of partial results [dim]: [groups][2][16 or 32], or
-    float* part_ml;          // [splits][total_q * q_heads]; their (m, l)
+    float *part_o, *part_ml; // many rows: [splits][total_q * q_heads] partial results [dim], and their (m, l)
+    float *few_o, *few_ml;   // few rows: [groups][16 or 32]
     float scale;
     int32_t batch, total_q, q_heads, group, table_cols, max_q, max_kv, causal, window;
     int32_t slots, groups;   // few rows: workgroups that the chip holds (0: keys are not cut), workgroups
@@ -263,7 +263,7 @@ struct AttnArgs {
 // How a call's keys are shared (fields as above) and the bytes of its partial results.
 struct AttnPlan {
     int32_t splits, chunk, slots, groups;
-    size_t ml, o;
+    size_t ml, o, few_ml, few_o;
 };
 
 AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_heads, int64_t max_q, int64_t max_kv,
