@@ -300,29 +300,35 @@ __device__ __forceinline__ void write_joined(const AttnArgs& a, int64_t row, int
 // its NaN would reach the rows that do not see the key.  Such blocks are cleared,
 // and the product of (block is poisoned) with (row sees the key) says which
 // outputs become NaN.  All of a lane's values of V lie in one block.
-template <int ND, int QT>
-__device__ __forceinline__ void poison_seen(uint32_t (&vs)[8], const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][ND], uint4 ones)
+__device__ __forceinline__ bool poisoned_blocks(uint32_t (&vs)[8], uint4& bad)
 {
     bool any = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) any |= vs[j] == 0xFFu;
-    if (!__any(any)) return;
-    uint32_t bad[4];
+    if (!__any(any)) return false;
+    constexpr uint32_t one = Dec<0>::kOnes & 0xFFFFu;
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        bad[j] = (vs[2 * j] == 0xFFu ? ones.x & 0xFFFFu : 0u) | (vs[2 * j + 1] == 0xFFu ? ones.x & 0xFFFF0000u : 0u);
+    for (int j = 0; j < 4; ++j) w[j] = (vs[2 * j] == 0xFFu ? one : 0u) | (vs[2 * j + 1] == 0xFFu ? one << 16 : 0u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) vs[j] = vs[j] == 0xFFu ? 0u : vs[j];
+    bad = make_uint4(w[0], w[1], w[2], w[3]);
+    return true;
+}
+
+template <int ND, int QT>
+__device__ __forceinline__ void mark_poisoned(uint4 bad, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][ND])
+{
+    constexpr uint32_t one = Dec<0>::kOnes & 0xFFFFu;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         uint32_t seen[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float a = sc[t][j >> 1][2 * (j & 1)], b = sc[t][j >> 1][2 * (j & 1) + 1];
-            seen[j] = (a != -__builtin_inff() ? ones.x & 0xFFFFu : 0u) | (b != -__builtin_inff() ? ones.x & 0xFFFF0000u : 0u);
+            seen[j] = (a != -__builtin_inff() ? one : 0u) | (b != -__builtin_inff() ? one << 16 : 0u);
         }
-        const f32x4_t n = Dec<0>::mfma(make_uint4(bad[0], bad[1], bad[2], bad[3]),
-                                       make_uint4(seen[0], seen[1], seen[2], seen[3]), f32x4_t{0, 0, 0, 0});
+        const f32x4_t n = Dec<0>::mfma(bad, make_uint4(seen[0], seen[1], seen[2], seen[3]), f32x4_t{0, 0, 0, 0});
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -429,8 +435,8 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
                     if (!there || key < rows.see[t].lo || key >= rows.see[t].hi) sc[t][s][r] = -__builtin_inff();
                 src.keep(4 * s + r, there);
             }
-        if constexpr (BIAS == 0) src.poison(groups, sc, sum.o);
     }
+    if constexpr (BIAS == 0) src.poison(groups, whole, sc, sum.o);
 
     // running maximum, P
     uint4 p[QT];
@@ -517,9 +523,10 @@ struct FromRaw {
 
     __device__ __forceinline__ void keep(int j, bool there) { vs[j] = there ? vs[j] : 0; }
 
-    __device__ __forceinline__ void poison(uint32_t, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
+    __device__ __forceinline__ void poison(uint32_t, bool whole, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
     {
-        poison_seen<D / 16, QT>(vs, sc, o, make_uint4(Dec<0>::kOnes, Dec<0>::kOnes, Dec<0>::kOnes, Dec<0>::kOnes));
+        uint4 bad;                                       // where all rows see the keys, the products do it
+        if (!whole && poisoned_blocks(vs, bad)) mark_poisoned<D / 16, QT>(bad, sc, o);
     }
 
     __device__ __forceinline__ void decode_scales()
@@ -873,12 +880,12 @@ __global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift
 template <int D>
 struct Tiles {
     static constexpr int kWaves = 8;
-    static constexpr int kQT = D == 256 ? 1 : 2;
+    static constexpr int kQT = 1;
     static constexpr int kRows = kWaves * 16 * kQT;
-    static constexpr int kSteps = D == 256 ? 2 : 4;      // of 32 keys, a round
+    static constexpr int kSteps = D == 64 ? 4 : 2;       // of 32 keys, a round
     static constexpr int kKeys = kSteps * kStep;
     static constexpr int kFrags = D / 16;                // operands of K, and of V, a step
-    static constexpr int kStepBytes = 2 * kFrags * 1024;
+    static constexpr int kStepBytes = (2 * kFrags + 1) * 1024;   // and which blocks of V are poisoned (MXFP4)
     static constexpr int kRound = kSteps * kStepBytes;
     static constexpr int kLds = 2 * kRound + 2 * kSteps * 16;
 };
@@ -886,6 +893,7 @@ struct Tiles {
 // Operands from a step's place in LDS.
 template <int D, int BIAS, int QT>
 struct FromLds {
+    static constexpr int NF = D / 16;
     const lds_t* mem;                                    // the step's operands, at the lane's 16 bytes
 
     __device__ __forceinline__ uint4 frag(int n) const
@@ -895,63 +903,19 @@ struct FromLds {
     }
 
     __device__ __forceinline__ uint4 k(int s, int i) const { return frag(s * (D / 32) + i); }
-    __device__ __forceinline__ void keep(int, bool) {}
     __device__ __forceinline__ void decode_scales() {}
+    __device__ __forceinline__ void keep(int, bool) {}
 
-    // In a step with a poisoned block that some rows do not see: the NaN operands count for the
-    // rows that see their key, and v() gives zeros in their place.
-    bool clean = false;
-    __device__ __forceinline__ void poison(uint32_t groups, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
+    __device__ __forceinline__ void poison(uint32_t groups, bool, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][NF])
     {
-        if (!(groups & 4)) return;
-        clean = true;
-        constexpr uint32_t one = Dec<0>::kOnes & 0xFFFFu;
-#pragma unroll 1
-        for (int n = 0; n < D / 16; ++n) {
-            const uint4 v = frag(D / 16 + n);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t bad[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bad[j] = ((w[j] & 0x7FFFu) > 0x7F80u ? one : 0u) | ((w[j] >> 16 & 0x7FFFu) > 0x7F80u ? one << 16 : 0u);
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                uint32_t seen[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    seen[j] = (sc[t][j >> 1][2 * (j & 1)] != -__builtin_inff() ? one : 0u) |
-                              (sc[t][j >> 1][2 * (j & 1) + 1] != -__builtin_inff() ? one << 16 : 0u);
-                const f32x4_t c = Dec<0>::mfma(make_uint4(bad[0], bad[1], bad[2], bad[3]),
-                                               make_uint4(seen[0], seen[1], seen[2], seen[3]), f32x4_t{0, 0, 0, 0});
-                // o[t][n] with a runtime n: every n is compared, so that o stays in registers
-#pragma unroll
-                for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[t][d][r] = d == n && c[r] > 0.0f ? __builtin_nanf("") : o[t][d][r];
-            }
-        }
-    }
-
-    __device__ __forceinline__ uint4 v_frag(int n) const
-    {
-        uint4 v = frag(D / 16 + n);
-        if constexpr (BIAS == 0) {
-            if (clean) {
-                uint32_t* w = (uint32_t*)&v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = ((w[j] & 0x7FFFu) > 0x7F80u ? 0u : w[j] & 0xFFFFu) |
-                           ((w[j] >> 16 & 0x7FFFu) > 0x7F80u ? 0u : w[j] & 0xFFFF0000u);
-            }
-        }
-        return v;
+        if (groups & 4) mark_poisoned<NF, QT>(frag(2 * NF), sc, o);
     }
 
     template <int Y>
     __device__ __forceinline__ void v(uint4& lo, uint4& hi) const
     {
-        lo = v_frag(2 * Y);
-        hi = v_frag(2 * Y + 1);
+        lo = frag(NF + 2 * Y);
+        hi = frag(NF + 2 * Y + 1);
     }
 };
 
@@ -1016,7 +980,7 @@ struct DecodePart {
                 for (int t = 0; t < 4; ++t) {
                     const uint32_t at = (4 * q + t) * (D / 2) + m * (D / 32);
                     if constexpr (D == 64) b.w[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b16(c, at, 0, 0);
-                    else b.w[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b32(c, at + 4 * half, 0, 0);
+                    else b.w[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b32(c, at + (D == 256 ? 4 * half : 0), 0, 0);
                     b.s[4 * s + t] = __builtin_amdgcn_raw_buffer_load_b8(f, (4 * q + t) * (D / B) + m * (D / 16) / B, 0, 0);
                 }
             }
@@ -1056,22 +1020,29 @@ struct DecodePart {
         }
         uint32_t flag = there;
         if constexpr (BIAS == 0) {
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) bad |= b.s[j] == 0xFFu;
-            flag |= __any(bad) ? 4u : 0u;
+            uint4 bad;
+            if (poisoned_blocks(b.s, bad)) {
+                flag |= 4;
+                if (half == 0) put(2 * T::kFrags, bad);
+            }
         }
         if (lane == 0 && half == 0) *(__attribute__((address_space(3))) uint32_t*)(flags + step * 16) = flag;
         uint32_t sc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) sc[j] = X::scale(b.s[j]);
-        const int n0 = D / 16 + 8 * half;
+        // head_dim 128: a half's two bytes of the lane's word; 256: the lane's word of the half
+        constexpr int kBytes = D / 32 / kHalves;
+        if constexpr (D == 128 && kHalves == 2) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b.w[j] >>= 16 * half;
+        }
+        const int n0 = T::kFrags + 2 * kBytes * half;
         uint4 lo, hi;
         decode_v<BIAS, 0>(b.w, sc, lo, hi);
         put(n0, lo), put(n0 + 1, hi);
         decode_v<BIAS, 1>(b.w, sc, lo, hi);
         put(n0 + 2, lo), put(n0 + 3, hi);
-        if constexpr (D > 64) {
+        if constexpr (kBytes == 4) {
             decode_v<BIAS, 2>(b.w, sc, lo, hi);
             put(n0 + 4, lo), put(n0 + 5, hi);
             decode_v<BIAS, 3>(b.w, sc, lo, hi);
@@ -1081,7 +1052,7 @@ struct DecodePart {
 };
 
 template <int D, int BIAS>
-__global__ __launch_bounds__(512) void k_attn_tiles(AttnArgs a)
+__global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a)
 {
     using T = Tiles<D>;
     constexpr int QT = T::kQT;
@@ -1155,13 +1126,14 @@ __global__ __launch_bounds__(512) void k_attn_tiles(AttnArgs a)
                 part.decode(g0, at + T::kKeys + part.step * kStep, kv, now, lds + (buf ^ 1) * T::kRound,
                             flags + (buf ^ 1) * (T::kSteps * 16));
             }
+            if (my_end <= at || at + T::kKeys <= rows.first.lo) continue;   // nothing of this round is seen
 #pragma unroll 1
             for (int s = 0; s < T::kSteps; ++s) {
                 const int k = at + s * kStep;
-                if (k >= my_end || k + kStep <= rows.first.lo) continue;
+                if (k >= my_end) break;
+                FromLds<D, BIAS, QT> src{lds + buf * T::kRound + s * T::kStepBytes + lane * 16};
                 const uint32_t groups = __builtin_amdgcn_readfirstlane(
                     *(const __attribute__((address_space(3))) uint32_t*)(flags + buf * (T::kSteps * 16) + s * 16));
-                FromLds<D, BIAS, QT> src{lds + buf * T::kRound + s * T::kStepBytes + lane * 16};
                 attend_step<D, BIAS, QT>(src, groups, k, my_end, rows, lane, sum);
             }
         }
