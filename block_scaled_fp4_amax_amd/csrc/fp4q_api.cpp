@@ -803,6 +803,7 @@ int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k
     a.slots = slots;
     a.tokens = tokens;
     a.num_slots = a.kv.num_pages * a.kv.page_size;
+    a.per_page = make_div64((uint32_t)(a.kv.page_size / kKvGroup));
     return hip_status(launch_kv_append(r.bias, r.x_f32, a, (hipStream_t)stream));
 }
 
@@ -823,6 +824,7 @@ int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* 
     a.slots = slots;
     a.tokens = tokens;
     a.num_slots = a.kv.num_pages * a.kv.page_size;
+    a.per_page = make_div64((uint32_t)(a.kv.page_size / kKvGroup));
     return hip_status(launch_kv_read(r.bias, r.y_f32, a, (hipStream_t)stream));
 }
 

@@ -8,12 +8,14 @@
 // that is the target.
 //
 // Both move bytes: 2 per value on the 16-bit side and 1/2 + 1/block on the
-// cache's.  A workgroup takes one head and a run of tokens, so what it touches in
-// the cache is contiguous while the tokens' slots are (a page's rows of a head are),
-// and on the 16-bit side it touches runs of head_dim values.
+// cache's.  A workgroup of the writer takes one head and a run of tokens, so what it
+// writes is contiguous while the tokens' slots are (a page's rows of a head are):
+// 32768 tokens of 8 x 128 (170 MB, MXFP4) 36 us, 4.7 TB/s; all heads of the same
+// tokens side by side took 39.
 #include "fp4q_device.h"
 #include "kv_index.h"
 #include "launch.h"
+#include "mfma16.h"
 #include "nv_block.h"
 
 namespace fp4q {
@@ -21,6 +23,7 @@ namespace fp4q {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kReadHeads = 4;                            // neighbouring heads of a token that a lane of the reader takes
 
 // Scale exponent of an MXFP4 block from the binary32 bits of its largest
 // magnitude: the least k with amax <= 6 2^k, within [-126, 125].
@@ -73,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
     const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
     const int part = (int)threadIdx.x % lanes;
     if (token >= a.tokens) return;                         // whole rows leave together
-    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.kv.page_size, a.kv.heads, head);
+    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, head);
     if (row < 0) return;
     const char* x = (const char*)(is_v ? a.v : a.k);
     const int64_t ld = is_v ? a.ld_v : a.ld_k;
@@ -129,69 +132,76 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
     }
 }
 
+// Eight values a lane, so that a store of the wave writes whole rows of bf16, of four heads of a
+// token.  Measured: 131072 rows of 8 x 128 (689 MB, AMD-FP4) 140 us, 4.9 TB/s; the rows that 32768
+// tokens just wrote (MXFP4) 26 us.  Sixteen values a lane write half lines with each store: 133
+// and 43 us (non-temporal), 141 and 28 us (ordinary stores).
 template <int BIAS, bool YF32>
 __global__ __launch_bounds__(kThreads) void k_kv_read(KvReadArgs a)
 {
-    const int lanes = a.kv.dim >> 4;
-    const int head = (int)blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
+    const int lanes = a.kv.dim >> 3;
+    // neighbouring workgroups take all heads of the same tokens
+    const uint32_t groups = (uint32_t)(a.kv.heads + kReadHeads - 1) / kReadHeads;
+    const uint32_t run = blockIdx.x / groups;
+    const int head0 = (int)(blockIdx.x - run * groups) * kReadHeads;
+    const bool is_v = blockIdx.y != 0;
+    const int64_t token = (int64_t)run * (kThreads / lanes) + (int)threadIdx.x / lanes;
     const int part = (int)threadIdx.x % lanes;
     if (token >= a.tokens) return;
-    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.kv.page_size, a.kv.heads, head);
-    float y[16];
-    if (row < 0) {
+    const uint8_t* codes = is_v ? a.kv.v_codes : a.kv.k_codes;
+    const uint8_t* scales = is_v ? a.kv.v_scales : a.kv.k_scales;
+    const float* outer = is_v ? a.kv.v_outer : a.kv.k_outer;
+    constexpr int kBlock = BIAS == 0 ? 32 : 16;
+    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, head0);
+    uint32_t c[kReadHeads], sb[kReadHeads];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = 0.0f;
-    } else {
-        const uint8_t* codes = is_v ? a.kv.v_codes : a.kv.k_codes;
-        const uint8_t* scales = is_v ? a.kv.v_scales : a.kv.k_scales;
-        const uint2 c = *(const uint2*)(codes + row * (a.kv.dim / 2) + part * 8);
-        if constexpr (BIAS == 0) {
-            const uint32_t sb = scales[row * (a.kv.dim / 32) + part / 2];
-            decode16(c, sb == 0 ? 0x1p-127f : __uint_as_float(sb << 23), y);
-            if (sb == 0xFFu) {
+    for (int u = 0; u < kReadHeads; ++u) {               // rows that are not there read as zeros
+        const bool in = row >= 0 && head0 + u < a.kv.heads;
+        const int64_t r = row + (int64_t)u * a.kv.page_size;
+        c[u] = in ? *(const uint32_t*)(codes + r * (a.kv.dim / 2) + part * 4) : 0;
+        sb[u] = in ? scales[r * (a.kv.dim / kBlock) + part * 8 / kBlock] : 0;
+    }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(0x7FC00000u);
-            }
+    for (int u = 0; u < kReadHeads; ++u) {
+        const int head = head0 + u;
+        if (head >= a.kv.heads) return;
+        float d, y[8];
+        if constexpr (BIAS == 0) d = sb[u] == 0 ? 0x1p-127f : __uint_as_float(sb[u] << 23);
+        else d = DecBf16<BIAS>::scale(sb[u]);
+        decode_byte<0>(c[u], d, y[0], y[1]);
+        decode_byte<1>(c[u], d, y[2], y[3]);
+        decode_byte<2>(c[u], d, y[4], y[5]);
+        decode_byte<3>(c[u], d, y[6], y[7]);
+        if (BIAS != 0 && outer) {
+            const float s_o = outer[head];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= s_o;
+        }
+        if (BIAS == 0 && sb[u] == 0xFFu) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(0x7FC00000u);
+        }
+        const int64_t at = (token * a.kv.heads + head) * a.kv.dim + part * 8;
+        if (YF32) {
+            float* o = (float*)(is_v ? a.v : a.k) + at;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                st_nt16(o + 4 * i, make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                              __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])));
         } else {
-            const float* outer = is_v ? a.kv.v_outer : a.kv.k_outer;
-            decode16(c, scale_decode<BIAS>(scales[row * (a.kv.dim / 16) + part]), y);
-            if (outer) {
-                const float s_o = outer[head];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] *= s_o;
-            }
+            st_nt16((uint16_t*)(is_v ? a.v : a.k) + at,
+                    make_uint4(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]), Dec<0>::round2(y[4], y[5]),
+                               Dec<0>::round2(y[6], y[7])));
         }
     }
-    const int64_t at = (token * a.kv.heads + head) * a.kv.dim + part * 16;
-    if (YF32) {
-        float* o = (float*)(is_v ? a.v : a.k) + at;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st_nt16(o + 4 * i, make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
-                                          __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])));
-    } else {
-        uint16_t* o = (uint16_t*)(is_v ? a.v : a.k) + at;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = f32_to_bf16(y[2 * i]) | (f32_to_bf16(y[2 * i + 1]) << 16);
-        st_nt16(o, make_uint4(w[0], w[1], w[2], w[3]));
-        st_nt16(o + 8, make_uint4(w[4], w[5], w[6], w[7]));
-    }
-}
-
-dim3 kv_grid(const KvView& kv, int64_t tokens)
-{
-    const int rows = kThreads / (kv.dim >> 4);
-    return dim3((uint32_t)((tokens + rows - 1) / rows), (uint32_t)kv.heads, 2);
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(int bias, bool x_f32, const KvAppendArgs& a, hipStream_t s)
 {
-    const dim3 grid = kv_grid(a.kv, a.tokens);
+    const int rows = kThreads / (a.kv.dim / 16);
+    const dim3 grid((uint32_t)((a.tokens + rows - 1) / rows), (uint32_t)a.kv.heads, 2);
 #define FP4Q_APPEND(B)                                                                                  \
     do {                                                                                                \
         if (x_f32) hipLaunchKernelGGL((k_kv_append<B, true>), grid, dim3(kThreads), 0, s, a);           \
@@ -206,7 +216,8 @@ hipError_t launch_kv_append(int bias, bool x_f32, const KvAppendArgs& a, hipStre
 
 hipError_t launch_kv_read(int bias, bool y_f32, const KvReadArgs& a, hipStream_t s)
 {
-    const dim3 grid = kv_grid(a.kv, a.tokens);
+    const int rows = kThreads / (a.kv.dim / 8), groups = (a.kv.heads + kReadHeads - 1) / kReadHeads;
+    const dim3 grid((uint32_t)((a.tokens + rows - 1) / rows * groups), 2);
 #define FP4Q_READ(B)                                                                                    \
     do {                                                                                                \
         if (y_f32) hipLaunchKernelGGL((k_kv_read<B, true>), grid, dim3(kThreads), 0, s, a);             \

@@ -35,12 +35,33 @@ inline DivBy make_div(uint32_t d) { return DivBy{(((uint64_t)1 << 32) + d - 1) /
 
 FP4Q_HD uint32_t div_by(uint32_t u, const DivBy& k) { return (uint32_t)((u * k.m) >> 32); }
 
+// Exact g / d for any 64-bit g below 2^56 and d at most 256: the upper half of g M with M =
+// ceil(2^64 / d), by the argument above (d = 1 has no such M).  A 64-bit division in
+// each lane took most of the reader's time (131072 rows: 173 us).
+struct DivBy64 {
+    uint64_t m;
+    uint32_t d;
+};
+
+inline DivBy64 make_div64(uint32_t d) { return DivBy64{d > 1 ? ~(uint64_t)0 / d + 1 : 0, d}; }
+
+FP4Q_HD uint64_t div_by(uint64_t g, const DivBy64& k)
+{
+    if (k.d == 1) return g;
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __umul64hi(g, k.m);
+#else
+    return (uint64_t)(((unsigned __int128)g * k.m) >> 64);
+#endif
+}
+
 // Row of a slot (= page * page_size + place in the page) of one head: the row
 // number to multiply by the bytes of a row, or -1 for a slot outside the cache.
-FP4Q_HD int64_t kv_row_of_slot(int64_t slot, int64_t num_slots, int32_t page_size, int32_t heads, int32_t head)
+FP4Q_HD int64_t kv_row_of_slot(int64_t slot, int64_t num_slots, const DivBy64& groups_per_page, int32_t heads, int32_t head)
 {
     if (slot < 0 || slot >= num_slots) return -1;
-    const int64_t page = slot / page_size;
+    const int64_t page = (int64_t)div_by((uint64_t)slot / kKvGroup, groups_per_page);
+    const int32_t page_size = (int32_t)groups_per_page.d * kKvGroup;
     return (page * heads + head) * page_size + (slot - page * page_size);
 }
 

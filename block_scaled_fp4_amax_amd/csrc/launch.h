@@ -227,6 +227,7 @@ struct KvAppendArgs {
     int64_t ld_k, ld_v;
     const int64_t* slots;    // [tokens]
     int64_t tokens, num_slots;
+    DivBy64 per_page;        // 16-token groups of a page
 };
 
 struct KvReadArgs {
@@ -234,6 +235,7 @@ struct KvReadArgs {
     void *k, *v;             // bf16 or FP32 [tokens, heads, dim]
     const int64_t* slots;
     int64_t tokens, num_slots;
+    DivBy64 per_page;
 };
 
 // bias: 7 (E4M3), 15 (UE5M3) or 0 (MXFP4)

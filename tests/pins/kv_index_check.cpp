@@ -27,11 +27,18 @@ int main()
         for (uint32_t q = 1; q * d <= top && q < 4096; ++q)
             CHECK(div_by(q * d, k) == q && div_by(q * d - 1, k) == q - 1);
     }
+    for (uint32_t d = 1; d <= (uint32_t)kKvMaxPage / kKvGroup; ++d) {
+        const DivBy64 k = make_div64(d);
+        const uint64_t top = (uint64_t)1 << 43;                // pages below 2^31 of at most 4096 tokens
+        for (uint64_t q = 0; q < 3000; ++q)
+            for (uint64_t g : {q, top - q, q * d, q * d + d - 1, top / d * d - q * d, top / d * d - q * d - 1, q * 2862933555777941757u % top})
+                if (g <= top) CHECK(div_by(g, k) == g / d);
+    }
     // slots
     const int64_t big[] = {INT64_MIN, -((int64_t)1 << 40), -1, 0, 1, 47, 48, 49, 7 * 48 - 1, 7 * 48, INT64_MAX};
     for (int64_t slot : big)
         for (int h = 0; h < 3; ++h) {
-            const int64_t row = kv_row_of_slot(slot, 7 * 48, 48, 3, h);
+            const int64_t row = kv_row_of_slot(slot, 7 * 48, make_div64(48 / kKvGroup), 3, h);
             if (slot < 0 || slot >= 7 * 48) CHECK(row == -1);
             else CHECK(row == (slot / 48 * 3 + h) * 48 + slot % 48 && row < 7 * 3 * 48);
         }
