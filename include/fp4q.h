@@ -470,7 +470,8 @@ typedef struct {
  *   slots   int64 [tokens] device.  A slot below 0 or at or beyond num_pages *
  *           page_size writes nothing (padding).  A slot named twice in one call
  *           gets one of the rows, or parts of both.
- * NaN and infinities are treated as in fp4_quantize.
+ * NaN and infinities are treated as in fp4_quantize.  tokens <= 2^27
+ * (FP4Q_ERR_UNSUPPORTED).
  */
 int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k, int64_t ld_k, const void* v,
                   int64_t ld_v, const int64_t* slots, int64_t tokens, void* stream);
@@ -481,6 +482,8 @@ int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k
  *   k, v    bf16 or FP32 (cfg->output_dtype) [tokens, kv_heads, head_dim] device,
  *           contiguous, 16-byte aligned, written.
  *   slots   int64 [tokens] device; a slot outside the cache reads as zeros.
+ * tokens <= 2^27, and tokens * ceil(kv_heads / 4) * head_dim < 2^34
+ * (FP4Q_ERR_UNSUPPORTED).
  */
 int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                 void* stream);

@@ -161,6 +161,24 @@ def test_many_splits_and_bounds():
         s2.check()
 
 
+@pytest.mark.parametrize("H", [1, 3])
+def test_more_sequences_than_lanes(H):
+    """Batches past 64 and 128 sequences, keys cut into parts in some of them, several without
+    queries, and one of many rows."""
+    rng = np.random.default_rng(11)
+    lens = [int(n) for n in rng.integers(0, 40, 150)]
+    for b, n in ((0, 900), (63, 700), (64, 2500), (127, 1), (128, 1300), (149, 3000)):
+        lens[b] = n
+    ql = [1] * 150
+    for b in (5, 62, 65, 148):
+        ql[b] = 0
+    s = Setup("nvfp4", 64, H, 4, 16, lens, ql, extra_cols=3).device()
+    s.check(max_q=1)
+    ql[64], ql[149] = 9, 8
+    s = Setup("mxfp4", 64, H, 4, 16, lens, ql, extra_cols=3).device()
+    s.check(max_q=9)
+
+
 def test_counts_beyond_the_bounds_are_cut():
     s = Setup("nvfp4", 64, 1, 2, 16, [64, 32], [1, 1]).device()
     full = s.kv_lens.copy()

@@ -95,6 +95,7 @@ def test_append_and_read_rules():
     assert append(cfg=fq.make_cfg(input_dtype="fp32"), ld_k=130) == fq.ERR_ALIGN
     assert append(tokens=(1 << 27) + 1) == fq.ERR_UNSUPPORTED and read(tokens=(1 << 27) + 1) == fq.ERR_UNSUPPORTED
     assert append(ld_k=1 << 32) == fq.ERR_UNSUPPORTED
+    assert read(c=cache(kv_heads=64), tokens=1 << 26) == fq.ERR_UNSUPPORTED
     for n in ("k", "v", "slots"):
         assert append(**{n: None}) == fq.ERR_NULL and read(**{n: None}) == fq.ERR_NULL
         assert append(**{n: MIS}) == fq.ERR_ALIGN and read(**{n: MIS}) == fq.ERR_ALIGN
