@@ -1,18 +1,17 @@
 // kernels_linear.hip -- y = x W^T with bf16 activations and a 4-bit weight.
 //
-// A wave computes 16 MT rows of y (columns of the product) by 16 NT of its columns, on
-// v_mfma_f32_16x16x32_bf16 with W as the A operand (rows) and x as B (columns):
-//   y^T[n, m] = sum_k W[n, k] x[m, k].
-// A step covers 64 values of K in two products; lane l holds, of row l % 16 of either
-// operand, the values 64 s + 16 (l / 16) .. + 15: eight bytes of codes under one
-// inner scale, and 32 bytes of x.  One row through 2880 x 2880 takes 5.2 us, of
-// which a launch and one trip to memory are most.  W is decoded in registers to bf16, exactly
+// Rows of W are the A operand and rows of x the B operand of v_mfma_f32_16x16x32_bf16,
+//   y^T[n, m] = sum_k W[n, k] x[m, k],
+// 16 of each a product.  A step covers 64 values of K in two products; lane l holds, of row
+// l % 16 of either operand, the values 64 s + 16 (l / 16) .. + 15: eight bytes of codes under
+// one inner scale, and 32 bytes of x.  W is decoded in registers to bf16, exactly
 // (mfma16.h), so the products are exact and the sums binary32.  Where W has outer
 // scales per 64 (or more) values of K, the two products of a step start from
 // zero and the outer scale multiplies their sum into the accumulator.
 //
-// The waves of a workgroup share the tile and take every KS-th pair of steps; their sums
-// are joined through LDS in a fixed order.
+// Small weights under at most 16 rows of x (k_linear): a workgroup takes 16 rows of W, its eight
+// waves every eighth pair of steps, and joins them through LDS in a fixed order.  One row through
+// 2880 x 2880 takes 5.2 us, of which a launch and one trip to memory are most.
 #include "fp4q_device.h"
 #include "launch.h"
 #include "lds_load.h"
@@ -53,105 +52,85 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t r, int c, f3
     }
 }
 
+// Weights that k_linear takes.  Cold weights, 1 and 16 rows, MXFP4 (k_linear / tiles): 2880 x 2880 5.1, 6.2 /
+// 9.1, 9.7 us; 4096 x 4096 7.6, 9.9 / 9.5, 10.1; 8192 x 4096 13.2, 17.4 / 10.9, 11.3; 8192 x
+// 8192 22.9, 32.0 / 14.8, 14.9.
 constexpr int64_t kSmallWeight = (int64_t)1 << 24;
 constexpr int kPair = 128;                               // values of K of a pair of steps
 
-template <int BIAS, int NT>
+// A lane's codes and scale bytes of a pair of steps.
 struct WRaw {
-    uint2 c[NT][2];
-    uint32_t s[NT][2];
+    uint2 c[2];
+    uint32_t s[2];
 };
 
-template <int BIAS, int MT, int NT, int OUTER, int KS>
-__global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
+constexpr int kSmallWaves = 8;
+
+template <int BIAS, int OUTER>
+__global__ __launch_bounds__(64 * kSmallWaves) void k_linear(LinearArgs a)
 {
     constexpr int B = Dec<BIAS>::kBlock;
-    __shared__ float join[KS / 2][MT * NT * 4][64];
+    __shared__ float join[kSmallWaves / 2][4][64];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int row = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * (16 * NT), m0 = (int)blockIdx.y * (16 * MT);
-
-    f32x4_t acc[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+    const int n0 = (int)blockIdx.x * 16;
 
     // rows of W beyond N repeat the last one; their results are not stored
-    const uint8_t *wc[NT], *ws[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int64_t r = min(n0 + 16 * n + row, a.N - 1);
-        wc[n] = a.codes + r * (a.K / 2) + quarter * 8;
-        ws[n] = a.scales + r * (a.K / B) + (B == 16 ? quarter : quarter >> 1);
-    }
-    const uint16_t* xr[MT];
-    bool live[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        live[m] = m0 + 16 * m + row < a.M;
-        xr[m] = a.x + (int64_t)(live[m] ? m0 + 16 * m + row : 0) * a.ld_x + quarter * 16;
-    }
+    const int64_t r0 = min(n0 + row, a.N - 1);
+    const uint8_t* const wc = a.codes + r0 * (a.K / 2) + quarter * 8;
+    const uint8_t* const ws = a.scales + r0 * (a.K / B) + (B == 16 ? quarter : quarter >> 1);
+    const bool live = row < a.M;
+    const uint16_t* const xr = a.x + (int64_t)(live ? row : 0) * a.ld_x + quarter * 16;
 
     // Lanes whose 16 values lie beyond K (K % 64 == 32: half a step; the second step of a last
     // pair) take zeros for both operands.
-    auto load_w = [&](int k0, WRaw<BIAS, NT>& w) {
+    auto load_w = [&](int k0, WRaw& w) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int k = k0 + 64 * s;
             const bool in = k + 16 * quarter < a.K;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                w.c[n][s] = in ? *(const uint2*)(wc[n] + k / 2) : make_uint2(0, 0);
-                w.s[n][s] = in ? ws[n][k / B] : 0;
-            }
+            w.c[s] = in ? *(const uint2*)(wc + k / 2) : make_uint2(0, 0);
+            w.s[s] = in ? ws[k / B] : 0;
         }
     };
 
+    f32x4_t acc = {0, 0, 0, 0};
     int k = wave * kPair;
-    WRaw<BIAS, NT> cur;
+    WRaw cur;
     if (k < a.K) load_w(k, cur);
-    for (; k < a.K; k += KS * kPair) {
-        WRaw<BIAS, NT> nxt;
-        load_w(k + KS * kPair, nxt);
-        uint4 x[MT][2][2];
+    for (; k < a.K; k += kSmallWaves * kPair) {
+        WRaw nxt;
+        load_w(k + kSmallWaves * kPair, nxt);
+        uint4 x[2][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const bool in = live[m] && k + 64 * s + 16 * quarter < a.K;
-                const uint4* p = (const uint4*)(xr[m] + k + 64 * s);
-                x[m][s][0] = in ? p[0] : make_uint4(0, 0, 0, 0);
-                x[m][s][1] = in ? p[1] : make_uint4(0, 0, 0, 0);
-            }
+        for (int s = 0; s < 2; ++s) {
+            const bool in = live && k + 64 * s + 16 * quarter < a.K;
+            const uint4* p = (const uint4*)(xr + k + 64 * s);
+            x[s][0] = in ? p[0] : make_uint4(0, 0, 0, 0);
+            x[s][1] = in ? p[1] : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             if (OUTER != kInnerOnly && k + 64 * s >= a.K) break;
+            const float sc = DecBf16<BIAS>::scale(cur.s[s]);
+            const uint4 w0 = DecBf16<BIAS>::octet(cur.c[s].x, sc), w1 = DecBf16<BIAS>::octet(cur.c[s].y, sc);
+            f32x4_t so;
+            if constexpr (OUTER == kPerTile) {
+                const float v = a.outer[(min(n0, a.N - 1) >> 6) * a.outer_n + ((k + 64 * s) >> 6) * a.outer_k];
+                so = f32x4_t{v, v, v, v};
+            } else if constexpr (OUTER == kPerRow) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float sc = DecBf16<BIAS>::scale(cur.s[n][s]);
-                const uint4 w0 = DecBf16<BIAS>::octet(cur.c[n][s].x, sc), w1 = DecBf16<BIAS>::octet(cur.c[n][s].y, sc);
-                f32x4_t so;
-                if constexpr (OUTER == kPerTile) {
-                    const float v = a.outer[(min(n0 + 16 * n, a.N - 1) >> 6) * a.outer_n + ((k + 64 * s) >> 6) * a.outer_k];
-                    so = f32x4_t{v, v, v, v};
-                } else if constexpr (OUTER == kPerRow) {
+                for (int r = 0; r < 4; ++r)
+                    so[r] = a.outer[min(n0 + 4 * quarter + r, a.N - 1) * a.outer_n + (k + 64 * s) / a.obs];
+            }
+            f32x4_t p = OUTER == kInnerOnly ? acc : f32x4_t{0, 0, 0, 0};
+            p = Dec<0>::mfma(w0, x[s][0], p);
+            p = Dec<0>::mfma(w1, x[s][1], p);
+            if constexpr (OUTER == kInnerOnly) {
+                acc = p;
+            } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        so[r] = a.outer[min(n0 + 16 * n + 4 * quarter + r, a.N - 1) * a.outer_n + (k + 64 * s) / a.obs];
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    f32x4_t p = OUTER == kInnerOnly ? acc[m][n] : f32x4_t{0, 0, 0, 0};
-                    p = Dec<0>::mfma(w0, x[m][s][0], p);
-                    p = Dec<0>::mfma(w1, x[m][s][1], p);
-                    if constexpr (OUTER == kInnerOnly) {
-                        acc[m][n] = p;
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[m][n][r] = __builtin_fmaf(p[r], so[r], acc[m][n][r]);
-                    }
-                }
+                for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(p[r], so[r], acc[r]);
             }
         }
         cur = nxt;
@@ -159,34 +138,20 @@ __global__ __launch_bounds__(64 * KS) void k_linear(LinearArgs a)
 
     // join the waves: the upper half of those left into the lower half
 #pragma unroll
-    for (int half = KS / 2; half >= 1; half >>= 1) {
+    for (int half = kSmallWaves / 2; half >= 1; half >>= 1) {
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) join[wave - half][(m * NT + n) * 4 + r][lane] = acc[m][n][r];
+            for (int r = 0; r < 4; ++r) join[wave - half][r][lane] = acc[r];
         }
         __syncthreads();
         if (wave < half) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[m][n][r] += join[wave][(m * NT + n) * 4 + r][lane];
+            for (int r = 0; r < 4; ++r) acc[r] += join[wave][r][lane];
         }
         __syncthreads();
     }
-    if (wave != 0) return;
-    const float whole = a.outer_kind == kOuterTensor ? a.outer[0] : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (!live[m]) continue;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) store4(a, m0 + 16 * m + row, n0 + 16 * n + 4 * quarter, acc[m][n] * whole);
-    }
+    if (wave != 0 || !live) return;
+    store4(a, row, n0 + 4 * quarter, acc * (a.outer_kind == kOuterTensor ? a.outer[0] : 1.0f));
 }
 
 // ---------------------------------------------------------------- tiles
@@ -441,8 +406,7 @@ template <int BIAS, int OUTER>
 hipError_t launch_outer(const LinearArgs& a, hipStream_t s)
 {
     if (a.splits == 0) {
-        hipLaunchKernelGGL((k_linear<BIAS, 1, 1, OUTER, 8>), dim3((uint32_t)((a.N + 15) / 16), (uint32_t)((a.M + 15) / 16)),
-                           dim3(512), 0, s, a);
+        hipLaunchKernelGGL((k_linear<BIAS, OUTER>), dim3((uint32_t)((a.N + 15) / 16)), dim3(64 * kSmallWaves), 0, s, a);
         return hipGetLastError();
     }
     if (a.M <= 16) return launch_tile<BIAS, 1, OUTER != kInnerOnly>(a, s);

@@ -526,11 +526,14 @@ typedef struct {
  * as in the products.
  * K and V enter the products exactly; the weights of V are rounded to bf16 (MXFP4)
  * or FP16 (NVFP4, AMD-FP4: weights below 2^-14 of a row's largest are then multiples of
- * 2^-24 of it) before they are multiplied and summed; everything else is binary32.
+ * 2^-24 of it) before they are multiplied and summed; everything else is binary32,
+ * but that NVFP4 and AMD-FP4 caches keep of a query's values what lies above 2^-38 of its
+ * largest.
  * workspace: fp4q_attn_workspace_bytes() bytes (0 for calls whose keys are not
  * split), 16-byte aligned.  It needs no initial value and holds nothing between
- * calls.  The result depends on the split, which depends on batch, max_q, max_kv,
- * window and the heads alone, so equal calls give equal bits.
+ * calls.  How keys are shared among workgroups, and so the last bits of a result,
+ * depends on the bounds, the heads and the sequences' lengths alone: equal calls give
+ * equal bits.
  * Limits (FP4Q_ERR_UNSUPPORTED): max_kv <= 2^27, batch <= 65535, max_q * q_heads /
  * kv_heads <= 2^22, total_q * q_heads < 2^31.
  */
