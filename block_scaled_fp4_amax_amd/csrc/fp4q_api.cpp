@@ -766,7 +766,8 @@ int check_attn(const KvView& kv, const fp4q_attn* a)
     if (!(a->scale > 0.0f) || a->scale > 3.4028235e38f) return FP4Q_ERR_MODE;
     if (a->max_kv > kKvMaxTokens || (int64_t)a->table_cols * kv.page_size >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
     const int64_t rows = (int64_t)a->max_q * (a->q_heads / kv.heads);
-    if (rows > ((int64_t)1 << 22) || a->batch > 65535 || (int64_t)a->total_q * a->q_heads >= (int64_t)1 << 31)
+    if (rows > ((int64_t)1 << 22) || a->batch > 65535 || (int64_t)a->batch * kv.heads >= (int64_t)1 << 24 ||
+        (int64_t)a->total_q * a->q_heads >= (int64_t)1 << 31)
         return FP4Q_ERR_UNSUPPORTED;
     return FP4Q_OK;
 }

@@ -1260,6 +1260,7 @@ static void plan_few(AttnPlan& p, const KvView& kv, int64_t batch, int64_t rows,
     const int64_t heads = batch * kv.heads;
     p.groups = (int32_t)heads;
     if (keys <= kUnit * kMinShare || heads >= 2 * slots) return;
+    if (heads * (keys / kUnit + 2) >= (int64_t)1 << 30) return;   // units are counted in 32 bits
     // no share makes more parts than these: a part is a share, or the last of its sequence
     const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
     const int64_t parts = std::min(per_head + batch, batch * ((keys / kUnit + 2) / kMinShare + 1));
@@ -1285,7 +1286,7 @@ AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_h
     const int64_t tile = kv.dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows;
     const int64_t blocks = batch * kv.heads * ((rows + tile - 1) / tile);
     const int64_t want = std::min({256 / blocks, keys / 512, (int64_t)kMaxSplits, 65535 / batch});
-    if (want <= 1) return p;
+    if (want <= 1 || total_q * q_heads >= (int64_t)1 << 26) return p;   // rows of one launch of the join
     p.splits = (int32_t)want;
     p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);
     const size_t n = (size_t)want * total_q * q_heads;

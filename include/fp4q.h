@@ -534,8 +534,8 @@ typedef struct {
  * calls.  How keys are shared among workgroups, and so the last bits of a result,
  * depends on the bounds, the heads and the sequences' lengths alone: equal calls give
  * equal bits.
- * Limits (FP4Q_ERR_UNSUPPORTED): max_kv <= 2^27, batch <= 65535, max_q * q_heads /
- * kv_heads <= 2^22, total_q * q_heads < 2^31.
+ * Limits (FP4Q_ERR_UNSUPPORTED): max_kv <= 2^27, batch <= 65535, batch * kv_heads <
+ * 2^24, max_q * q_heads / kv_heads <= 2^22, total_q * q_heads < 2^31.
  */
 size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn);
 int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,

@@ -115,6 +115,7 @@ def test_attention_rules():
     for kw in (dict(max_kv=(1 << 27) + 1), dict(table_cols=1 << 27), dict(batch=65536), dict(max_q=1 << 22),
                dict(total_q=1 << 30)):
         assert attn(**kw) == fq.ERR_UNSUPPORTED, kw
+    assert attn(c=cache(kv_heads=4096), q_heads=4096, batch=4096, ld_q=1 << 20) == fq.ERR_UNSUPPORTED
     for n in ("q", "kv_lens", "out", "page_table"):
         assert attn(**{n: None}) == fq.ERR_NULL
     for n in ("q", "out"):
@@ -131,6 +132,26 @@ def test_attention_rules():
     assert attn(ws=FAKE, wsb=need - 1, **long) == fq.ERR_WORKSPACE
     assert attn(ws=MIS, wsb=need, **long) == fq.ERR_ALIGN
     assert fq.lib().fp4q_attn_workspace_bytes(ct.byref(fq.make_cfg()), ct.byref(cache()), ct.byref(args(batch=-1))) == 0
+
+
+@no_gpu
+def test_attention_workspace_at_the_ends():
+    """Scratch is bounded by what the chip holds, and a call whose units or rows would pass the
+    counters does without it."""
+    def need(c=None, **kw):
+        return fq.lib().fp4q_attn_workspace_bytes(ct.byref(fq.make_cfg()), ct.byref(c if c is not None else cache()),
+                                                  ct.byref(args(**kw)))
+    one = dict(max_q=1, q_starts=FAKE)
+    assert need(max_kv=512, table_cols=32, **one) == 0
+    assert need(max_kv=8192, table_cols=512, batch=1024, total_q=1024, **one) == 0       # heads fill the chip
+    for n in (1, 7, 64, 500):
+        assert 0 < need(max_kv=1 << 27, table_cols=1 << 23, batch=n, total_q=n, **one) < 1 << 28
+    # 1000 sequences of 2^27 keys: 2^31 units
+    assert need(max_kv=1 << 27, table_cols=1 << 23, batch=1000, total_q=1000, **one) == 0
+    # rows of many, split: scratch follows the tensor, until one launch cannot join it
+    many = dict(max_q=64, batch=1, max_kv=1 << 20, table_cols=1 << 16)
+    assert need(total_q=64, **many) > 0
+    assert need(total_q=1 << 25, **many) == 0
 
 
 def test_binding_refuses_host_tensors_and_bad_shapes():
