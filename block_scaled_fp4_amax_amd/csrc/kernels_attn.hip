@@ -48,7 +48,6 @@ constexpr int kWaves = 4;
 constexpr int kUnit = 128;                               // keys that a workgroup of few rows takes at once
 constexpr int kMinShare = 4;                             // units of a workgroup's share, at least
 constexpr int kFewRows = 32;
-constexpr int kMaxSplits = 64;
 constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
@@ -889,9 +888,9 @@ template <int D>
 struct Tiles {
     static constexpr int kWaves = 8;
     static constexpr int kQT = 1;
-    static constexpr int kRows = kWaves * 16 * kQT;
-    static constexpr int kSteps = D == 64 ? 4 : 2;       // of 32 keys, a round
-    static constexpr int kKeys = kSteps * kStep;
+    static constexpr int kKeys = kv_round(D);            // of a round
+    static constexpr int kSteps = kKeys / kStep;
+    static_assert(kWaves * 16 * kQT == kTileRows, "a workgroup's rows");
     static constexpr int kFrags = D / 16;                // operands of K, and of V, a step
     static constexpr int kStepBytes = (2 * kFrags + 1) * 1024;   // and which blocks of V are poisoned (MXFP4)
     static constexpr int kRound = kSteps * kStepBytes;
@@ -1077,17 +1076,17 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     if (count <= kFewRows && a.batch > 1) return;        // k_attn_few's
     // the last rows, which see the most keys, first
     const int block = (int)(gridDim.y - 1 - blockIdx.y);
-    if (block * T::kRows >= count) return;
-    const int row0 = block * T::kRows + wave * (16 * QT);
+    if (block * kTileRows >= count) return;
+    const int row0 = block * kTileRows + wave * (16 * QT);
     Rows<D, BIAS, QT> rows;
     Sums<D, QT> sum;
     rows.load(a, qr, kv, head, row0, lane);
     sum.clear();
     // keys of the workgroup's rows (this split's part) and of the wave's
-    const KeyRange kf = key_range(block * T::kRows / a.group, qr.count, kv, a.causal, a.window);
-    const KeyRange kl = key_range((min((block + 1) * T::kRows, count) - 1) / a.group, qr.count, kv, a.causal, a.window);
-    const int begin = kf.lo / T::kKeys * T::kKeys + split * a.chunk;
-    const int end = min(kl.hi, begin + a.chunk);
+    const KeyRange kf = key_range(block * kTileRows / a.group, qr.count, kv, a.causal, a.window);
+    const KeyRange kl = key_range((min((block + 1) * kTileRows, count) - 1) / a.group, qr.count, kv, a.causal, a.window);
+    const KeyRange mine = tile_part(kf, kl, T::kKeys, split, a.chunk);
+    const int begin = mine.lo, end = mine.hi;
     const int my_end = row0 < count ? min(rows.last.hi, end) : 0;
 
     const DecodePart<D, BIAS> part(a.kv, wave, lane);
@@ -1230,7 +1229,7 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
     static const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tiles<D, BIAS>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
     if (st != hipSuccess) return st;
-    const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + T::kRows - 1) / T::kRows), (uint32_t)(a.batch * a.splits));
+    const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
     hipLaunchKernelGGL((k_attn_tiles<D, BIAS>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
     if (a.splits > 1) {
         const int64_t all = (int64_t)a.total_q * a.q_heads;
@@ -1277,19 +1276,16 @@ AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_h
     AttnPlan p{1, 1 << 30, 0, 0, 0, 0, 0, 0};
     const int64_t rows = max_q * (q_heads / kv.heads);
     if (rows == 0 || batch == 0) return p;
-    // keys that one tile of rows can see
-    int64_t keys = std::min(max_kv, table_cols * kv.page_size);
-    if (window) keys = std::min(keys, window + max_q + kStep);
+    const int64_t all = std::min(max_kv, table_cols * kv.page_size);
+    // keys that the rows of few can see: their walk starts at the step of the first
+    const int64_t keys = window ? std::min(all, window + max_q + kStep) : all;
     if (rows <= kFewRows || batch > 1) plan_few(p, kv, batch, std::min<int64_t>(rows, kFewRows), keys);
     if (rows <= kFewRows) return p;
-    // Tiles of rows fill the chip by themselves or split the keys until they do once.
-    const int64_t tile = kv.dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows;
-    const int64_t blocks = batch * kv.heads * ((rows + tile - 1) / tile);
-    const int64_t want = std::min({256 / blocks, keys / 512, (int64_t)kMaxSplits, 65535 / batch});
-    if (want <= 1 || total_q * q_heads >= (int64_t)1 << 26) return p;   // rows of one launch of the join
-    p.splits = (int32_t)want;
-    p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);
-    const size_t n = (size_t)want * total_q * q_heads;
+    const TilePlan t = plan_tiles(batch, kv.heads, q_heads / kv.heads, max_q, all, window, kv.dim);
+    if (t.splits == 1 || total_q * q_heads >= (int64_t)1 << 26) return p;   // rows of one launch of the join
+    p.splits = t.splits;
+    p.chunk = t.chunk;
+    const size_t n = (size_t)t.splits * total_q * q_heads;
     p.ml = n * 2 * sizeof(float);
     p.o = n * kv.dim * sizeof(float);
     return p;

@@ -134,4 +134,45 @@ FP4Q_HD KeyRange key_range(int32_t i, int32_t n, int32_t kv, int32_t causal, int
     return KeyRange{lo, hi};
 }
 
+// ---------------------------------------------------------------- keys of many rows
+// A workgroup of many rows walks the keys of its rows in rounds of kv_round(head_dim) keys, from the
+// round of the first row's first key.  Its keys may be cut into `splits` parts of `chunk` keys (a
+// multiple of every round), one a workgroup.
+constexpr int kTileRows = 128;           // rows (queries times heads of a group) of a workgroup
+constexpr int kMaxSplits = 64;
+
+FP4Q_HD constexpr int kv_round(int head_dim) { return head_dim == 64 ? 128 : 64; }
+
+// Part `split` of the keys from the first row's range to the last row's; hi <= lo where it has none.
+FP4Q_HD KeyRange tile_part(const KeyRange& first, const KeyRange& last, int32_t round, int32_t split, int32_t chunk)
+{
+    const int32_t lo = first.lo / round * round + split * chunk;
+    return KeyRange{lo, last.hi < lo + chunk ? last.hi : lo + chunk};
+}
+
+struct TilePlan {
+    int32_t splits, chunk;
+};
+
+// How the keys of many rows are cut, for sequences of up to max_q queries and `keys` keys.  Tiles of
+// rows fill the chip by themselves, or their keys are split until they do once.
+inline TilePlan plan_tiles(int64_t batch, int64_t heads, int64_t group, int64_t max_q, int64_t keys, int64_t window,
+                           int head_dim)
+{
+    TilePlan p{1, 1 << 30};
+    // a window's keys: those of the first row, one more for each later query, and what the start is
+    // rounded down by
+    const int64_t span = window + max_q - 1 + kv_round(head_dim) - 1;
+    if (window > 0 && span < keys) keys = span;
+    const int64_t blocks = batch * heads * ((max_q * group + kTileRows - 1) / kTileRows);
+    int64_t want = blocks > 0 ? 256 / blocks : 1;
+    if (want > keys / 512) want = keys / 512;
+    if (want > kMaxSplits) want = kMaxSplits;
+    if (batch > 0 && want > 65535 / batch) want = 65535 / batch;
+    if (want <= 1) return p;
+    p.splits = (int32_t)want;
+    p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);
+    return p;
+}
+
 }  // namespace fp4q
