@@ -296,6 +296,14 @@ __device__ __forceinline__ void write_joined(const AttnArgs& a, int64_t row, int
     if (a.lse && lane == 0) a.lse[row] = lse;
 }
 
+// A scale byte of V that some rows see and others do not, as one whose products are finite (0 times it is then 0):
+// E4M3 has no codes above 0x7F, which FP16 would read as infinity or NaN.
+template <int BIAS>
+__device__ __forceinline__ uint32_t finite_scale(uint32_t byte)
+{
+    return BIAS == 7 ? byte & 0x7Fu : byte;
+}
+
 // MXFP4 keys some rows see and others do not, with a poisoned block of V: 0 times
 // its NaN would reach the rows that do not see the key.  Such blocks are cleared,
 // and the product of (block is poisoned) with (row sees the key) says which
@@ -420,8 +428,8 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
     }
 
     // A step whose keys are not all seen by all rows: scores of unseen keys are
-    // -infinity.  V of keys that are not there (whose bytes may be anything) is
-    // cleared, so that 0 times it is 0.
+    // -infinity.  V of keys that are not there, or that come before every row's window (their
+    // bytes may be anything), is cleared, so that 0 times it is 0.
     const bool whole = (groups & 3) == 3 && at >= rows.last.lo && at + kStep <= rows.first.hi && at + kStep <= end;
     if (!whole) {
 #pragma unroll
@@ -429,7 +437,7 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int key = at + 16 * s + 4 * quarter + r;
-                const bool there = (groups >> s & 1) && key < end;
+                const bool there = (groups >> s & 1) && key >= rows.first.lo && key < end;
 #pragma unroll
                 for (int t = 0; t < QT; ++t)
                     if (!there || key < rows.see[t].lo || key >= rows.see[t].hi) sc[t][s][r] = -__builtin_inff();
@@ -521,7 +529,7 @@ struct FromRaw {
         return Dec<BIAS>::octet(raw.k[s][i], Dec<BIAS>::scale(byte));
     }
 
-    __device__ __forceinline__ void keep(int j, bool there) { vs[j] = there ? vs[j] : 0; }
+    __device__ __forceinline__ void keep(int j, bool there) { vs[j] = there ? finite_scale<BIAS>(vs[j]) : 0; }
 
     __device__ __forceinline__ void poison(uint32_t, bool whole, const f32x4_t (&sc)[QT][2], f32x4_t (&o)[QT][D / 16])
     {
@@ -995,8 +1003,10 @@ struct DecodePart {
     }
 
     // Writes the operands of the step at `at` to the round's LDS, and the step's flags: which groups are there,
-    // and (bit 2) whether V has a poisoned block.
-    __device__ __forceinline__ void decode(const int64_t (&row)[2], int at, int kv, Bytes& b, lds_t* round, lds_t* flags) const
+    // and (bit 2) whether V has a poisoned block.  seen: the keys that some row of the workgroup sees; V of others
+    // is cleared (attend_step).
+    __device__ __forceinline__ void decode(const int64_t (&row)[2], int at, const KeyRange& seen, Bytes& b, lds_t* round,
+                                           lds_t* flags) const
     {
         using X = Dec<BIAS>;
         lds_t* to = round + step * T::kStepBytes + lane * 16;
@@ -1018,11 +1028,13 @@ struct DecodePart {
             return;
         }
         const uint32_t there = (row[0] >= 0 ? 1u : 0u) | (row[1] >= 0 ? 2u : 0u);
-        if (there != 3 || at + kStep > kv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b.s[j] = finite_scale<BIAS>(b.s[j]);
+        if (there != 3 || at < seen.lo || at + kStep > seen.hi) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int key = at + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
-                if (!(there >> (j >> 2) & 1) || key >= kv) b.s[j] = 0;
+                if (!(there >> (j >> 2) & 1) || key < seen.lo || key >= seen.hi) b.s[j] = 0;
             }
         }
         uint32_t flag = there;
@@ -1085,7 +1097,7 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     // keys of the workgroup's rows (this split's part) and of the wave's
     const KeyRange kf = key_range(block * kTileRows / a.group, qr.count, kv, a.causal, a.window);
     const KeyRange kl = key_range((min((block + 1) * kTileRows, count) - 1) / a.group, qr.count, kv, a.causal, a.window);
-    const KeyRange mine = tile_part(kf, kl, T::kKeys, split, a.chunk);
+    const KeyRange seen{kf.lo, kl.hi}, mine = tile_part(kf, kl, T::kKeys, split, a.chunk);
     const int begin = mine.lo, end = mine.hi;
     const int my_end = row0 < count ? min(rows.last.hi, end) : 0;
 
@@ -1121,7 +1133,7 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
         part.load(g0, now);
         next_rows(g1);
         part.load(g1, next);
-        part.decode(g0, begin + part.step * kStep, kv, now, lds, flags);
+        part.decode(g0, begin + part.step * kStep, seen, now, lds, flags);
         int buf = 0;
         for (int at = begin; at < end; at += T::kKeys, buf ^= 1) {
             lds_barrier();                               // this round is decoded, the other one's place is free
@@ -1130,7 +1142,7 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
             if (at + T::kKeys < end) {
                 next_rows(g1);
                 part.load(g1, next);
-                part.decode(g0, at + T::kKeys + part.step * kStep, kv, now, lds + (buf ^ 1) * T::kRound,
+                part.decode(g0, at + T::kKeys + part.step * kStep, seen, now, lds + (buf ^ 1) * T::kRound,
                             flags + (buf ^ 1) * (T::kSteps * 16));
             }
             if (my_end <= at || at + T::kKeys <= rows.first.lo) continue;   // nothing of this round is seen

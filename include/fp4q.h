@@ -522,7 +522,9 @@ typedef struct {
  * are cut to table_cols * page_size; a page number outside the cache makes its keys
  * absent (page table entries beyond a sequence's keys are not read).  Rows of q that
  * belong to no sequence are not written.  What unseen keys hold never reaches
- * a result; an MXFP4 block poisoned by NaN makes the rows that see its key NaN,
+ * a result (but MXFP4 scale bytes 253 and 254, which fp4_kv_append does not write, with
+ * values of 2^128 and more: they are infinite, and at a key that some queries see they make
+ * others NaN); an MXFP4 block poisoned by NaN makes the rows that see its key NaN,
  * as in the products.
  * K and V enter the products exactly; the weights of V are rounded to bf16 (MXFP4)
  * or FP16 (NVFP4, AMD-FP4: weights below 2^-14 of a row's largest are then multiples of
