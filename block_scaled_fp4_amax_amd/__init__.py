@@ -560,6 +560,8 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, wor
     if x.dim() != 2 or codes.dim() != 2:
         raise ValueError("x and the weight's codes must be 2-D")
     (M, K), N = x.shape, codes.shape[0]
+    if codes.element_size() != 1 or scales.element_size() != 1:
+        raise ValueError("codes and scales must hold bytes, got %s and %s" % (codes.dtype, scales.dtype))
     if codes.shape[1] * 2 != K:
         raise ValueError("x and the weight disagree on K (%d vs %d)" % (K, codes.shape[1] * 2))
     if K > 1 and x.stride(1) != 1:
