@@ -641,6 +641,13 @@ def _ints(t, dtype, rows, cols, what, device):
         raise ValueError("%s must be contiguous and on %s" % (what, device))
 
 
+def _ints32(where, *values):
+    """The structures' 32-bit fields would take larger integers modulo 2^32."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7FFFFFFF:
+            raise Fp4Error(ERR_UNSUPPORTED, "%s: %d" % (where, v))
+
+
 class KVCache:
     """The paged 4-bit cache of one layer's keys and values (layout and rules
     in include/fp4q.h): uint8 codes [pages, kv_heads, page_size, head_dim / 2]
@@ -734,10 +741,11 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
         raise ValueError("give max_kv or table_cols")
     if table_cols is None:
         table_cols = -(-int(max_kv) // cache.page_size)
-    a = _Attn(batch=int(batch), total_q=int(total_q), q_heads=int(q_heads), table_cols=int(table_cols),
-              max_q=int(total_q if max_q is None else max_q),
-              max_kv=int(table_cols * cache.page_size if max_kv is None else max_kv), causal=1, window=int(window),
-              scale=1.0, ld_q=int(q_heads) * cache.head_dim, q_starts=16)
+    n = [int(v) for v in (batch, total_q, q_heads, table_cols, total_q if max_q is None else max_q,
+                          table_cols * cache.page_size if max_kv is None else max_kv, window)]
+    _ints32("fp4_attn_workspace", *n)
+    a = _Attn(batch=n[0], total_q=n[1], q_heads=n[2], table_cols=n[3], max_q=n[4], max_kv=n[5], causal=1, window=n[6],
+              scale=1.0, ld_q=n[2] * cache.head_dim, q_starts=16)
     n = lib().fp4q_attn_workspace_bytes(ct.byref(cache.cfg), cache._ref, ct.byref(a))
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
@@ -788,6 +796,7 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
         max_q = 1 if q_starts is None else T
     if max_kv is None:
         max_kv = cols * cache.page_size
+    _ints32("fp4_attn", max_q, max_kv, window)
     a = ct.byref(_Attn(q.data_ptr(), ld, page_table.data_ptr(), kv_lens.data_ptr(),
                        None if q_starts is None else q_starts.data_ptr(), None if sinks is None else sinks.data_ptr(),
                        out.data_ptr(), None if lse is None else lse.data_ptr(),
