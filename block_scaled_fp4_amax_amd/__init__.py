@@ -580,7 +580,7 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, wor
     if codes.device != dev or scales.device != dev or (outer is not None and outer.device != dev):
         raise ValueError("x and the weight must be on one device")
     if y is None:
-        y = _held_on(torch.empty((M, N), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=dev), stream)
+        y = _new((M, N), out_dtype if out_dtype is not None else torch.bfloat16, dev, stream)
     elif tuple(y.shape) != (M, N) or (N > 1 and y.stride(1) != 1) or y.device != dev:
         raise ValueError("y must be a [%d, %d] view with contiguous rows on %s" % (M, N, dev))
     if y.dtype not in (torch.bfloat16, torch.float32):
@@ -588,7 +588,7 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, wor
     if workspace is None:
         need = lib().fp4q_linear_workspace_bytes(M, N, K)
         if need:
-            workspace = _held_on(_empty(need, torch.uint8, dev), stream)
+            workspace = _new(need, torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
@@ -603,12 +603,16 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, wor
 # Single tokens make these calls every few microseconds, so they are marshalled with what costs
 # least: plain addresses (checked to be on the cache's device), configurations and structures
 # built once for a cache, and the stream's raw handle.
-def _held_on(t, stream):
-    """A tensor allocated here stays reserved until the work of a caller's
-    stream that uses it is done."""
-    if stream is not None:
-        torch = _torch()
-        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+def _new(shape, dtype, device, stream):
+    """A tensor that work on `stream` writes.  It is that stream's own memory (what the current
+    stream has freed may still be written by its queued work), and once it is freed it stays
+    reserved until what the current stream has queued by then is done."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -718,7 +722,7 @@ def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
     shape = (n, cache.kv_heads, cache.head_dim)
     if out is None:
         dtype = dtype if dtype is not None else torch.bfloat16
-        k, v = (_held_on(torch.empty(shape, dtype=dtype, device=dev), stream) for _ in "kv")
+        k, v = (_new(shape, dtype, dev, stream) for _ in "kv")
     else:
         k, v = out
         for t in (k, v):
@@ -783,14 +787,13 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
                               or sinks.device != dev):
         raise ValueError("sinks must be a contiguous float32 [%d] on %s" % (Hq, dev))
     if out is None:
-        out = _held_on(torch.empty((T, Hq, D), dtype=out_dtype if out_dtype is not None else torch.bfloat16, device=dev),
-                       stream)
+        out = _new((T, Hq, D), out_dtype if out_dtype is not None else torch.bfloat16, dev, stream)
     elif tuple(out.shape) != (T, Hq, D) or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous %s on %s" % ([T, Hq, D], dev))
     cfg = cache._by_dtype.get(out.dtype)
     if cfg is None:
         raise Fp4Error(ERR_DTYPE, "out dtype %s" % out.dtype)
-    lse = _held_on(torch.empty((T, Hq), dtype=torch.float32, device=dev), stream) if with_lse else None
+    lse = _new((T, Hq), torch.float32, dev, stream) if with_lse else None
     cols = page_table.shape[1]
     if max_q is None:
         max_q = 1 if q_starts is None else T
@@ -805,7 +808,7 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     if workspace is None:
         need = lib().fp4q_attn_workspace_bytes(cfg, cache._ref, a)
         if need:
-            workspace = _held_on(_empty(need, torch.uint8, dev), stream)
+            workspace = _new(need, torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
