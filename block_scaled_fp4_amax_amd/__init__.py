@@ -593,9 +593,9 @@ def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, wor
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
     ycfg = _with_dtypes(cfg, "bf16", _dtype_name(y))
-    _check(lib().fp4_linear(ct.byref(ycfg), x.data_ptr(), M, x.stride(0) if M > 1 else K, codes.data_ptr(),
-                            scales.data_ptr(), None if outer is None else outer.data_ptr(), 1 if outer_transposed else 0, N,
-                            K, y.data_ptr(), y.stride(0) if M > 1 else N, scratch, size, _raw_stream(stream, dev)), "fp4_linear")
+    _launch("fp4_linear", lib().fp4_linear, dev, ct.byref(ycfg), x.data_ptr(), M, x.stride(0) if M > 1 else K,
+            codes.data_ptr(), scales.data_ptr(), None if outer is None else outer.data_ptr(), 1 if outer_transposed else 0, N,
+            K, y.data_ptr(), y.stride(0) if M > 1 else N, scratch, size, _raw_stream(stream, dev))
     return y
 
 
@@ -650,6 +650,17 @@ def _ints32(where, *values):
     for v in values:
         if not -0x80000000 <= v <= 0x7FFFFFFF:
             raise Fp4Error(ERR_UNSUPPORTED, "%s: %d" % (where, v))
+
+
+def _launch(where, entry, device, *args):
+    """Calls a C entry point with the tensors' device current: its kernels start there."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device.index:
+        st = entry(*args)
+    else:
+        with torch.cuda.device(device):
+            st = entry(*args)
+    _check(st, where)
 
 
 class KVCache:
@@ -708,8 +719,8 @@ def fp4_kv_append(cache, k, v, slots, *, stream=None):
     if k.dtype != v.dtype or v.shape[0] != n or k.device != dev or v.device != dev:
         raise ValueError("k and v must agree in shape and dtype and lie on the cache's device")
     _ints(slots, torch.int64, n, None, "slots", dev)
-    _check(lib().fp4_kv_append(cache._by_dtype[k.dtype], cache._ref, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
-                               slots.data_ptr(), n, _raw_stream(stream, dev)), "fp4_kv_append")
+    _launch("fp4_kv_append", lib().fp4_kv_append, dev, cache._by_dtype[k.dtype], cache._ref, k.data_ptr(), ld_k, v.data_ptr(),
+            ld_v, slots.data_ptr(), n, _raw_stream(stream, dev))
 
 
 def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
@@ -731,8 +742,8 @@ def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
     cfg = cache._by_dtype.get(k.dtype)
     if cfg is None:
         raise Fp4Error(ERR_DTYPE, "k dtype %s" % k.dtype)
-    _check(lib().fp4_kv_read(cfg, cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
-           "fp4_kv_read")
+    _launch("fp4_kv_read", lib().fp4_kv_read, dev, cfg, cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+            _raw_stream(stream, dev))
     return k, v
 
 
@@ -812,7 +823,7 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
-    _check(lib().fp4_attn(cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev)), "fp4_attn")
+    _launch("fp4_attn", lib().fp4_attn, dev, cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev))
     return (out, lse) if with_lse else out
 
 

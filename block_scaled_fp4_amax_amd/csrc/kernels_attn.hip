@@ -1208,13 +1208,12 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, float unshift)
     write_joined<D>(a, row, qh, top, l, acc, unshift, lane);
 }
 
-// A kernel's LDS limit is a property of the function: raised once, outside any launch.
 template <int D, int BIAS, int QT>
 hipError_t launch_few(AttnArgs a, hipStream_t s)
 {
     constexpr int lds = lds_bytes<D, BIAS, QT>();
-    static const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static OncePerDevice once;
+    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>), lds);
     if (st != hipSuccess) return st;
     a.part_o = a.few_o;
     a.part_ml = a.few_ml;
@@ -1238,8 +1237,8 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
         const hipError_t st = launch_few<D, BIAS, 2>(a, s);
         if (st != hipSuccess) return st;
     }
-    static const hipError_t st = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tiles<D, BIAS>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
+    static OncePerDevice once;
+    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_tiles<D, BIAS>), T::kLds);
     if (st != hipSuccess) return st;
     const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
     hipLaunchKernelGGL((k_attn_tiles<D, BIAS>), grid, dim3(64 * T::kWaves), T::kLds, s, a);

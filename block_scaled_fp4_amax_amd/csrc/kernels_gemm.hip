@@ -30,8 +30,6 @@
 // K-values beyond K load as zero codes with scale byte 0 (2^-127), adding
 // exact zeros.  Workgroup ids are remapped so each XCD (ids dealt round-robin)
 // works on a contiguous run of tiles that share operand panels in its L2.
-#include <mutex>
-
 #include "fp4q_device.h"
 #include "launch.h"
 
@@ -557,15 +555,9 @@ hipError_t launch_mx_gemm(const GemmArgs& g, hipStream_t s)
         k_mx_gemm<false, kScaleRowBytes>, k_mx_gemm<true, kScaleRowBytes>, k_mx_gemm<false, kScaleRow8>,
         k_mx_gemm<true, kScaleRow8>,      k_mx_gemm<false, kScaleTiled>,   k_mx_gemm<true, kScaleTiled>,
         k_mx_gemm_lds<false>,             k_mx_gemm_lds<true>};
-    // the dynamic-LDS limit is a property of the kernel function: raise it once
-    // per variant (not per launch, so launches stay capturable in a HIP graph)
-    static std::once_flag once[8];
-    static hipError_t attr_status[8];
-    std::call_once(once[variant], [&] {
-        attr_status[variant] = hipFuncSetAttribute(reinterpret_cast<const void*>(fns[variant]),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    });
-    if (attr_status[variant] != hipSuccess) return attr_status[variant];
+    static OncePerDevice once[8];
+    const hipError_t st = allow_lds(once[variant], reinterpret_cast<const void*>(fns[variant]), (int)lds);
+    if (st != hipSuccess) return st;
     hipLaunchKernelGGL(fns[variant], dim3(T), dim3(kThreads), lds, s, g);
     return hipGetLastError();
 }

@@ -390,9 +390,9 @@ template <int BIAS, int MT, bool OUTER>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t s)
 {
     using T = Tile<BIAS, MT, OUTER>;
-    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(k_linear_tile<BIAS, MT, OUTER>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
-    if (allowed != hipSuccess) return allowed;
+    static OncePerDevice once;
+    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_linear_tile<BIAS, MT, OUTER>), T::kLds);
+    if (st != hipSuccess) return st;
     const dim3 grid((uint32_t)((a.N + T::kN - 1) / T::kN), (uint32_t)((a.M + 16 * MT - 1) / (16 * MT)), (uint32_t)a.splits);
     hipLaunchKernelGGL((k_linear_tile<BIAS, MT, OUTER>), grid, dim3(512), T::kLds, s, a);
     if (a.parts) {

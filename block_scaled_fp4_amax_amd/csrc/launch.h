@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "kv_index.h"
+#include "per_device.h"
 
 namespace fp4q {
 
@@ -19,6 +20,18 @@ inline void set_tile_grid(int32_t total_tiles, int32_t& per_xcd, int32_t& wgs_pe
     per_xcd = (total_tiles + 7) / 8;
     wgs_per_xcd = per_xcd < kTileWgsPerXcd ? per_xcd : kTileWgsPerXcd;
     if (wgs_per_xcd < 1) wgs_per_xcd = 1;
+}
+
+// Raises a kernel's limit of dynamic LDS, a property of the function on each device: at its first launch
+// there, not at every one, so that later launches can be captured in a HIP graph.
+inline hipError_t allow_lds(OncePerDevice& once, const void* kernel, int bytes)
+{
+    int device = 0;
+    const hipError_t st = hipGetDevice(&device);
+    if (st != hipSuccess) return st;
+    return (hipError_t)once(device, [&] {
+        return (int)hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
 }
 
 // Rowwise NVFP4 / AMDFP4 parameters (modes none, tensorwise, 1D outer).

@@ -31,6 +31,7 @@
  *   - All tensor pointers are DEVICE pointers (hipMalloc / torch CUDA tensors)
  *     except where an argument says "host".  `stream` is a hipStream_t (NULL =
  *     the null stream).  Calls are asynchronous: FP4Q_OK means "enqueued".
+ *     The device of the tensors and the stream is the calling thread's current one.
  *   - x and y are bf16 tensors passed as their 16-bit patterns, row-major.
  *     x has leading dimension ld_x >= cols (elements); every other tensor is
  *     contiguous.

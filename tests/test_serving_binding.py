@@ -1,6 +1,9 @@
 """Refusals of the serving calls' binding (no GPU): arguments that the C entry points
 cannot see are wrong."""
+import contextlib
 import ctypes as ct
+import os
+import subprocess
 import types
 
 import pytest
@@ -36,3 +39,35 @@ def test_attention_refuses_bounds_beyond_32_bits(kw):
     with pytest.raises(fq.Fp4Error) as e:
         fq.fp4_attn_workspace(cpu_cache(), 2, 4, 2, table_cols=4, **kw)
     assert e.value.status == fq.ERR_UNSUPPORTED
+
+
+def test_what_is_done_once_is_done_on_each_device(tmp_path):
+    """The kernels' LDS limits are raised on every device that launches them."""
+    exe = str(tmp_path / "per_device_check")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "pins", "per_device_check.cpp")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-o", exe, src], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_calls_run_with_the_device_of_their_tensors(monkeypatch):
+    seen, current = [], [0]
+
+    @contextlib.contextmanager
+    def on(device):
+        before, current[0] = current[0], device.index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", on)
+
+    def entry(*args):
+        seen.append((current[0], args))
+        return 0 if args[0] else fq.ERR_SHAPE
+
+    fq._launch("fp4_attn", entry, torch.device("cuda", 3), 1, 2)
+    fq._launch("fp4_attn", entry, torch.device("cuda", 0), 5)
+    assert seen == [(3, (1, 2)), (0, (5,))] and current == [0]
+    with pytest.raises(fq.Fp4Error, match="fp4_attn"):
+        fq._launch("fp4_attn", entry, torch.device("cuda", 1), 0)
