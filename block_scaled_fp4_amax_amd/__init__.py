@@ -196,9 +196,16 @@ def _ct_workspace(cfg, rows, cols, residual, device, workspace, staged):
 
 
 # ------------------------------------------------------------------ marshalling helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first call that needs it (an import statement costs every call)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -647,9 +654,8 @@ def _ints(t, dtype, rows, cols, what, device):
 
 def _ints32(where, *values):
     """The structures' 32-bit fields would take larger integers modulo 2^32."""
-    for v in values:
-        if not -0x80000000 <= v <= 0x7FFFFFFF:
-            raise Fp4Error(ERR_UNSUPPORTED, "%s: %d" % (where, v))
+    if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
+        raise Fp4Error(ERR_UNSUPPORTED, "%s: %s" % (where, values))
 
 
 def _launch(where, entry, device, *args):
