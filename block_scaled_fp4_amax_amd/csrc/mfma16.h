@@ -28,8 +28,8 @@ struct Dec {
     static constexpr float kUnshift = BIAS == 0 ? 1.0f : BIAS == 7 ? 256.0f : 16.0f;
 
     // A scale byte as the decoders below take it: 2^k in binary32 (MXFP4; the
-    // byte 0xFF gives an operand whose conversions are NaN) or d / 2^kShift
-    // twice in FP16.
+    // conversions read the exponent alone, so byte 0 is 2^-127, and byte 0xFF gives
+    // NaN) or d / 2^kShift twice in FP16.
     static __device__ __forceinline__ uint32_t scale(uint32_t byte)
     {
         if constexpr (BIAS == 0) return byte << 23;
