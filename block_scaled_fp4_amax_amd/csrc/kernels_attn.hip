@@ -263,19 +263,24 @@ __device__ __forceinline__ void store_row(void* out, bool f32, int64_t row, int 
 // The factor of a row's O and its log-sum-exp (natural) from (m, l) and the head's sink.
 __device__ __forceinline__ float finish_row(float m, float l, const float* sinks, int head, float& lse)
 {
-    float f = 1.0f;
+    float f = 1.0f, sink = 0.0f;
+    bool led = false;                                    // by the sink
     if (sinks) {
-        const float s = sinks[head] * kLog2e;
+        sink = sinks[head];
+        float s = sink * kLog2e;
+        // a finite sink stays finite (its type's lowest value, or one above all scores)
+        if (__builtin_isinf(s) && !__builtin_isinf(sink)) s = __builtin_copysignf(3.4028235e38f, s);
         const float top = fmaxf(m, s);
         f = __builtin_amdgcn_exp2f(m - top);
         l = l * f + __builtin_amdgcn_exp2f(s - top);
         m = top;
+        led = s == top;
     }
     if (l == 0.0f) {                                     // a row that sees nothing
         lse = -__builtin_inff();
         return 0.0f;
     }
-    lse = (m + __builtin_log2f(l)) * kLn2;
+    lse = led ? sink + __builtin_log2f(l) * kLn2 : (m + __builtin_log2f(l)) * kLn2;
     return f / l;
 }
 
