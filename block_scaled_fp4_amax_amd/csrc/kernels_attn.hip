@@ -590,6 +590,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* lds, co
             g[s].row = hi >= 0 ? (int64_t)hi << 32 | lo : 0;
         }
         ++known;
+        wait_reads();                                    // of the step before, whose stage is filled now
         ring.issue(slot, g);
         groups |= (uint32_t)(g[0].ok | g[1].ok << 1) << (2 * behind);
         slot = (slot + 1) % R::kDepth;

@@ -67,6 +67,13 @@ __device__ __forceinline__ void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
 }
 
+// Waits for the wave's own reads of LDS, before a load overwrites the places that they read: the two are
+// not ordered with each other.
+__device__ __forceinline__ void wait_reads()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+}
+
 typedef __attribute__((address_space(3))) unsigned char lds_t;
 
 __device__ __forceinline__ uint32_t lds_address(const lds_t* p)
