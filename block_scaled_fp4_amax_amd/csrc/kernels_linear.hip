@@ -271,6 +271,7 @@ __global__ __launch_bounds__(512) void k_linear_tile(LinearArgs a)
         // says that the stage before, whose place is filled next, has been read
         if (s + T::kDepth - 2 < s1) wait_loads<(T::kDepth - 2) * T::kLoads>();
         else wait_loads<0>();
+        wait_reads();
         lds_barrier();
         const int free = slot == 0 ? T::kDepth - 1 : slot - 1;
         if (wave < 4 && s + T::kDepth - 1 < s1) issue(s + T::kDepth - 1, free);
