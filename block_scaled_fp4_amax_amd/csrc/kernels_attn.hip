@@ -26,7 +26,9 @@
 // kept down to 2^-28 of the row's largest value.
 //
 // Running maximum.  m moves only when some row's score exceeds it by 8 (powers of
-// two), so P stays below 2^8 and O is seldom rescaled.
+// two), so O is seldom rescaled.  P stays below 2^8 in bf16.  In FP16 m is held 7 below the
+// largest score when it moves: P's largest lies within [2^7, 2^15], and what FP16 rounds to multiples
+// of 2^-24 is 2^7 further below it, at no cost.
 //
 // Few rows: the four waves of a workgroup take every fourth step of the same rows and
 // join through LDS, and the keys are split over workgroups, whose partial (O, m, l) a
@@ -52,6 +54,9 @@ constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
 constexpr float kLazy = 8.0f;
+// powers of two between m and the score that moves it
+template <int BIAS>
+constexpr float kRoom = BIAS == 0 ? 0.0f : 7.0f;
 
 // A group's rows through a buffer descriptor in scalar registers: a lane's offsets are the
 // same for every group, so a load takes no address arithmetic on lanes.
@@ -458,8 +463,8 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
         float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
                           fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
         top *= rows.c[t];
-        if (__any(top > sum.m[t] + kLazy)) {
-            const float mn = fmaxf(sum.m[t], column_max(top));
+        if (__any(top > sum.m[t] + (kLazy + kRoom<BIAS>))) {
+            const float mn = fmaxf(sum.m[t], column_max(top) - kRoom<BIAS>);
             const float f = __builtin_amdgcn_exp2f(sum.m[t] - mn);
             sum.m[t] = mn;
             sum.l[t] *= f;

@@ -528,8 +528,8 @@ typedef struct {
  * others NaN); an MXFP4 block poisoned by NaN makes the rows that see its key NaN,
  * as in the products.
  * K and V enter the products exactly; the weights of V are rounded to bf16 (MXFP4)
- * or FP16 (NVFP4, AMD-FP4: weights below 2^-14 of a row's largest are then multiples of
- * 2^-24 of it) before they are multiplied and summed; everything else is binary32,
+ * or FP16 (NVFP4, AMD-FP4: weights below 2^-21 of a row's largest are then multiples of at
+ * most 2^-31 of it) before they are multiplied and summed; everything else is binary32,
  * but that NVFP4 and AMD-FP4 caches keep of a query's values what lies above 2^-38 of its
  * largest.
  * workspace: fp4q_attn_workspace_bytes() bytes (0 for calls whose keys are not
