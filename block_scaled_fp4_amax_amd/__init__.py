@@ -784,7 +784,8 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     scale        of q . k, default head_dim ** -0.5.
     window       > 0: each query sees at most that many keys, up to its own.
     sinks        float32 [q_heads]: a logit that joins each row's softmax.
-    Returns out (bf16, or out_dtype float32), or (out, lse) with with_lse."""
+    Returns out (bf16, or out_dtype float32, which also keeps twice the bits of the
+    weights), or (out, lse) with with_lse."""
     torch = _torch()
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, head_dim]")

@@ -22,7 +22,9 @@
 // Rounding.  K and V decode exactly (mfma16.h).  P is rounded to the 16-bit
 // operand type (half a step: 2^-8 of a term in bf16, 2^-11 in FP16), and l sums the rounded P
 // (a product with ones), so a row of equal values of V is returned exactly; S, m, l
-// and O are binary32.  FP16 holds q scaled by a power of two per row: its bits are
+// and O are binary32.  Where the result is asked for in binary32 (FINE), P is two such terms, the
+// second what the first has left (off by 2^-16 in bf16, 2^-22 in FP16), and each takes its products: 48
+// sequences up to 8192 keys (MXFP4, head_dim 64) 33 -> 36.5 us, two prompts of 4096 tokens (128) 285 -> 345 us.  FP16 holds q scaled by a power of two per row: its bits are
 // kept down to 2^-28 of the row's largest value.
 //
 // Running maximum.  m moves only when some row's score exceeds it by 8 (powers of
@@ -413,7 +415,7 @@ struct Sums {
 
 // One step: 32 keys from `at`, whose operands `src` gives; bits 0 and 1 of `groups` say which of
 // its two groups of 16 are there.
-template <int D, int BIAS, int QT, class Src>
+template <int D, int BIAS, int QT, bool FINE, class Src>
 __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, int end, const Rows<D, BIAS, QT>& rows,
                                             int lane, Sums<D, QT>& sum)
 {
@@ -457,7 +459,7 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
     if constexpr (BIAS == 0) src.poison(groups, whole, sc, sum.o);
 
     // running maximum, P
-    uint4 p[QT];
+    uint4 p[QT], rest[FINE ? QT : 1];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
@@ -477,6 +479,11 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
             e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][k >> 2][k & 3], rows.c[t], -sum.m[t]));
         p[t] = make_uint4(X::round2(e[0], e[1]), X::round2(e[2], e[3]), X::round2(e[4], e[5]), X::round2(e[6], e[7]));
         sum.l[t] = X::mfma(ones, p[t], sum.l[t]);
+        if constexpr (FINE) {
+            rest[t] = make_uint4(X::rest2(e[0], e[1], p[t].x), X::rest2(e[2], e[3], p[t].y), X::rest2(e[4], e[5], p[t].z),
+                                 X::rest2(e[6], e[7], p[t].w));
+            sum.l[t] = X::mfma(ones, rest[t], sum.l[t]);
+        }
     }
 
     // O^T += V^T P^T, two values of head_dim (one byte of codes) at a time
@@ -489,6 +496,10 @@ __device__ __forceinline__ void attend_step(Src& src, uint32_t groups, int at, i
         for (int t = 0; t < QT; ++t) {
             sum.o[t][2 * y] = X::mfma(lo, p[t], sum.o[t][2 * y]);
             sum.o[t][2 * y + 1] = X::mfma(hi, p[t], sum.o[t][2 * y + 1]);
+            if constexpr (FINE) {
+                sum.o[t][2 * y] = X::mfma(lo, rest[t], sum.o[t][2 * y]);
+                sum.o[t][2 * y + 1] = X::mfma(hi, rest[t], sum.o[t][2 * y + 1]);
+            }
         }
     };
     two(std::integral_constant<int, 0>{});
@@ -566,7 +577,7 @@ struct FromRaw {
 // Steps at, at + stride, ... before end, through the wave's ring.  The rows of the next
 // 64 steps are looked up together, a step a lane: a scalar look-up in each step would
 // be waited for with the step's LDS reads, which count on the same counter.
-template <int D, int BIAS, int QT>
+template <int D, int BIAS, int QT, bool FINE>
 __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* lds, const int32_t* table, int head, int at,
                                        int end, int stride, const Rows<D, BIAS, QT>& rows, int lane, Sums<D, QT>& sum)
 {
@@ -614,7 +625,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, unsigned char* lds, co
         Raw<D, BIAS> raw;
         ring.read(now, raw);
         FromRaw<D, BIAS, QT> src(raw, lane);
-        attend_step<D, BIAS, QT>(src, groups, at, end, rows, lane, sum);
+        attend_step<D, BIAS, QT, FINE>(src, groups, at, end, rows, lane, sum);
     }
 }
 
@@ -672,7 +683,7 @@ __device__ __forceinline__ void join_waves(JoinLds<D, QT>& lds, int wave, int la
 }
 
 // Final results of a wave's rows.
-template <int D, int BIAS, int QT>
+template <int D, int BIAS, int QT, bool F32>
 __device__ __forceinline__ void write_rows(const AttnArgs& a, const Rows<D, BIAS, QT>& rows, const Sums<D, QT>& sum,
                                            int head, int lane)
 {
@@ -688,7 +699,7 @@ __device__ __forceinline__ void write_rows(const AttnArgs& a, const Rows<D, BIAS
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) y[D / 16 * r + n] = l == 0.0f ? 0.0f : sum.o[t][n][r] * f;
-        store_row<D>(a.out, a.out_f32 != 0, row, lane >> 4, y);
+        store_row<D>(a.out, F32, row, lane >> 4, y);
         if (a.lse && lane < 16) a.lse[row] = lse;
     }
 }
@@ -781,7 +792,7 @@ __device__ __forceinline__ int share_of(int total, const AttnArgs& a)
 
 __device__ __forceinline__ int parts_of(int units, int share) { return (units + share - 1) / share; }
 
-template <int D, int BIAS, int QT>
+template <int D, int BIAS, int QT, bool FINE>
 __global__ __launch_bounds__(64 * kWaves, QT == 1 && D == 64 ? 4 : D == 256 && QT == 2 ? 1 : 2) void k_attn_few(AttnArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -823,11 +834,11 @@ __global__ __launch_bounds__(64 * kWaves, QT == 1 && D == 64 ? 4 : D == 256 && Q
     Sums<D, QT> sum;
     rows.load(a, QueryRange{q.first_q, q.queries}, q.kv, head, 0, lane);
     sum.clear();
-    attend<D, BIAS, QT>(a, smem + wave * Ring<D, BIAS>::kWave, a.table + (int64_t)seq * a.table_cols, head,
+    attend<D, BIAS, QT, FINE>(a, smem + wave * Ring<D, BIAS>::kWave, a.table + (int64_t)seq * a.table_cols, head,
                         q.lo + from * kUnit + wave * kStep, min(q.hi, q.lo + to * kUnit), kUnit, rows, lane, sum);
     join_waves<D, QT>(*reinterpret_cast<JoinLds<D, QT>*>(smem), wave, lane, sum);
     if (wave != 0) return;
-    if (parts == 1) write_rows<D, BIAS, QT>(a, rows, sum, head, lane);
+    if (parts == 1) write_rows<D, BIAS, QT, FINE>(a, rows, sum, head, lane);
     else write_parts<D, BIAS, QT>(a, rows, sum, (int64_t)blockIdx.x * (16 * QT), false, lane);
 }
 
@@ -1081,7 +1092,7 @@ struct DecodePart {
     }
 };
 
-template <int D, int BIAS>
+template <int D, int BIAS, bool FINE>
 __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a)
 {
     using T = Tiles<D>;
@@ -1164,13 +1175,13 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
                 FromLds<D, BIAS, QT> src{lds + buf * T::kRound + s * T::kStepBytes + lane * 16};
                 const uint32_t groups = __builtin_amdgcn_readfirstlane(
                     *(const __attribute__((address_space(3))) uint32_t*)(flags + buf * (T::kSteps * 16) + s * 16));
-                attend_step<D, BIAS, QT>(src, groups, k, my_end, rows, lane, sum);
+                attend_step<D, BIAS, QT, FINE>(src, groups, k, my_end, rows, lane, sum);
             }
         }
     }
     if (row0 >= count) return;
     if (a.splits > 1) write_parts<D, BIAS, QT>(a, rows, sum, (int64_t)split * a.total_q * a.q_heads, true, lane);
-    else write_rows<D, BIAS, QT>(a, rows, sum, head, lane);
+    else write_rows<D, BIAS, QT, FINE>(a, rows, sum, head, lane);
 }
 
 // Joins the splits of one row a wave: row r of sequence b's.
@@ -1219,16 +1230,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, float unshift)
     write_joined<D>(a, row, qh, top, l, acc, unshift, lane);
 }
 
-template <int D, int BIAS, int QT>
+template <int D, int BIAS, int QT, bool FINE>
 hipError_t launch_few(AttnArgs a, hipStream_t s)
 {
     constexpr int lds = lds_bytes<D, BIAS, QT>();
     static OncePerDevice once;
-    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT>), lds);
+    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_few<D, BIAS, QT, FINE>), lds);
     if (st != hipSuccess) return st;
     a.part_o = a.few_o;
     a.part_ml = a.few_ml;
-    hipLaunchKernelGGL((k_attn_few<D, BIAS, QT>), dim3((uint32_t)a.groups), dim3(64 * kWaves), lds, s, a);
+    hipLaunchKernelGGL((k_attn_few<D, BIAS, QT, FINE>), dim3((uint32_t)a.groups), dim3(64 * kWaves), lds, s, a);
     if (a.slots) {
         const int64_t rows = std::min<int64_t>((int64_t)a.max_q * a.group, kFewRows);
         hipLaunchKernelGGL((k_attn_few_join<D, QT>), dim3((uint32_t)((rows + 3) / 4), (uint32_t)a.kv.heads, (uint32_t)a.batch),
@@ -1237,22 +1248,22 @@ hipError_t launch_few(AttnArgs a, hipStream_t s)
     return hipGetLastError();
 }
 
-template <int D, int BIAS>
+template <int D, int BIAS, bool FINE>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
 {
     using T = Tiles<D>;
     const int64_t rows = (int64_t)a.max_q * a.group;
-    if (rows <= 16) return launch_few<D, BIAS, 1>(a, s);
-    if (rows <= kFewRows) return launch_few<D, BIAS, 2>(a, s);
+    if (rows <= 16) return launch_few<D, BIAS, 1, FINE>(a, s);
+    if (rows <= kFewRows) return launch_few<D, BIAS, 2, FINE>(a, s);
     if (a.groups) {                                      // a batch may hold sequences of few rows too
-        const hipError_t st = launch_few<D, BIAS, 2>(a, s);
+        const hipError_t st = launch_few<D, BIAS, 2, FINE>(a, s);
         if (st != hipSuccess) return st;
     }
     static OncePerDevice once;
-    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_tiles<D, BIAS>), T::kLds);
+    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_tiles<D, BIAS, FINE>), T::kLds);
     if (st != hipSuccess) return st;
     const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
-    hipLaunchKernelGGL((k_attn_tiles<D, BIAS>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
+    hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
     if (a.splits > 1) {
         const int64_t all = (int64_t)a.total_q * a.q_heads;
         hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
@@ -1263,9 +1274,9 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
 template <int BIAS>
 hipError_t launch_bias(const AttnArgs& a, hipStream_t s)
 {
-    if (a.kv.dim == 64) return launch_dim<64, BIAS>(a, s);
-    if (a.kv.dim == 128) return launch_dim<128, BIAS>(a, s);
-    return launch_dim<256, BIAS>(a, s);
+    if (a.kv.dim == 64) return a.out_f32 ? launch_dim<64, BIAS, true>(a, s) : launch_dim<64, BIAS, false>(a, s);
+    if (a.kv.dim == 128) return a.out_f32 ? launch_dim<128, BIAS, true>(a, s) : launch_dim<128, BIAS, false>(a, s);
+    return a.out_f32 ? launch_dim<256, BIAS, true>(a, s) : launch_dim<256, BIAS, false>(a, s);
 }
 
 }  // namespace

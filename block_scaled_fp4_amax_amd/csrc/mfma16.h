@@ -71,6 +71,17 @@ struct Dec {
         }
     }
 
+    // What round2 has left of them, rounded too.
+    static __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t rounded)
+    {
+        if constexpr (BIAS == 0) {
+            return round2(a - __uint_as_float(rounded << 16), b - __uint_as_float(rounded & 0xFFFF0000u));
+        } else {
+            const f16x2_t v = __builtin_bit_cast(f16x2_t, rounded);
+            return round2(a - (float)v[0], b - (float)v[1]);
+        }
+    }
+
     static constexpr uint32_t kOnes = BIAS == 0 ? 0x3F803F80u : 0x3C003C00u;
 
     // C += A B with A [16 rows x 32], B [32 x 16 columns]: lane l holds A's row

@@ -527,11 +527,14 @@ typedef struct {
  * values of 2^128 and more: they are infinite, and at a key that some queries see they make
  * others NaN); an MXFP4 block poisoned by NaN makes the rows that see its key NaN,
  * as in the products.
- * K and V enter the products exactly; the weights of V are rounded to bf16 (MXFP4)
- * or FP16 (NVFP4, AMD-FP4: weights below 2^-21 of a row's largest are then multiples of at
- * most 2^-31 of it) before they are multiplied and summed; everything else is binary32,
- * but that NVFP4 and AMD-FP4 caches keep of a query's values what lies above 2^-38 of its
- * largest.
+ * K and V enter the products exactly.  With bf16 output the weights of V are rounded to
+ * bf16 (MXFP4, a relative 2^-8) or FP16 (NVFP4, AMD-FP4: 2^-11; weights below 2^-21 of a
+ * row's largest are then multiples of at most 2^-31 of it) before they are multiplied and
+ * summed.  With FP32 output a weight enters as two such terms, whose sum is good to 2^-16
+ * (MXFP4) or 2^-22 (to the same multiples).  Everything else is binary32, but that NVFP4 and
+ * AMD-FP4 caches keep of a query's values what lies above 2^-38 of its largest.  The sums are divided
+ * by the sum of the weights at the end: MXFP4 values v with 2^8 sum_j |v_j| beyond binary32's range
+ * may give infinities (NVFP4 and AMD-FP4 values cannot).
  * workspace: fp4q_attn_workspace_bytes() bytes (0 for calls whose keys are not
  * split), 16-byte aligned.  It needs no initial value and holds nothing between
  * calls.  How keys are shared among workgroups, and so the last bits of a result,

@@ -9,8 +9,9 @@ import torch
 
 import block_scaled_fp4_amax_amd as fq
 import kv_reference as R
+from test_gpu_attn import Setup
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
 ONE = {"nvfp4": 0x38, "amdfp4": 0x78, "mxfp4": 127}            # the scale byte of 1
 
@@ -60,3 +61,32 @@ def test_many_small_weights_under_a_large_one(fmt, D, n, max_kv):
     o, _, tol, _ = R.attention(q.double().numpy(), buf, fmt, page, table, lens, starts, 1.0, u_p=2.0 ** -11, a_p=2.0 ** -32)
     assert np.all(tol < o / 4)                                # the bound is one that nothing but the small weights meets
     assert np.all(np.abs(got - o) <= tol + 2.0 ** -24 * np.abs(o))
+
+
+# two 16-bit terms of a weight: half a step of what the first has left
+U_TWO = {"mxfp4": 2.0 ** -16, "nvfp4": 2.0 ** -22, "amdfp4": 2.0 ** -22}
+A_TWO = {"mxfp4": 0.0, "nvfp4": 2.0 ** -32, "amdfp4": 2.0 ** -32}
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "amdfp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv,ql,G,window,wide", [([1, 70, 513], [1, 1, 1], 4, 0, 0), ([2000, 40], [3, 2], 8, 0, 200),
+                                                 ([150, 60], [60, 2], 4, 0, 0), ([1500], [40], 2, 1100, 200)])
+def test_binary32_results_keep_two_terms_of_a_weight(fmt, D, kv, ql, G, window, wide):
+    """Few rows with one part and with several, tiles of rows, tiles with split keys."""
+    s = Setup(fmt, D, 2, G, 16, kv, ql, outer=fmt == "amdfp4", extra_cols=wide).device()
+    o, l, tol, ltol = R.attention(s.q.double().numpy(), s.buf, fmt, 16, s.table, s.kv_lens, s.q_starts,
+                                  float(np.float32(D ** -0.5)), window=window, outer=s.outer, u_p=U_TWO[fmt], a_p=A_TWO[fmt])
+    out, lse = (t.double().cpu().numpy() for t in s.run(window=window, max_q=max(ql), out_dtype=torch.float32))
+    off = np.abs(out - o) / (tol + 2.0 ** -24 * np.abs(o) + 1e-37)
+    assert np.all(off <= 1), "off by %.1f bounds" % off.max()
+    assert np.all(np.abs(lse - l) <= ltol)
+
+
+def test_poisoned_blocks_in_binary32_results():
+    for n in (3, 80):
+        s = Setup("mxfp4", 128, 1, 2, 16, [80, 80], [n, 1])
+        s.buf["v_scales"][s.table[0, 4], 0, 14, 2] = 0xFF     # key 78, values 64 .. 95: the last two queries see it
+        s.buf["v_scales"][s.table[1, 4], 0, 15, 0] = 0xFF
+        out, _ = s.device().check(out_dtype=torch.float32)
+        assert torch.isnan(out[n - 2:n, :, 64:96]).all() and not torch.isnan(out[:n - 2]).any()
