@@ -1315,7 +1315,8 @@ AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_h
     if (rows <= kFewRows || batch > 1) plan_few(p, kv, batch, std::min<int64_t>(rows, kFewRows), keys);
     if (rows <= kFewRows) return p;
     const TilePlan t = plan_tiles(batch, kv.heads, q_heads / kv.heads, max_q, all, window, kv.dim);
-    if (t.splits == 1 || total_q * q_heads >= (int64_t)1 << 26) return p;   // rows of one launch of the join
+    // a launch of the join, four rows a workgroup of 256, has fewer than 2^32 lanes
+    if (t.splits == 1 || (total_q * q_heads + 3) / 4 * 256 >= (int64_t)1 << 32) return p;
     p.splits = t.splits;
     p.chunk = t.chunk;
     const size_t n = (size_t)t.splits * total_q * q_heads;
