@@ -552,7 +552,8 @@ def fp4q_linear_workspace_bytes(M, N, K):
 def fp4_linear(x, w, cfg, *, outer_transposed=False, out_dtype=None, y=None, workspace=None, stream=None):
     """y = x @ W^T with bf16 x [M, K] (a view with a row pitch is accepted) and a
     4-bit W [N, K] given as {"codes", "scales", "outer"} in cfg's format, as fp4_quantize
-    returns it (or the row_* buffers of fp4_cast_transpose under those names).
+    returns it (or the row_* buffers of fp4_cast_transpose under those names).  Outer scales: none,
+    one for the tensor, 64 x 64 tiles, or row segments of a multiple of 64.
 
     The gradient of x is the same product over the columnwise buffers: with
     w = {"codes": col_codes [K, N / 2], "scales": col_scales, "outer": ...} and dy [M, N] in

@@ -913,7 +913,8 @@ int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, 
     if (r.obs && (K % r.obs || (r.outer_kind == kOuter2D && N % r.obs))) return FP4Q_ERR_SHAPE;
     if ((r.outer_kind == kOuter2D && r.obs != 64) || (r.outer_kind == kOuter1D && r.obs % 64)) return FP4Q_ERR_UNSUPPORTED;
     if (K > ((int64_t)1 << 22) || M > ((int64_t)1 << 20) || N > ((int64_t)1 << 24)) return FP4Q_ERR_UNSUPPORTED;
-    // 32-bit byte offsets within a tile of x (64 rows) and within the outer scales
+    // byte offsets below 2^31 within a tile of x (128 rows: 127 of 2^24 bytes and K's 2^23) and within
+    // the outer scales
     if (M > 1 && ld_x > ((int64_t)1 << 23)) return FP4Q_ERR_UNSUPPORTED;
     if ((r.outer_kind == kOuter1D ? N * (K / r.obs) : r.outer_kind == kOuter2D ? (N / 64) * (K / 64) : 0) >= (int64_t)1 << 29)
         return FP4Q_ERR_UNSUPPORTED;

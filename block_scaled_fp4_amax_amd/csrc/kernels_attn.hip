@@ -100,7 +100,8 @@ struct Raw {
 
 // A wave's steps on their way: kDepth stages of LDS, filled by loads that write LDS
 // directly (16 bytes a lane to consecutive places), kDepth - 1 steps ahead of
-// their use.  A stage costs 3, 5 or 9 load instructions and no registers, where
+// their use.  (The MXFP4 forms wait for them all at a step's first product: the compiler's wait for the loads
+// of q, which nothing converts before the loop.)  A stage costs 3, 5 or 9 load instructions and no registers, where
 // loading a lane's own words took 24 instructions and kept one step in flight
 // (4 x 131072 keys, NVFP4, head_dim 128: 87 us, with this ring 79, and 71 with
 // non-temporal loads).  Two stages and twice the workgroups take as long as four.
@@ -905,13 +906,14 @@ __global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift
 }
 
 // ---------------------------------------------------------------- many rows
-// Eight waves take rows of their own and the same keys, 128 (head_dim 256: 64) at a time.  Each wave
+// Eight waves take rows of their own and the same keys, 64 (head_dim 64: 128) at a time.  Each wave
 // decodes a part of those keys' K and V once for all into LDS, as whole operands (64 lanes of 16
 // bytes, written and read without bank conflicts), for the next keys while this one's are
 // used; its bytes are loaded another round ahead.  Few workgroups split the keys `splits` ways.
-// Two prompts of 4096 tokens (MXFP4, 32 / 8 heads of 128): 249 to 270 us, about 0.7 PFLOP/s (305 with
-// each wave decoding for itself).  Bound: of 503 thousand active cycles the vector unit takes
-// 257 (softmax, decoding) and the matrix unit 185, and they overlap little; 32 rows a wave
+// Two prompts of 4096 tokens (MXFP4, 32 / 8 heads of 128): 248 us a call among others, 266 to 280 under
+// the profiler, about 0.7 PFLOP/s (305 with each wave decoding for itself).  Bound: of 507 thousand
+// active cycles the vector unit takes 260 (softmax, decoding), LDS 225 (each operand that is read feeds one
+// product) and the matrix unit 185, and they overlap little; 32 rows a wave
 // (fewer vector instructions, half the waves), operands read ahead into
 // registers and raised priority around the products all measured 270 to 300.
 template <int D>

@@ -155,14 +155,15 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_linear(LinearArgs a)
 }
 
 // ---------------------------------------------------------------- tiles
-// Larger work: a workgroup of eight waves takes 16 MT rows of x and 32 kWN rows of W, 256
-// values of K at a time through a ring of LDS stages filled by direct loads:
-//   x       [16 MT][256] bf16, a row's 32 chunks of 16 bytes at chunk ^ (row % 16),
-//   codes   [32 kWN][128 bytes], a row's eight chunks at chunk ^ (row / 2 % 4 * 2),
-//   scales  [32 kWN][8], a word for 32 values of K (one byte of MXFP4, two of the
+// Larger work: a workgroup of eight waves takes 16 MT rows of x and 32 kWN rows of W, S = 256
+// values of K (128 with eight tiles of x rows, of whose stages LDS would not hold two) at a time
+// through a ring of LDS stages filled by direct loads:
+//   x       [16 MT][S] bf16, a row's S / 8 chunks of 16 bytes at chunk ^ (row % 16),
+//   codes   [32 kWN][S / 2 bytes], a row's S / 32 chunks at chunk ^ (row & (S / 32 - 2)),
+//   scales  [32 kWN][S / 32], a word for 32 values of K (one byte of MXFP4, two of the
 //           others: rows of scale bytes have no better alignment, 90 bytes for
 //           MXFP4 and K = 2880),
-//   outer scales [4][32 kWN] FP32, per 64 values of K.
+//   outer scales [S / 64][32 kWN] FP32, per 64 values of K.
 // Wave w takes W's rows 32 (w % kWN) .. + 31 and the (w / kWN)-th part of the stage's K;
 // the parts join through LDS.  Waves 0 to 3, one of each SIMD, issue the loads, and the SIMD's
 // other wave computes meanwhile.  So a workgroup reads x from the caches once for
