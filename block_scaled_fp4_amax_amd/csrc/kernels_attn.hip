@@ -23,8 +23,9 @@
 // operand type (half a step: 2^-8 of a term in bf16, 2^-11 in FP16), and l sums the rounded P
 // (a product with ones), so a row of equal values of V is returned exactly; S, m, l
 // and O are binary32.  Where the result is asked for in binary32 (FINE), P is two such terms, the
-// second what the first has left (off by 2^-16 in bf16, 2^-22 in FP16), and each takes its products: 48
-// sequences up to 8192 keys (MXFP4, head_dim 64) 33 -> 36.5 us, two prompts of 4096 tokens (128) 285 -> 345 us.  FP16 holds q scaled by a power of two per row: its bits are
+// second what the first has left (off by 2^-16 in bf16, 2^-22 in FP16), and each takes its
+// products: 48 sequences up to 8192 keys (MXFP4, head_dim 64) 33 -> 36.5 us, two prompts of 4096 tokens
+// (128) 285 -> 345 us.  FP16 holds q scaled by a power of two per row: its bits are
 // kept down to 2^-28 of the row's largest value.
 //
 // Running maximum.  m moves only when some row's score exceeds it by 8 (powers of
@@ -100,9 +101,9 @@ struct Raw {
 
 // A wave's steps on their way: kDepth stages of LDS, filled by loads that write LDS
 // directly (16 bytes a lane to consecutive places), kDepth - 1 steps ahead of
-// their use.  (The MXFP4 forms wait for them all at a step's first product: the compiler's wait for the loads
-// of q, which nothing converts before the loop.)  A stage costs 3, 5 or 9 load instructions and no registers, where
-// loading a lane's own words took 24 instructions and kept one step in flight
+// their use.  (The MXFP4 forms wait for them all at a step's first product: the compiler's wait
+// for the loads of q, which nothing converts before the loop.)  A stage costs 3, 5 or 9 load
+// instructions and no registers, where loading a lane's own words took 24 instructions and kept one step in flight
 // (4 x 131072 keys, NVFP4, head_dim 128: 87 us, with this ring 79, and 71 with
 // non-temporal loads).  Two stages and twice the workgroups take as long as four.
 //   K codes   [32 keys][D / 2], D = 256 with a row's eight 16-byte chunks at
