@@ -3,7 +3,8 @@ block-scaled FP4 quantisation library.
 
 The functions carry the C-ABI names (fp4_quantize, fp4_dequantize, fp4_qdq,
 fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_linear,
-fp4_kv_append, fp4_kv_read, fp4_attn and the fp4q_* helpers).  They
+fp4_kv_append, fp4_kv_append_rope, fp4_kv_read, fp4_attn, fp4_add_rms_norm,
+fp4_add_rms_norm_backward and the fp4q_* helpers).  They
 only marshal arguments: torch supplies device memory and the current HIP
 stream, every step of the computation runs in the library's HIP kernels.  If
 the library is not built, importing the binding raises; there is no fallback.
@@ -18,7 +19,8 @@ __all__ = [
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
     "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "fp4q_linear_workspace_bytes", "KVCache", "fp4_kv_append",
-    "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "LIB_PATH",
+    "fp4_kv_append_rope", "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "fp4_add_rms_norm", "fp4_add_rms_norm_backward",
+    "fp4q_add_rms_norm_backward_workspace_bytes", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -64,6 +66,29 @@ class _Attn(ct.Structure):
         (n, ct.c_void_p) for n in ("page_table", "kv_lens", "q_starts", "sinks", "out", "lse")] + [
         ("scale", ct.c_float)] + [(n, ct.c_int32) for n in ("batch", "total_q", "q_heads", "table_cols", "max_q",
                                                             "max_kv", "causal", "window")]
+
+
+class _KvRope(ct.Structure):
+    _fields_ = [(n, ct.c_void_p) for n in ("k", "v", "q", "q_out")] + [
+        (n, ct.c_int64) for n in ("ld_k", "ld_v", "ld_q", "ld_q_out")] + [
+        (n, ct.c_void_p) for n in ("slots", "positions", "cos", "sin")] + [
+        ("tokens", ct.c_int64), ("table_rows", ct.c_int64)] + [
+        (n, ct.c_int32) for n in ("rot_dim", "q_heads", "interleaved", "reserved")]
+
+
+class _AddRmsNorm(ct.Structure):
+    _fields_ = [("x", ct.c_void_p), ("residual", ct.c_void_p), ("ld_x", ct.c_int64), ("ld_residual", ct.c_int64)] + [
+        (n, ct.c_void_p) for n in ("weight", "residual_out", "rstd", "y", "fp8", "fp8_scales")] + [
+        ("rows", ct.c_int64), ("hidden", ct.c_int64), ("eps", ct.c_double)] + [
+        (n, ct.c_int32) for n in ("x_dtype", "residual_dtype", "weight_dtype", "y_dtype", "fp8_mode", "reserved")]
+
+
+class _RmsNormGrad(ct.Structure):
+    _fields_ = [(n, ct.c_void_p) for n in ("dy", "h", "dresidual")] + [
+        (n, ct.c_int64) for n in ("ld_dy", "ld_h", "ld_dresidual")] + [
+        (n, ct.c_void_p) for n in ("weight", "rstd", "dx", "dweight")] + [
+        ("rows", ct.c_int64), ("hidden", ct.c_int64)] + [
+        (n, ct.c_int32) for n in ("dy_dtype", "h_dtype", "weight_dtype", "reserved")]
 
 
 def make_cfg(format="nvfp4", scale_format=None, two_level="none", outer_block_size=0, outer_2d=False,
@@ -138,6 +163,14 @@ def lib():
         KV, AT = ct.POINTER(_KvCache), ct.POINTER(_Attn)
         L.fp4_kv_append.restype = ct.c_int
         L.fp4_kv_append.argtypes = [C, KV, P, I64, P, I64, P, I64, P]
+        L.fp4_kv_append_rope.restype = ct.c_int
+        L.fp4_kv_append_rope.argtypes = [C, KV, ct.POINTER(_KvRope), P]
+        L.fp4_add_rms_norm.restype = ct.c_int
+        L.fp4_add_rms_norm.argtypes = [ct.POINTER(_AddRmsNorm), P]
+        L.fp4_add_rms_norm_backward.restype = ct.c_int
+        L.fp4_add_rms_norm_backward.argtypes = [ct.POINTER(_RmsNormGrad), P, SZ, P]
+        L.fp4q_add_rms_norm_backward_workspace_bytes.restype = SZ
+        L.fp4q_add_rms_norm_backward_workspace_bytes.argtypes = [I64, I64]
         L.fp4_kv_read.restype = ct.c_int
         L.fp4_kv_read.argtypes = [C, KV, P, I64, P, P, P]
         L.fp4q_attn_workspace_bytes.restype = SZ
@@ -730,6 +763,59 @@ def fp4_kv_append(cache, k, v, slots, *, stream=None):
             ld_v, slots.data_ptr(), n, _raw_stream(stream, dev))
 
 
+def _same_device(device, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s, got %s" % (n, device, t.device))
+
+
+def fp4_kv_append_rope(cache, k, v, slots, positions, cos, sin, *, q=None, q_out=None, interleaved=False, stream=None):
+    """fp4_kv_append of keys that are turned by their positions on the way; returns the
+    queries of the same tokens turned too, or None without q (see include/fp4q.h).
+
+    k, v, slots  as in fp4_kv_append; q: their dtype, [tokens, q_heads, head_dim], a view with a token
+                 pitch is accepted.
+    positions    int32 [tokens]: a token's row of the tables.  A token whose position lies outside them
+                 is padding: nothing is cached for it, and its queries come back as zeros.
+    cos, sin     float32 [rows, rot_dim / 2]; the first rot_dim values of a head (a multiple of 16) turn.
+    interleaved  pairs are values 2 j and 2 j + 1 of a head; else j and j + rot_dim / 2.
+    q_out        where the queries go; q itself turns them in place."""
+    torch, dev = _torch(), cache.device
+    types = (torch.bfloat16, torch.float32)
+    ld_k = _heads_rows(k, cache.kv_heads, cache.head_dim, "k", types)
+    ld_v = _heads_rows(v, cache.kv_heads, cache.head_dim, "v", types)
+    n = k.shape[0]
+    if k.dtype != v.dtype or v.shape[0] != n or k.device != dev or v.device != dev:
+        raise ValueError("k and v must agree in shape and dtype and lie on the cache's device")
+    _ints(slots, torch.int64, n, None, "slots", dev)
+    _ints(positions, torch.int32, n, None, "positions", dev)
+    if (cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32
+            or not cos.is_contiguous() or not sin.is_contiguous()):
+        raise ValueError("cos and sin must be contiguous float32 [rows, rot_dim / 2]")
+    _same_device(dev, cos=cos, sin=sin, q=q, q_out=q_out)
+    ld_q = ld_out = q_heads = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, q_heads, head_dim]")
+        q_heads = q.shape[1]
+        ld_q = _heads_rows(q, q_heads, cache.head_dim, "q", (k.dtype,))
+        if q_out is None:
+            q_out = _new((n, q_heads, cache.head_dim), q.dtype, dev, stream)
+        ld_out = _heads_rows(q_out, q_heads, cache.head_dim, "q_out", (k.dtype,))
+        if q.shape[0] != n or q_out.shape[0] != n:
+            raise ValueError("q and q_out must hold the %d tokens of k" % n)
+    _ints32("fp4_kv_append_rope", q_heads, 2 * cos.shape[1])
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    a = _KvRope(k.data_ptr(), v.data_ptr(), p(q), p(q_out), ld_k, ld_v, ld_q, ld_out, slots.data_ptr(), positions.data_ptr(),
+                cos.data_ptr(), sin.data_ptr(), n, cos.shape[0], 2 * cos.shape[1], q_heads, 1 if interleaved else 0, 0)
+    _launch("fp4_kv_append_rope", lib().fp4_kv_append_rope, dev, cache._by_dtype[k.dtype], cache._ref, ct.byref(a),
+            _raw_stream(stream, dev))
+    return q_out
+
+
 def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
     """(k, v): bf16 (or float32: dtype) [tokens, kv_heads, head_dim] that the
     cache holds at slots (int64 [tokens]; zeros for one outside the cache).  `out` may supply
@@ -833,6 +919,126 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
     _launch("fp4_attn", lib().fp4_attn, dev, cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev))
     return (out, lse) if with_lse else out
+
+
+# ------------------------------------------------------------------ residual and norm
+_FP8_MODES = {None: 0, "mx": 1, "row": 2}
+
+
+def _norm_rows(t, shape, what, types):
+    """Row pitch of a [rows, hidden] bf16 or float32 tensor whose rows are contiguous."""
+    if t.dtype not in types:
+        raise Fp4Error(ERR_DTYPE, "%s dtype %s" % (what, t.dtype))
+    if len(t.shape) != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s must be %s, got %s" % (what, "2-D" if shape is None else list(shape), list(t.shape)))
+    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s rows must be contiguous (stride(1) == 1)" % what)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_weight(weight, hidden, types):
+    if weight.dtype not in types:
+        raise Fp4Error(ERR_DTYPE, "weight dtype %s" % weight.dtype)
+    if tuple(weight.shape) != (hidden,) or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous [%d]" % hidden)
+
+
+def _out(t, shape, dtype, device, what, stream):
+    """A given output, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s %s on %s" % (what, dtype, list(shape), device))
+    return t
+
+
+def fp4_add_rms_norm(x, weight, residual=None, *, eps=1e-6, fp8=None, y=None, y_dtype=None, out=None, stream=None):
+    """h = x + residual and its root-mean-square norm times weight, in bf16 or float32, in 8 bits with
+    scales, or both (see include/fp4q.h for the rounding).
+
+    x, residual  bf16 or float32 [rows, hidden], each its own; views with a row pitch are accepted.
+    fp8          None, "mx" (E4M3 with a UE8M0 scale byte for 32 values) or "row" (a float32
+                 scale a row).
+    y            whether the norm itself is returned; by default where fp8 is None.  y_dtype: bf16, or
+                 float32.
+    out          may supply any result; "residual" may be the given residual.
+    Returns {"residual": h in residual's dtype (x itself without one), "rstd": float32 [rows], "y", "fp8": uint8
+    [rows, hidden], "fp8_scales": uint8 [rows, hidden / 32] or float32 [rows]}; what was not asked for
+    is None."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    if fp8 not in _FP8_MODES:
+        raise ValueError("fp8 must be None, 'mx' or 'row', got %r" % (fp8,))
+    ld_x = _norm_rows(x, None, "x", types)
+    (rows, hidden), dev = x.shape, x.device
+    if not x.is_cuda:
+        raise ValueError("fp4q takes device tensors; got one on %s" % dev)
+    ld_r = 0 if residual is None else _norm_rows(residual, x.shape, "residual", types)
+    _norm_weight(weight, hidden, types)
+    _same_device(dev, weight=weight, residual=residual)
+    given = out or {}
+    if y is None:
+        y = fp8 is None
+    y_dtype = y_dtype if y_dtype is not None else torch.bfloat16
+    if y_dtype not in types:
+        raise Fp4Error(ERR_DTYPE, "y dtype %s" % y_dtype)
+    res = dict(residual=x, y=None, fp8=None, fp8_scales=None)
+    if residual is not None:
+        res["residual"] = _out(given.get("residual"), (rows, hidden), residual.dtype, dev, "residual", stream)
+    res["rstd"] = _out(given.get("rstd"), (rows,), torch.float32, dev, "rstd", stream)
+    if y:
+        res["y"] = _out(given.get("y"), (rows, hidden), y_dtype, dev, "y", stream)
+    if fp8 is not None:
+        res["fp8"] = _out(given.get("fp8"), (rows, hidden), torch.uint8, dev, "fp8", stream)
+        res["fp8_scales"] = _out(given.get("fp8_scales"), (rows, hidden // 32) if fp8 == "mx" else (rows,),
+                                 torch.uint8 if fp8 == "mx" else torch.float32, dev, "fp8_scales", stream)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    f32 = lambda d: 2 if d == torch.float32 else 0  # noqa: E731
+    a = _AddRmsNorm(x.data_ptr(), p(residual), ld_x, ld_r, weight.data_ptr(), None if residual is None else p(res["residual"]),
+                    p(res["rstd"]), p(res["y"]), p(res["fp8"]), p(res["fp8_scales"]), rows, hidden, eps, f32(x.dtype),
+                    0 if residual is None else f32(residual.dtype), f32(weight.dtype), f32(y_dtype), _FP8_MODES[fp8], 0)
+    _launch("fp4_add_rms_norm", lib().fp4_add_rms_norm, dev, ct.byref(a), _raw_stream(stream, dev))
+    return res
+
+
+def fp4q_add_rms_norm_backward_workspace_bytes(rows, hidden):
+    return lib().fp4q_add_rms_norm_backward_workspace_bytes(int(rows), int(hidden))
+
+
+def fp4_add_rms_norm_backward(dy, h, weight, rstd, *, dresidual=None, dx=None, dweight=None, workspace=None, stream=None):
+    """The gradient of fp4_add_rms_norm from dy (that of y; bf16 or float32), what the call returned as
+    "residual" (h) and "rstd", and dresidual, the gradient of "residual" (h's dtype; None: zero).
+    Returns {"dx": the gradient of x, and of the residual, in h's dtype, "dweight": float32 [hidden]}.
+    dx may be dresidual.  workspace: at least fp4q_add_rms_norm_backward_workspace_bytes(rows, hidden) bytes,
+    else one is allocated where it is needed."""
+    torch = _torch()
+    types = (torch.bfloat16, torch.float32)
+    ld_h = _norm_rows(h, None, "h", types)
+    (rows, hidden), dev = h.shape, h.device
+    if not h.is_cuda:
+        raise ValueError("fp4q takes device tensors; got one on %s" % dev)
+    ld_dy = _norm_rows(dy, h.shape, "dy", types)
+    ld_dr = 0 if dresidual is None else _norm_rows(dresidual, h.shape, "dresidual", (h.dtype,))
+    _norm_weight(weight, hidden, types)
+    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (rows,) or not rstd.is_contiguous():
+        raise ValueError("rstd must be a contiguous float32 [%d]" % rows)
+    _same_device(dev, dy=dy, weight=weight, rstd=rstd, dresidual=dresidual, workspace=workspace)
+    dx = _out(dx, (rows, hidden), h.dtype, dev, "dx", stream)
+    dweight = _out(dweight, (hidden,), torch.float32, dev, "dweight", stream)
+    if workspace is None:
+        need = lib().fp4q_add_rms_norm_backward_workspace_bytes(rows, hidden)
+        if need:
+            workspace = _new(need, torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
+    f32 = lambda t: 2 if t.dtype == torch.float32 else 0  # noqa: E731
+    a = _RmsNormGrad(dy.data_ptr(), h.data_ptr(), None if dresidual is None else dresidual.data_ptr(), ld_dy, ld_h, ld_dr,
+                     weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(), rows, hidden, f32(dy), f32(h),
+                     f32(weight), 0)
+    _launch("fp4_add_rms_norm_backward", lib().fp4_add_rms_norm_backward, dev, ct.byref(a), scratch, size,
+            _raw_stream(stream, dev))
+    return {"dx": dx, "dweight": dweight}
 
 
 class ErrorFeedback:

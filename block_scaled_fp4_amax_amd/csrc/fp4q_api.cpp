@@ -808,6 +808,58 @@ int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k
     return hip_status(launch_kv_append(r.bias, r.x_f32, a, (hipStream_t)stream));
 }
 
+int fp4_kv_append_rope(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_kv_rope* rope, void* stream)
+{
+    Resolved r;
+    KvRopeArgs a;
+    const int st = resolve_cache(cfg, cache, r, a.kv);
+    if (st) return st;
+    if (!rope) return FP4Q_ERR_NULL;
+    const fp4q_kv_rope& o = *rope;
+    const int64_t row = (int64_t)a.kv.heads * a.kv.dim, q_row = (int64_t)o.q_heads * a.kv.dim;
+    const bool has_q = o.q != nullptr || o.q_out != nullptr;
+    if (o.interleaved != 0 && o.interleaved != 1) return FP4Q_ERR_MODE;
+    if (o.tokens < 0 || o.table_rows < 0 || (o.tokens > 1 && (o.ld_k < row || o.ld_v < row))) return FP4Q_ERR_SHAPE;
+    if (o.rot_dim < 16 || o.rot_dim % 16 || o.rot_dim > a.kv.dim) return FP4Q_ERR_SHAPE;
+    if (has_q && (o.q_heads < 1 || (o.tokens > 1 && (o.ld_q < q_row || o.ld_q_out < q_row)))) return FP4Q_ERR_SHAPE;
+    if (o.q && o.q == o.q_out && o.tokens > 1 && o.ld_q != o.ld_q_out) return FP4Q_ERR_SHAPE;
+    if (o.tokens > kMaxKvRows || o.ld_k > ((int64_t)1 << 31) || o.ld_v > ((int64_t)1 << 31) || o.table_rows > ((int64_t)1 << 31))
+        return FP4Q_ERR_UNSUPPORTED;
+    if (has_q && (o.ld_q > ((int64_t)1 << 31) || o.ld_q_out > ((int64_t)1 << 31) || o.q_heads > 65535))
+        return FP4Q_ERR_UNSUPPORTED;
+    // units of heads are the launch's second dimension
+    if (2 * (int64_t)a.kv.heads + (has_q ? o.q_heads : 0) > 65535) return FP4Q_ERR_UNSUPPORTED;
+    if (o.tokens == 0 || (a.kv.num_pages == 0 && !has_q)) return FP4Q_OK;
+    if (!o.k || !o.v || !o.slots || !o.positions || (has_q && (!o.q || !o.q_out)) || (o.table_rows > 0 && (!o.cos || !o.sin)))
+        return FP4Q_ERR_NULL;
+    const int64_t per16 = r.x_f32 ? 4 : 8;
+    if (misaligned(o.k, 16) || misaligned(o.v, 16) || misaligned(o.q, 16) || misaligned(o.q_out, 16) || misaligned(o.slots, 8) ||
+        misaligned(o.positions, 4) || misaligned(o.cos, 16) || misaligned(o.sin, 16) ||
+        (o.tokens > 1 && (o.ld_k % per16 || o.ld_v % per16 || (has_q && (o.ld_q % per16 || o.ld_q_out % per16)))))
+        return FP4Q_ERR_ALIGN;
+    a.k = o.k;
+    a.v = o.v;
+    a.q = o.q;
+    a.q_out = o.q_out;
+    a.ld_k = o.ld_k;
+    a.ld_v = o.ld_v;
+    a.ld_q = o.ld_q;
+    a.ld_out = o.ld_q_out;
+    a.slots = o.slots;
+    a.positions = o.positions;
+    a.cos = o.cos;
+    a.sin = o.sin;
+    a.tokens = o.tokens;
+    a.table_rows = o.table_rows;
+    a.num_slots = a.kv.num_pages * a.kv.page_size;
+    a.rot = o.rot_dim;
+    a.q_heads = has_q ? o.q_heads : 0;
+    a.interleaved = o.interleaved;
+    a.per = 1;
+    a.per_page = make_div64((uint32_t)(a.kv.page_size / kKvGroup));
+    return hip_status(launch_kv_append_rope(r.bias, r.x_f32, a, (hipStream_t)stream));
+}
+
 int fp4_kv_read(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
                 void* stream)
 {
@@ -954,6 +1006,107 @@ int fp4_linear(const fp4q_cfg* cfg, const uint16_t* x, int64_t M, int64_t ld_x, 
     a.parts = p.bytes > 0 ? (float*)workspace : nullptr;
     a.parts_ld = p.ld;
     return hip_status(launch_linear(r.bias, a, (hipStream_t)stream));
+}
+
+namespace {
+
+bool is_dtype(int32_t d) { return d == FP4Q_DTYPE_BF16 || d == FP4Q_DTYPE_FP32; }
+
+// Rows of the norm: hidden values in chunks of eight, pitches of whole 16 bytes.
+int check_norm(int64_t rows, int64_t hidden)
+{
+    if (rows < 0 || hidden < 8 || hidden % 8) return FP4Q_ERR_SHAPE;
+    if (hidden > 16384 || rows > ((int64_t)1 << 31) || rows * (hidden / 8) >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
+    return FP4Q_OK;
+}
+
+bool bad_pitch(int64_t rows, int64_t ld, int32_t dtype) { return rows > 1 && ld % (dtype == FP4Q_DTYPE_FP32 ? 4 : 8); }
+
+}  // namespace
+
+int fp4_add_rms_norm(const fp4q_add_rms_norm* norm, void* stream)
+{
+    if (!norm) return FP4Q_ERR_NULL;
+    const fp4q_add_rms_norm& o = *norm;
+    if (!is_dtype(o.x_dtype) || !is_dtype(o.residual_dtype) || !is_dtype(o.weight_dtype) || !is_dtype(o.y_dtype))
+        return FP4Q_ERR_DTYPE;
+    if (o.fp8_mode < 0 || o.fp8_mode > 2 || !(o.eps >= 0.0)) return FP4Q_ERR_MODE;
+    const int st = check_norm(o.rows, o.hidden);
+    if (st) return st;
+    if (o.fp8_mode == 1 && o.hidden % 32) return FP4Q_ERR_SHAPE;
+    if (o.rows > 1 && (o.ld_x < o.hidden || (o.residual && o.ld_residual < o.hidden))) return FP4Q_ERR_SHAPE;
+    if (o.rows == 0) return FP4Q_OK;
+    if (!o.x || !o.weight || (o.residual != nullptr) != (o.residual_out != nullptr)) return FP4Q_ERR_NULL;
+    if (o.fp8_mode != 0 && (!o.fp8 || !o.fp8_scales)) return FP4Q_ERR_NULL;
+    if (misaligned(o.x, 16) || misaligned(o.residual, 16) || misaligned(o.weight, 16) || misaligned(o.residual_out, 16) ||
+        misaligned(o.y, 16) || misaligned(o.rstd, 4) || (o.fp8_mode && misaligned(o.fp8, 16)) ||
+        (o.fp8_mode == 2 && misaligned(o.fp8_scales, 4)) || bad_pitch(o.rows, o.ld_x, o.x_dtype) ||
+        (o.residual && bad_pitch(o.rows, o.ld_residual, o.residual_dtype)))
+        return FP4Q_ERR_ALIGN;
+    NormArgs a;
+    a.x = o.x;
+    a.residual = o.residual;
+    a.ld_x = o.ld_x;
+    a.ld_r = o.ld_residual;
+    a.weight = o.weight;
+    a.residual_out = o.residual_out;
+    a.rstd = o.rstd;
+    a.y = o.y;
+    a.fp8 = o.fp8;
+    a.fp8_scales = o.fp8_scales;
+    a.rows = o.rows;
+    a.hidden = o.hidden;
+    a.eps = o.eps;
+    a.x_f32 = o.x_dtype == FP4Q_DTYPE_FP32;
+    a.r_f32 = o.residual_dtype == FP4Q_DTYPE_FP32;
+    a.w_f32 = o.weight_dtype == FP4Q_DTYPE_FP32;
+    a.y_f32 = o.y_dtype == FP4Q_DTYPE_FP32;
+    a.fp8_mode = o.fp8_mode;
+    return hip_status(launch_add_rms_norm(a, (hipStream_t)stream));
+}
+
+size_t fp4q_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t hidden)
+{
+    return check_norm(rows, hidden) ? 0 : plan_rms_norm_backward(rows, hidden).bytes;
+}
+
+int fp4_add_rms_norm_backward(const fp4q_rms_norm_grad* grad, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!grad) return FP4Q_ERR_NULL;
+    const fp4q_rms_norm_grad& o = *grad;
+    if (!is_dtype(o.dy_dtype) || !is_dtype(o.h_dtype) || !is_dtype(o.weight_dtype)) return FP4Q_ERR_DTYPE;
+    const int st = check_norm(o.rows, o.hidden);
+    if (st) return st;
+    if (o.rows > 1 && (o.ld_dy < o.hidden || o.ld_h < o.hidden || (o.dresidual && o.ld_dresidual < o.hidden)))
+        return FP4Q_ERR_SHAPE;
+    if (o.rows == 0 && !o.dweight) return FP4Q_OK;
+    if (!o.weight || (o.rows > 0 && (!o.dy || !o.h || !o.rstd || !o.dx))) return FP4Q_ERR_NULL;
+    if (misaligned(o.dy, 16) || misaligned(o.h, 16) || misaligned(o.dresidual, 16) || misaligned(o.weight, 16) ||
+        misaligned(o.rstd, 4) || misaligned(o.dx, 16) || misaligned(o.dweight, 16) || bad_pitch(o.rows, o.ld_dy, o.dy_dtype) ||
+        bad_pitch(o.rows, o.ld_h, o.h_dtype) || (o.dresidual && bad_pitch(o.rows, o.ld_dresidual, o.h_dtype)))
+        return FP4Q_ERR_ALIGN;
+    const NormGradPlan p = plan_rms_norm_backward(o.rows, o.hidden);
+    if (o.dweight && p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return FP4Q_ERR_WORKSPACE;
+    if (o.dweight && p.bytes > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
+    NormGradArgs a;
+    a.dy = o.dy;
+    a.h = o.h;
+    a.dres = o.dresidual;
+    a.ld_dy = o.ld_dy;
+    a.ld_h = o.ld_h;
+    a.ld_dres = o.ld_dresidual;
+    a.weight = o.weight;
+    a.rstd = o.rstd;
+    a.dx = o.dx;
+    a.dw = o.dweight;
+    a.parts = p.bytes > 0 ? (float*)workspace : nullptr;
+    a.rows = o.rows;
+    a.hidden = o.hidden;
+    a.dy_f32 = o.dy_dtype == FP4Q_DTYPE_FP32;
+    a.h_f32 = o.h_dtype == FP4Q_DTYPE_FP32;
+    a.w_f32 = o.weight_dtype == FP4Q_DTYPE_FP32;
+    a.groups = p.groups;
+    return hip_status(launch_rms_norm_backward(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

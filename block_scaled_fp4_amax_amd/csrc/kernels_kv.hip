@@ -58,30 +58,13 @@ __device__ __forceinline__ void load16(const void* p, float (&v)[16])
     }
 }
 
-// One lane quantises 16 values: a whole NVFP4 / AMD-FP4 block, or half of an
-// MXFP4 block whose other half is its neighbour's.  BIAS 0 is MXFP4.
-template <int BIAS, bool XF32>
-__global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
+// Quantises a lane's 16 values of a row of K or V and writes their codes and scale bytes: a
+// whole NVFP4 / AMD-FP4 block, or half of an MXFP4 block whose other half is its
+// neighbour's.
+template <int BIAS>
+__device__ __forceinline__ void quantise_row16(const KvView& kv, bool is_v, int head, int part, int64_t row,
+                                               float (&v)[16], const double* recip, const float2* rne)
 {
-    __shared__ double recip[kRecipTableSize];
-    __shared__ float2 rne[BIAS == 0 ? 1 : kRneTableSize];
-    if constexpr (BIAS != 0) {
-        fill_recip_table(recip, (int)threadIdx.x);
-        fill_rne_table<BIAS>(rne, (int)threadIdx.x);
-        __syncthreads();
-    }
-    const int lanes = a.kv.dim >> 4;                       // lanes of a row: 4, 8 or 16
-    const int head = (int)blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
-    const int part = (int)threadIdx.x % lanes;
-    if (token >= a.tokens) return;                         // whole rows leave together
-    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, head);
-    if (row < 0) return;
-    const char* x = (const char*)(is_v ? a.v : a.k);
-    const int64_t ld = is_v ? a.ld_v : a.ld_k;
-    float v[16];
-    load16<XF32>(x + (token * ld + (int64_t)head * a.kv.dim + part * 16) * (XF32 ? 4 : 2), v);
     uint2 code;
     uint32_t scale;
     if constexpr (BIAS == 0) {
@@ -107,7 +90,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
             scale = 0xFFu;
         }
     } else {
-        const float* outer = is_v ? a.kv.v_outer : a.kv.k_outer;
+        const float* outer = is_v ? kv.v_outer : kv.k_outer;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = sanitize(v[i]);
         if (outer) {
@@ -122,13 +105,185 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
         code = codes16_rne(v, rne[s.code]);
         scale = s.code;
     }
-    uint8_t* codes = is_v ? a.kv.v_codes : a.kv.k_codes;
-    uint8_t* scales = is_v ? a.kv.v_scales : a.kv.k_scales;
-    *(uint2*)(codes + row * (a.kv.dim / 2) + part * 8) = code;
+    uint8_t* codes = is_v ? kv.v_codes : kv.k_codes;
+    uint8_t* scales = is_v ? kv.v_scales : kv.k_scales;
+    *(uint2*)(codes + row * (kv.dim / 2) + part * 8) = code;
     if constexpr (BIAS == 0) {
-        if ((part & 1) == 0) scales[row * (a.kv.dim / 32) + part / 2] = (uint8_t)scale;
+        if ((part & 1) == 0) scales[row * (kv.dim / 32) + part / 2] = (uint8_t)scale;
     } else {
-        scales[row * (a.kv.dim / 16) + part] = (uint8_t)scale;
+        scales[row * (kv.dim / 16) + part] = (uint8_t)scale;
+    }
+}
+
+// BIAS 0 is MXFP4.
+template <int BIAS, bool XF32>
+__global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
+{
+    __shared__ double recip[kRecipTableSize];
+    __shared__ float2 rne[BIAS == 0 ? 1 : kRneTableSize];
+    if constexpr (BIAS != 0) {
+        fill_recip_table(recip, (int)threadIdx.x);
+        fill_rne_table<BIAS>(rne, (int)threadIdx.x);
+        __syncthreads();
+    }
+    const int lanes = a.kv.dim >> 4;                       // lanes of a row: 4, 8 or 16
+    const int head = (int)blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
+    const int part = (int)threadIdx.x % lanes;
+    if (token >= a.tokens) return;                         // whole rows leave together
+    const int64_t row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, head);
+    if (row < 0) return;
+    const char* x = (const char*)(is_v ? a.v : a.k);
+    const int64_t ld = is_v ? a.ld_v : a.ld_k;
+    float v[16];
+    load16<XF32>(x + (token * ld + (int64_t)head * a.kv.dim + part * 16) * (XF32 ? 4 : 2), v);
+    quantise_row16<BIAS>(a.kv, is_v, head, part, row, v, recip, rne);
+}
+
+// Rotation of a lane's 16 values of a row by its token's angles, then as above.
+//
+// A pair (a, b) of the first rot_dim values turns into (a c - b s, b c + a s), each product,
+// sum and difference rounded to binary32: value j and j + rot_dim / 2, or 2 j and 2 j + 1
+// (interleaved), with c and s at place j of the token's row of the tables.  rot_dim is a multiple
+// of 16, so a chunk of eight values lies in one half, or beyond; where its partners are
+// another chunk, the lane loads that one too (from the caches, where its own lane's
+// load brings it).
+template <bool XF32>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8])
+{
+    const char* q = (const char*)p + at * (XF32 ? 4 : 2);
+    if constexpr (XF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 u = ((const float4*)q)[i];
+            v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+        }
+    } else {
+        const uint4 u = *(const uint4*)q;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+    }
+}
+
+// The angles of a chunk of eight values from `at`: eight of each (halves), or four (interleaved).
+struct Angles {
+    float c[8], s[8];
+    int partner;                                         // distance to the pair's other chunk; 0: no rotation
+
+    __device__ __forceinline__ void load(const KvRopeArgs& a, int64_t position, int at)
+    {
+        const int half = a.rot >> 1;
+        partner = at >= a.rot ? 0 : a.interleaved ? 1 : at < half ? half : -half;
+        if (partner == 0) return;
+        const int64_t from = position * half + (a.interleaved ? at >> 1 : at < half ? at : at - half);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i == 1 && a.interleaved) break;
+            const float4 u = ((const float4*)(a.cos + from))[i], w = ((const float4*)(a.sin + from))[i];
+            c[4 * i] = u.x, c[4 * i + 1] = u.y, c[4 * i + 2] = u.z, c[4 * i + 3] = u.w;
+            s[4 * i] = w.x, s[4 * i + 1] = w.y, s[4 * i + 2] = w.z, s[4 * i + 3] = w.w;
+        }
+    }
+
+    // x: the chunk's values; p: their partners' (halves)
+    __device__ __forceinline__ void turn(bool interleaved, const float (&x)[8], const float (&p)[8], float (&y)[8]) const
+    {
+        if (interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
+                y[2 * j + 1] = x[2 * j + 1] * c[j] + x[2 * j] * s[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float other = p[j] * s[j];
+                y[j] = partner > 0 ? x[j] * c[j] - other : x[j] * c[j] + other;
+            }
+        }
+    }
+};
+
+// A workgroup takes `per` heads of K, of V or of q (blockIdx.y) for a run of tokens: a lane keeps its
+// angles for all of them.
+template <int BIAS, bool XF32>
+__global__ __launch_bounds__(kThreads) void k_kv_append_rope(KvRopeArgs a)
+{
+    __shared__ double recip[kRecipTableSize];
+    __shared__ float2 rne[BIAS == 0 ? 1 : kRneTableSize];
+    int unit = (int)blockIdx.y;
+    const int kv_units = (a.kv.heads + a.per - 1) / a.per;
+    const bool is_q = unit >= 2 * kv_units, is_v = !is_q && unit >= kv_units;
+    unit -= is_q ? 2 * kv_units : is_v ? kv_units : 0;
+    if constexpr (BIAS != 0) {
+        if (!is_q) {                                     // the same for the whole workgroup
+            fill_recip_table(recip, (int)threadIdx.x);
+            fill_rne_table<BIAS>(rne, (int)threadIdx.x);
+            __syncthreads();
+        }
+    }
+    const int lanes = a.kv.dim >> 4;
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
+    const int part = (int)threadIdx.x % lanes;
+    if (token >= a.tokens) return;
+    const int64_t position = a.positions[token];
+    const bool known = position >= 0 && position < a.table_rows;
+    const int heads = is_q ? a.q_heads : a.kv.heads, h0 = unit * a.per, h1 = min(heads, h0 + a.per);
+    const char* x = (const char*)(is_q ? a.q : is_v ? a.v : a.k);
+    const int64_t ld = is_q ? a.ld_q : is_v ? a.ld_v : a.ld_k;
+    int64_t row = -1;
+    if (!is_q) {
+        if (known) row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, h0);
+        if (row < 0) return;                             // a row's lanes leave together
+    }
+    Angles turn[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        turn[i].partner = 0;
+        if (!is_v && known) turn[i].load(a, position, part * 16 + 8 * i);
+    }
+    for (int head = h0; head < h1; ++head, row += a.kv.page_size) {
+        const int64_t at = token * ld + (int64_t)head * a.kv.dim + part * 16;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float own[8], other[8], y[8];
+            load8<XF32>(x, at + 8 * i, own);
+            if (turn[i].partner != 0) {
+                if (!a.interleaved) load8<XF32>(x, at + 8 * i + turn[i].partner, other);
+                turn[i].turn(a.interleaved != 0, own, other, y);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = own[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * i + j] = y[j];
+        }
+        if (!is_q) {
+            quantise_row16<BIAS>(a.kv, is_v, head, part, row, v, recip, rne);
+            continue;
+        }
+        // q_out may be q: every lane of the row has its values before one of them stores
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int64_t to = token * a.ld_out + (int64_t)head * a.kv.dim + part * 16;
+        if (!known) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+        }
+        if (XF32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *(float4*)((float*)a.q_out + to + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *(uint4*)((uint16_t*)a.q_out + to + 8 * i) =
+                    make_uint4(Dec<0>::round2(v[8 * i], v[8 * i + 1]), Dec<0>::round2(v[8 * i + 2], v[8 * i + 3]),
+                               Dec<0>::round2(v[8 * i + 4], v[8 * i + 5]), Dec<0>::round2(v[8 * i + 6], v[8 * i + 7]));
+        }
     }
 }
 
@@ -211,6 +366,28 @@ hipError_t launch_kv_append(int bias, bool x_f32, const KvAppendArgs& a, hipStre
     else if (bias == 7) FP4Q_APPEND(7);
     else FP4Q_APPEND(15);
 #undef FP4Q_APPEND
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_append_rope(int bias, bool x_f32, const KvRopeArgs& given, hipStream_t s)
+{
+    KvRopeArgs a = given;
+    const int rows = kThreads / (a.kv.dim / 16);
+    const int64_t runs = (a.tokens + rows - 1) / rows;
+    // heads of a workgroup: as many as leave four workgroups a compute unit
+    a.per = 1;
+    while (a.per < 8 && runs * (2 * a.kv.heads + a.q_heads) / (2 * a.per) >= 1024) a.per *= 2;
+    const int units = 2 * ((a.kv.heads + a.per - 1) / a.per) + (a.q_heads + a.per - 1) / a.per;
+    const dim3 grid((uint32_t)runs, (uint32_t)units);
+#define FP4Q_ROPE(B)                                                                                    \
+    do {                                                                                                \
+        if (x_f32) hipLaunchKernelGGL((k_kv_append_rope<B, true>), grid, dim3(kThreads), 0, s, a);      \
+        else hipLaunchKernelGGL((k_kv_append_rope<B, false>), grid, dim3(kThreads), 0, s, a);           \
+    } while (0)
+    if (bias == 0) FP4Q_ROPE(0);
+    else if (bias == 7) FP4Q_ROPE(7);
+    else FP4Q_ROPE(15);
+#undef FP4Q_ROPE
     return hipGetLastError();
 }
 

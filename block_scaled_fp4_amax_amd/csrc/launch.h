@@ -251,7 +251,22 @@ struct KvReadArgs {
     DivBy64 per_page;
 };
 
+struct KvRopeArgs {
+    KvView kv;
+    const void *k, *v, *q;   // bf16 or FP32 [tokens, heads or q_heads, dim], token pitches in elements
+    void* q_out;
+    int64_t ld_k, ld_v, ld_q, ld_out;
+    const int64_t* slots;    // [tokens]
+    const int32_t* positions;   // [tokens]
+    const float *cos, *sin;  // [table_rows, rot / 2]
+    int64_t tokens, table_rows, num_slots;
+    int32_t rot, q_heads, interleaved;
+    int32_t per;             // heads of a workgroup (set by the launcher)
+    DivBy64 per_page;
+};
+
 // bias: 7 (E4M3), 15 (UE5M3) or 0 (MXFP4)
+hipError_t launch_kv_append_rope(int bias, bool x_f32, const KvRopeArgs& a, hipStream_t s);
 hipError_t launch_kv_append(int bias, bool x_f32, const KvAppendArgs& a, hipStream_t s);
 hipError_t launch_kv_read(int bias, bool y_f32, const KvReadArgs& a, hipStream_t s);
 
@@ -311,6 +326,45 @@ struct LinearPlan {
 
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(int bias, const LinearArgs& a, hipStream_t s);
+
+// h = x + residual, its root-mean-square norm times a weight, and E4M3 codes of that.
+enum { kFp8None = 0, kFp8Mx = 1, kFp8Row = 2 };
+
+struct NormArgs {
+    const void *x, *residual;  // bf16 or FP32 [rows, hidden], row pitches in elements; residual may be null
+    int64_t ld_x, ld_r;
+    const void* weight;        // bf16 or FP32 [hidden]
+    void* residual_out;        // [rows, hidden], the residual's type
+    float* rstd;               // [rows] or null
+    void* y;                   // bf16 or FP32 [rows, hidden] or null
+    uint8_t* fp8;              // [rows, hidden]
+    void* fp8_scales;          // UE8M0 bytes [rows, hidden / 32] or FP32 [rows]
+    int64_t rows, hidden;
+    double eps;
+    int32_t x_f32, r_f32, w_f32, y_f32, fp8_mode;
+};
+
+hipError_t launch_add_rms_norm(const NormArgs& a, hipStream_t s);
+
+struct NormGradArgs {
+    const void *dy, *h, *dres; // [rows, hidden], dres of h's type or null
+    int64_t ld_dy, ld_h, ld_dres;
+    const void* weight;
+    const float* rstd;         // [rows]
+    void* dx;                  // [rows, hidden], h's type
+    float* dw;                 // [hidden] or null
+    float* parts;              // [groups, hidden], null with one workgroup
+    int64_t rows, hidden;
+    int32_t dy_f32, h_f32, w_f32, groups;
+};
+
+struct NormGradPlan {
+    int32_t groups;
+    size_t bytes;
+};
+
+NormGradPlan plan_rms_norm_backward(int64_t rows, int64_t hidden);
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s);
 
 // partial maxima used by the tensorwise amax pass
 constexpr int kAmaxPartials = 512;

@@ -477,6 +477,39 @@ typedef struct {
 int fp4_kv_append(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const void* k, int64_t ld_k, const void* v,
                   int64_t ld_v, const int64_t* slots, int64_t tokens, void* stream);
 
+/* One call of fp4_kv_append_rope (device pointers; the struct is read during the call). */
+typedef struct {
+    const void *k, *v;         /* as in fp4_kv_append: bf16 or FP32 (cfg->input_dtype) [tokens,
+                                  kv_heads, head_dim], token pitches ld_k and ld_v               */
+    const void* q;             /* the same type, [tokens, q_heads, head_dim], token pitch ld_q, or
+                                  NULL                                                          */
+    void* q_out;               /* q's type, [tokens, q_heads, head_dim], token pitch ld_q_out,
+                                  written; may be q itself, with its pitch                      */
+    int64_t ld_k, ld_v, ld_q, ld_q_out;
+    const int64_t* slots;      /* [tokens]                                                      */
+    const int32_t* positions;  /* [tokens]: a token's row of the tables                         */
+    const float *cos, *sin;    /* FP32 [table_rows, rot_dim / 2], 16-byte aligned                */
+    int64_t tokens, table_rows;
+    int32_t rot_dim;           /* values of a head that turn: a multiple of 16, up to head_dim    */
+    int32_t q_heads;
+    int32_t interleaved;       /* pairs are values 2 j and 2 j + 1; else j and j + rot_dim / 2     */
+    int32_t reserved;
+} fp4q_kv_rope;
+
+/*
+ * fp4_kv_append_rope -- fp4_kv_append of keys that are turned by their positions on the
+ * way, and the queries of the same tokens turned too, in one launch.
+ *   A pair (a, b) of the first rot_dim values of a head, with c and s at place j of row
+ *   positions[t] of the tables, becomes (a c - b s, b c + a s), each product, sum and
+ *   difference rounded to binary32.  Keys are quantised from that without another
+ *   rounding; q_out is rounded to its type.  Values from rot_dim on, and V, stay as they are.
+ * A position outside the tables marks padding: nothing of the token is written to the
+ * cache, and its row of q_out is zeros.  Everything else (slots, padding, NaN and
+ * infinities, alignments, limits) as in fp4_kv_append; q and q_out 16-byte aligned with pitches of
+ * a whole number of 16 bytes (ignored for one token), q_heads <= 65535 (FP4Q_ERR_UNSUPPORTED).
+ */
+int fp4_kv_append_rope(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_kv_rope* rope, void* stream);
+
 /*
  * fp4_kv_read -- the values that slots of the cache hold, dequantised as by
  * fp4_dequantize.
@@ -546,6 +579,72 @@ typedef struct {
 size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn);
 int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
              size_t workspace_bytes, void* stream);
+
+/* One call of fp4_add_rms_norm (device pointers; the struct is read during the call). */
+typedef struct {
+    const void *x, *residual;  /* [rows, hidden], row pitches ld_x and ld_residual elements
+                                  (>= hidden, a whole number of 16 bytes; ignored for one row);
+                                  residual may be NULL                                          */
+    int64_t ld_x, ld_residual;
+    const void* weight;        /* [hidden]                                                      */
+    void* residual_out;        /* h [rows, hidden] in the residual's type, written; may be residual
+                                  itself where that is contiguous; NULL without a residual       */
+    float* rstd;               /* r [rows] or NULL                                              */
+    void* y;                   /* [rows, hidden] or NULL                                        */
+    uint8_t* fp8;              /* E4M3 codes of y [rows, hidden] (fp8_mode)                      */
+    void* fp8_scales;          /* UE8M0 bytes [rows, hidden / 32], or FP32 [rows]                */
+    int64_t rows, hidden;
+    double eps;                /* >= 0                                                          */
+    int32_t x_dtype, residual_dtype, weight_dtype, y_dtype;   /* FP4Q_DTYPE_BF16 or _FP32        */
+    int32_t fp8_mode;          /* 0: no codes; 1: a scale for 32 values; 2: one for a row        */
+    int32_t reserved;
+} fp4q_add_rms_norm;
+
+/*
+ * fp4_add_rms_norm -- the residual's addition, the root-mean-square norm, and its output in
+ * bf16 or FP32, in 8 bits with scales, or both.
+ *   h = x + residual (binary32, then rounded to the residual's type; x without one)
+ *   r = 1 / sqrt(mean(h^2) + eps)  in binary64 from h as stored, rounded to binary32
+ *   y = (h r) w                    each product rounded to binary32
+ * Codes are E4M3 of y / scale, round to nearest even with subnormals, at most 448 in
+ * magnitude, NaN kept, with
+ *   fp8_mode 1  the scale of fp4_mx_project_fp8's mx8_row: 2^E for 32 values, E = floor(log2 amax) - 8
+ *               within [-127, 127] (byte 0 where there is no finite nonzero value); hidden % 32 == 0;
+ *   fp8_mode 2  amax / 448 for a row, in binary32, and the quotients rounded to binary32 first;
+ * amax over the finite values of y before it is rounded to y_dtype.  Results do not depend on how
+ * rows are shared among lanes, so equal rows give equal bits in every call.
+ * Needs hidden % 8 == 0 (FP4Q_ERR_SHAPE), hidden <= 16384 and rows < 2^31 / (hidden / 8)
+ * (FP4Q_ERR_UNSUPPORTED), all buffers but rstd and fp8_scales 16-byte aligned.
+ */
+int fp4_add_rms_norm(const fp4q_add_rms_norm* norm, void* stream);
+
+/* One call of fp4_add_rms_norm_backward (device pointers; the struct is read during the call). */
+typedef struct {
+    const void* dy;            /* the gradient of y [rows, hidden], row pitch ld_dy              */
+    const void* h;             /* [rows, hidden] as the forward call stored it, row pitch ld_h   */
+    const void* dresidual;     /* the gradient of residual_out, h's type, row pitch ld_dresidual,
+                                  or NULL                                                       */
+    int64_t ld_dy, ld_h, ld_dresidual;
+    const void* weight;        /* [hidden]                                                      */
+    const float* rstd;         /* [rows] of the forward call                                    */
+    void* dx;                  /* [rows, hidden], h's type: the gradient of x and of residual, written;
+                                  may be dresidual itself where that is contiguous               */
+    float* dweight;            /* FP32 [hidden] or NULL, written                                 */
+    int64_t rows, hidden;
+    int32_t dy_dtype, h_dtype, weight_dtype, reserved;
+} fp4q_rms_norm_grad;
+
+/*
+ * fp4_add_rms_norm_backward -- the gradient of fp4_add_rms_norm (of y; the 8-bit codes pass theirs on as if
+ * they were y).
+ *   n = h r,  g = dy w,  dx = r (g - n mean(n g)) + dresidual,  dweight = sum over rows of dy n
+ * in binary32, the rows' sums joined in binary64.  workspace:
+ * fp4q_add_rms_norm_backward_workspace_bytes() bytes, 16-byte aligned, no initial value.  How rows
+ * are shared, and so the last bits of dweight, depends on rows and hidden alone.
+ * rows == 0 writes zeros to dweight.  Limits and alignments as in fp4_add_rms_norm.
+ */
+size_t fp4q_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t hidden);
+int fp4_add_rms_norm_backward(const fp4q_rms_norm_grad* grad, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
