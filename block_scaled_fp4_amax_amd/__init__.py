@@ -3,7 +3,7 @@ block-scaled FP4 quantisation library.
 
 The functions carry the C-ABI names (fp4_quantize, fp4_dequantize, fp4_qdq,
 fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_linear,
-fp4_kv_append, fp4_kv_append_rope, fp4_kv_read, fp4_attn, fp4_add_rms_norm,
+fp4_kv_append, fp4_kv_append_rope, fp4_kv_read, fp4_attn, fp4_attn_tree, fp4_add_rms_norm,
 fp4_add_rms_norm_backward and the fp4q_* helpers).  They
 only marshal arguments: torch supplies device memory and the current HIP
 stream, every step of the computation runs in the library's HIP kernels.  If
@@ -19,7 +19,7 @@ __all__ = [
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
     "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "fp4q_linear_workspace_bytes", "KVCache", "fp4_kv_append",
-    "fp4_kv_append_rope", "fp4_kv_read", "fp4_attn", "fp4_attn_workspace", "fp4_add_rms_norm", "fp4_add_rms_norm_backward",
+    "fp4_kv_append_rope", "fp4_kv_read", "fp4_attn", "fp4_attn_tree", "fp4_attn_workspace", "fp4_add_rms_norm", "fp4_add_rms_norm_backward",
     "fp4q_add_rms_norm_backward_workspace_bytes", "LIB_PATH",
 ]
 
@@ -177,6 +177,8 @@ def lib():
         L.fp4q_attn_workspace_bytes.argtypes = [C, KV, AT]
         L.fp4_attn.restype = ct.c_int
         L.fp4_attn.argtypes = [C, KV, AT, P, SZ, P]
+        L.fp4_attn_tree.restype = ct.c_int
+        L.fp4_attn_tree.argtypes = [C, KV, AT, P, ct.c_int32, P, SZ, P]
         L.fp4_linear.restype = ct.c_int
         L.fp4_linear.argtypes = [C, P, I64, I64, P, P, P, ct.c_int32, I64, I64, P, I64, P, SZ, P]
         L.fp4q_linear_workspace_bytes.restype = SZ
@@ -859,7 +861,7 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
 
 
 def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv=None, scale=None, causal=True, window=0,
-             sinks=None, out=None, out_dtype=None, with_lse=False, workspace=None, stream=None):
+             sinks=None, out=None, out_dtype=None, with_lse=False, workspace=None, stream=None, _tree=None):
     """Attention of q (bf16 [tokens, q_heads, head_dim]) over the cache (see
     include/fp4q.h for masks, limits and rounding).
 
@@ -917,8 +919,31 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
-    _launch("fp4_attn", lib().fp4_attn, dev, cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev))
+    if _tree is None:
+        _launch("fp4_attn", lib().fp4_attn, dev, cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev))
+    else:
+        _launch("fp4_attn_tree", lib().fp4_attn_tree, dev, cfg, cache._ref, a, _tree.data_ptr(), _tree.shape[1], scratch,
+                size, _raw_stream(stream, dev))
     return (out, lse) if with_lse else out
+
+
+def fp4_attn_tree(q, cache, page_table, kv_lens, q_starts, tree, **kw):
+    """fp4_attn of trees of drafted tokens: each sequence's queries are the nodes of its tree, and
+    their keys are the last of its kv_lens.
+
+    tree   bool (or uint8) [tokens, cols]: row i names the drafted keys of its sequence that query i sees,
+           by their place in the tree (its ancestors and itself); all see the whole context before them, or
+           with a window as much of it as makes the window full.
+    Other arguments (but causal) and results as in fp4_attn; fp4_attn_workspace sizes these calls too."""
+    torch = _torch()
+    if tree.dim() != 2 or tree.shape[0] != q.shape[0] or tree.dtype not in (torch.bool, torch.uint8):
+        raise ValueError("tree must be bool or uint8 [%d, cols], got %s %s" % (q.shape[0], tree.dtype, list(tree.shape)))
+    if not tree.is_contiguous() or tree.device != cache.device:
+        raise ValueError("tree must be contiguous and on %s" % cache.device)
+    if "causal" in kw:
+        raise TypeError("fp4_attn_tree takes no causal")
+    _ints32("fp4_attn_tree", tree.shape[1])
+    return fp4_attn(q, cache, page_table, kv_lens, q_starts, _tree=tree, **kw)
 
 
 # ------------------------------------------------------------------ residual and norm

@@ -892,8 +892,11 @@ size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache
     return attn_bytes(p);
 }
 
-int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
-             size_t workspace_bytes, void* stream)
+namespace {
+
+// fp4_attn, or fp4_attn_tree with its mask.
+int attn_call(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, bool is_tree, const uint8_t* tree,
+              int32_t tree_cols, void* workspace, size_t workspace_bytes, void* stream)
 {
     Resolved r;
     AttnArgs a;
@@ -901,8 +904,12 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     if (st) return st;
     st = check_attn(a.kv, attn);
     if (st) return st;
+    if (is_tree && !attn->causal) return FP4Q_ERR_MODE;
+    if (tree_cols < 0) return FP4Q_ERR_SHAPE;
+    // a sequence's rows of the mask are addressed with 31 bits
+    if ((int64_t)attn->max_q * tree_cols >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
     if (attn->batch == 0 || attn->total_q == 0 || attn->max_q == 0) return FP4Q_OK;
-    if (!attn->q || !attn->kv_lens || !attn->out || (attn->table_cols > 0 && !attn->page_table))
+    if (!attn->q || !attn->kv_lens || !attn->out || (attn->table_cols > 0 && !attn->page_table) || (tree_cols > 0 && !tree))
         return FP4Q_ERR_NULL;
     if (misaligned(attn->q, 16) || misaligned(attn->out, 16) || misaligned(attn->page_table, 4) ||
         misaligned(attn->kv_lens, 4) || misaligned(attn->q_starts, 4) || misaligned(attn->sinks, 4) ||
@@ -940,8 +947,24 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.out_f32 = r.y_f32 ? 1 : 0;
+    a.tree = tree;
+    a.tree_cols = tree_cols;
     a.per_page = make_div((uint32_t)(a.kv.page_size / kKvGroup));
-    return hip_status(launch_attn(r.bias, a, (hipStream_t)stream));
+    return hip_status(is_tree ? launch_attn_tree(r.bias, a, (hipStream_t)stream) : launch_attn(r.bias, a, (hipStream_t)stream));
+}
+
+}  // namespace
+
+int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
+             size_t workspace_bytes, void* stream)
+{
+    return attn_call(cfg, cache, attn, false, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int fp4_attn_tree(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, const uint8_t* tree,
+                  int32_t tree_cols, void* workspace, size_t workspace_bytes, void* stream)
+{
+    return attn_call(cfg, cache, attn, true, tree, tree_cols, workspace, workspace_bytes, stream);
 }
 
 size_t fp4q_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)

@@ -134,6 +134,17 @@ FP4Q_HD KeyRange key_range(int32_t i, int32_t n, int32_t kv, int32_t causal, int
     return KeyRange{lo, hi};
 }
 
+// Keys [lo, hi) of the context, the kv - n keys before n drafted ones, that a query sees which sees
+// `drafted` of those: all, or with a window as many as leave `window` with the drafted keys (one
+// at least).
+FP4Q_HD KeyRange tree_context(int32_t kv, int32_t n, int32_t window, int32_t drafted)
+{
+    const int32_t end = kv > n ? kv - n : 0;
+    if (window <= 0) return KeyRange{0, end};
+    const int64_t lo = (int64_t)end + (drafted > 1 ? drafted : 1) - window;
+    return KeyRange{lo < 0 ? 0 : lo < end ? (int32_t)lo : end, end};
+}
+
 // ---------------------------------------------------------------- keys of many rows
 // A workgroup of many rows walks the keys of its rows in rounds of kv_round(head_dim) keys, from the
 // round of the first row's first key.  Its keys may be cut into `splits` parts of `chunk` keys (a

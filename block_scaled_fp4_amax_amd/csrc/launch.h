@@ -287,6 +287,8 @@ struct AttnArgs {
     int32_t slots, groups;   // few rows: workgroups that the chip holds (0: keys are not cut), workgroups
     int32_t splits, chunk;   // many rows: parts of a sequence's keys and the keys of one (a multiple of 128)
     int32_t out_f32;
+    const uint8_t* tree;     // fp4_attn_tree: [total_q, tree_cols], drafted keys that a query sees
+    int32_t tree_cols;
     DivBy per_page;          // 16-token groups of a page
 };
 
@@ -299,6 +301,7 @@ struct AttnPlan {
 AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_heads, int64_t max_q, int64_t max_kv,
                    int64_t table_cols, int64_t window);
 hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_tree(int bias, const AttnArgs& a, hipStream_t s);
 
 // y = x W^T with bf16 x [M, ld_x] and a 4-bit W [N, K] (rowwise codes and scale bytes).
 struct LinearArgs {

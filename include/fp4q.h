@@ -580,6 +580,22 @@ size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache
 int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, void* workspace,
              size_t workspace_bytes, void* stream);
 
+/*
+ * fp4_attn_tree -- fp4_attn of trees of drafted tokens: each sequence's queries are the n nodes of
+ * its tree, whose keys and values are the last n of its kv_lens[b] keys, in the same order.
+ *   tree       uint8 [total_q, tree_cols] device: query i sees drafted key j of its sequence where
+ *              tree[i][j] is not 0 (its ancestors and itself, for a tree; any other set
+ *              works too).  Drafted keys from tree_cols on are not seen.
+ * Every query sees the whole context, the kv_lens[b] - n keys before the drafted ones; with a window
+ * only its last keys, as many as make `window` with the c drafted keys that its row of the mask names
+ * (c of 0 counts as 1, and all c are seen even where they are more).  Where n is more than
+ * kv_lens[b], the first of the drafted tokens have no key.
+ * causal has to be 1 (FP4Q_ERR_MODE), max_q * tree_cols < 2^31 (FP4Q_ERR_UNSUPPORTED).  Everything else as in
+ * fp4_attn, the workspace's size too.
+ */
+int fp4_attn_tree(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, const uint8_t* tree,
+                  int32_t tree_cols, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One call of fp4_add_rms_norm (device pointers; the struct is read during the call). */
 typedef struct {
     const void *x, *residual;  /* [rows, hidden], row pitches ld_x and ld_residual elements
