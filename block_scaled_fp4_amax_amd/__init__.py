@@ -177,6 +177,8 @@ def lib():
         L.fp4q_attn_workspace_bytes.argtypes = [C, KV, AT]
         L.fp4_attn.restype = ct.c_int
         L.fp4_attn.argtypes = [C, KV, AT, P, SZ, P]
+        L.fp4q_attn_tree_workspace_bytes.restype = SZ
+        L.fp4q_attn_tree_workspace_bytes.argtypes = [C, KV, AT]
         L.fp4_attn_tree.restype = ct.c_int
         L.fp4_attn_tree.argtypes = [C, KV, AT, P, ct.c_int32, P, SZ, P]
         L.fp4_linear.restype = ct.c_int
@@ -843,7 +845,7 @@ def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
 
 
 def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=None, table_cols=None, window=0):
-    """Scratch for fp4_attn calls of this size (None if they need none), to keep
+    """Scratch for fp4_attn and fp4_attn_tree calls of this size (None if they need none), to keep
     between calls.  max_q, max_kv, window and table_cols as in the call; without
     table_cols, the columns that max_kv needs."""
     torch = _torch()
@@ -856,7 +858,8 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
     _ints32("fp4_attn_workspace", *n)
     a = _Attn(batch=n[0], total_q=n[1], q_heads=n[2], table_cols=n[3], max_q=n[4], max_kv=n[5], causal=1, window=n[6],
               scale=1.0, ld_q=n[2] * cache.head_dim, q_starts=16)
-    n = lib().fp4q_attn_workspace_bytes(ct.byref(cache.cfg), cache._ref, ct.byref(a))
+    n = max(f(ct.byref(cache.cfg), cache._ref, ct.byref(a))
+            for f in (lib().fp4q_attn_workspace_bytes, lib().fp4q_attn_tree_workspace_bytes))
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
 
@@ -913,7 +916,7 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
                        D ** -0.5 if scale is None else scale, batch, T, Hq, cols, max_q, max_kv, 1 if causal else 0,
                        window))
     if workspace is None:
-        need = lib().fp4q_attn_workspace_bytes(cfg, cache._ref, a)
+        need = (lib().fp4q_attn_workspace_bytes if _tree is None else lib().fp4q_attn_tree_workspace_bytes)(cfg, cache._ref, a)
         if need:
             workspace = _new(need, torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():

@@ -61,6 +61,7 @@ constexpr int kWaves = 4;
 constexpr int kUnit = 128;                               // keys that a workgroup of few rows takes at once
 constexpr int kMinShare = 4;                             // units of a workgroup's share, at least
 constexpr int kFewRows = 32;
+constexpr int kMinRounds = 4;                            // rounds of a part of a tree's keys, at least
 constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
@@ -918,32 +919,11 @@ __global__ __launch_bounds__(64 * kWaves, QT == 1 && D == 64 ? 4 : D == 256 && Q
     else write_parts<D, BIAS, QT, TREE>(a, rows, sum, (int64_t)blockIdx.x * (16 * QT), false, lane);
 }
 
-// Joins the parts of one row a wave.
-template <int D, int QT, bool TREE>
-__global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift)
+// Joins the parts of one row (of a sequence and head) from their places in the scratch.
+template <int D, class PartRow>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int parts, PartRow part_row, const QueryRange& qr, int row,
+                                           int head, float unshift, int lane)
 {
-    const int lane = (int)threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int row = (int)blockIdx.x * 4 + wave;          // of a sequence and head
-    const int head = (int)blockIdx.y, seq = (int)blockIdx.z;
-    const QueryRange qr = queries_of(a, seq);
-    if (row >= qr.count * a.group) return;
-    int total = 0;
-    Seq mine = seq_of_chunk<TREE>(a, 0, lane);
-    total = __builtin_amdgcn_readlane(lane_sums(mine.units), 63);
-    for (int b = 64; b < a.batch; b += 64)
-        total += __builtin_amdgcn_readlane(lane_sums(seq_of_chunk<TREE>(a, b, lane).units), 63);
-    const int share = share_of(total, a);
-    int first = 0;                                       // parts of a head before this sequence's
-    for (int b0 = 0; b0 + 64 <= seq; b0 += 64) {
-        first += __builtin_amdgcn_readlane(lane_sums(parts_of(mine.units, share)), 63);
-        mine = seq_of_chunk<TREE>(a, b0 + 64, lane);
-    }
-    const int n = parts_of(mine.units, share), upto = lane_sums(n);
-    const int parts = __builtin_amdgcn_readlane(n, seq & 63);
-    first += __builtin_amdgcn_readlane(upto, seq & 63) - parts;
-    if (parts <= 1) return;
-    const auto part_row = [&](int p) { return ((int64_t)(first + p) * a.kv.heads + head) * (16 * QT) + row; };
     constexpr int N = D / 64;
     float acc[N] = {}, l = 0.0f, top = kNoMax;
     for (int p0 = 0; p0 < parts; p0 += 64) {
@@ -978,6 +958,35 @@ __global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift
     }
     const int i = row / a.group, qh = head * a.group + row - i * a.group;
     write_joined<D>(a, (int64_t)(qr.first + i) * a.q_heads + qh, qh, top, l, acc, unshift, lane);
+}
+
+// Joins the parts of one row a wave.
+template <int D, int QT, bool TREE>
+__global__ __launch_bounds__(256) void k_attn_few_join(AttnArgs a, float unshift)
+{
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = (int)blockIdx.x * 4 + wave;          // of a sequence and head
+    const int head = (int)blockIdx.y, seq = (int)blockIdx.z;
+    const QueryRange qr = queries_of(a, seq);
+    if (row >= qr.count * a.group) return;
+    int total = 0;
+    Seq mine = seq_of_chunk<TREE>(a, 0, lane);
+    total = __builtin_amdgcn_readlane(lane_sums(mine.units), 63);
+    for (int b = 64; b < a.batch; b += 64)
+        total += __builtin_amdgcn_readlane(lane_sums(seq_of_chunk<TREE>(a, b, lane).units), 63);
+    const int share = share_of(total, a);
+    int first = 0;                                       // parts of a head before this sequence's
+    for (int b0 = 0; b0 + 64 <= seq; b0 += 64) {
+        first += __builtin_amdgcn_readlane(lane_sums(parts_of(mine.units, share)), 63);
+        mine = seq_of_chunk<TREE>(a, b0 + 64, lane);
+    }
+    const int n = parts_of(mine.units, share), upto = lane_sums(n);
+    const int parts = __builtin_amdgcn_readlane(n, seq & 63);
+    first += __builtin_amdgcn_readlane(upto, seq & 63) - parts;
+    if (parts <= 1) return;
+    const auto part_row = [&](int p) { return ((int64_t)(first + p) * a.kv.heads + head) * (16 * QT) + row; };
+    join_parts<D>(a, parts, part_row, qr, row, head, unshift, lane);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -1169,6 +1178,102 @@ struct DecodePart {
     }
 };
 
+// Trees: the rows of a sequence and head are its tiles, whose keys are cut, as those of few rows are, into
+// parts of at most `share` rounds, chosen on the device so that all sequences' parts fill the
+// chip about once; k_attn_tree_join joins them.  A part costs a first trip to memory and its share of the join, and
+// whole sequences leave compute units idle behind the longest: 16 trees of up to 64 nodes after up to 8192
+// keys (MXFP4, 64 / 8 heads of 64) 157 us uncut, 4 of 26 after up to 131072 (NVFP4, 32 / 8 of 128) 603 with
+// parts for one workgroup a compute unit.
+struct TreeSeq {
+    int units, tiles;                                    // rounds of its keys, tiles of its rows
+};
+
+template <int D>
+__device__ __forceinline__ TreeSeq tree_seq(const AttnArgs& a, int b)
+{
+    if (b >= a.batch) return TreeSeq{0, 0};
+    const QueryRange qr = queries_of(a, b);
+    const int kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
+    const int lo = tree_context(kv, qr.count, a.window, 0).lo / kv_round(D) * kv_round(D);
+    return TreeSeq{max(1, (kv - lo + kv_round(D) - 1) / kv_round(D)), (qr.count * a.group + kTileRows - 1) / kTileRows};
+}
+
+// Rounds of a part: with `slots` workgroups at once and half a part lost a tile.
+template <int D>
+__device__ __forceinline__ int tree_share(const AttnArgs& a, const TreeSeq& first, int lane)
+{
+    int total = __builtin_amdgcn_readlane(lane_sums(first.units * first.tiles), 63);
+    int items = __builtin_amdgcn_readlane(lane_sums(first.tiles), 63);
+    for (int b = 64; b < a.batch; b += 64) {
+        const TreeSeq s = tree_seq<D>(a, b + lane);
+        total += __builtin_amdgcn_readlane(lane_sums(s.units * s.tiles), 63);
+        items += __builtin_amdgcn_readlane(lane_sums(s.tiles), 63);
+    }
+    const int per_head = max(1, a.slots / a.kv.heads);
+    const int parts = max(per_head - items / 2, (per_head + 3) / 4);
+    return max((total + parts - 1) / parts, kMinRounds);
+}
+
+struct TreePlace {
+    int seq, tile, part, parts;                          // parts == 0: nothing here
+    int first;                                           // place of the sequence's first part
+    int tiles;
+};
+
+// Workgroup `place` of a head: the parts of sequence after sequence, tiles side by side in each.
+template <int D>
+__device__ __forceinline__ TreePlace tree_place(const AttnArgs& a, int place, int lane)
+{
+    if (a.slots == 0) {                                  // one workgroup a tile
+        const int tiles = (a.max_q * a.group + kTileRows - 1) / kTileRows;
+        return TreePlace{place / tiles, place % tiles, 0, 1, 0, tiles};
+    }
+    TreeSeq mine = tree_seq<D>(a, lane);
+    const int share = tree_share<D>(a, mine, lane);
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        if (b0) mine = tree_seq<D>(a, b0 + lane);
+        const int each = mine.tiles ? parts_of(mine.units, share) : 0, n = each * mine.tiles, upto = lane_sums(n);
+        const uint64_t past = __ballot(before + upto > place);
+        if (past) {
+            const int j = __ffsll((unsigned long long)past) - 1;
+            const int tiles = __builtin_amdgcn_readlane(mine.tiles, j), parts = __builtin_amdgcn_readlane(each, j);
+            const int first = before + __builtin_amdgcn_readlane(upto, j) - tiles * parts, at = place - first;
+            return TreePlace{b0 + j, at % tiles, at / tiles, parts, first, tiles};
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return TreePlace{0, 0, 0, 0, 0, 0};                  // more workgroups than parts
+}
+
+// Joins the parts of one row a wave.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_tree_join(AttnArgs a, float unshift)
+{
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row = (int)blockIdx.x * 4 + wave;          // of a sequence and head
+    const int head = (int)blockIdx.y, seq = (int)blockIdx.z;
+    const QueryRange qr = queries_of(a, seq);
+    if (row >= qr.count * a.group) return;
+    TreeSeq mine = tree_seq<D>(a, lane);
+    const int share = tree_share<D>(a, mine, lane);
+    int first = 0;                                       // parts of a head before this sequence's
+    for (int b0 = 0; b0 + 64 <= seq; b0 += 64) {
+        first += __builtin_amdgcn_readlane(lane_sums(mine.tiles ? parts_of(mine.units, share) * mine.tiles : 0), 63);
+        mine = tree_seq<D>(a, b0 + 64 + lane);
+    }
+    const int each = mine.tiles ? parts_of(mine.units, share) : 0, upto = lane_sums(each * mine.tiles);
+    const int parts = __builtin_amdgcn_readlane(each, seq & 63), tiles = __builtin_amdgcn_readlane(mine.tiles, seq & 63);
+    first += __builtin_amdgcn_readlane(upto, seq & 63) - parts * tiles;
+    if (parts <= 1) return;
+    const int tile = row / kTileRows, in_tile = row % kTileRows;
+    const auto part_row = [&](int p) {
+        return ((int64_t)(first + p * tiles + tile) * a.kv.heads + head) * kTileRows + in_tile;
+    };
+    join_parts<D>(a, parts, part_row, qr, row, head, unshift, lane);
+}
+
 template <int D, int BIAS, bool FINE, bool TREE>
 __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a)
 {
@@ -1179,14 +1284,22 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     lds_t* const flags = lds + 2 * T::kRound;
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int head = (int)blockIdx.x;
-    const int b = (int)blockIdx.z % a.batch, split = (int)blockIdx.z / a.batch;
+    int head, b, split, block, parts = 1;
+    if constexpr (TREE) {
+        head = (int)blockIdx.x % a.kv.heads;
+        const TreePlace p = tree_place<D>(a, (int)blockIdx.x / a.kv.heads, lane);
+        if (p.parts == 0) return;
+        b = p.seq, block = p.tile, split = p.part, parts = p.parts;
+    } else {
+        head = (int)blockIdx.x;
+        b = (int)blockIdx.z % a.batch, split = (int)blockIdx.z / a.batch;
+        // the last rows, which see the most keys, first
+        block = (int)(gridDim.y - 1 - blockIdx.y);
+    }
     const QueryRange qr = queries_of(a, b);
     const int kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
     const int count = qr.count * a.group;
-    if (count <= kFewRows && a.batch > 1) return;        // k_attn_few's
-    // the last rows, which see the most keys, first
-    const int block = (int)(gridDim.y - 1 - blockIdx.y);
+    if (!TREE && count <= kFewRows && a.batch > 1) return;   // k_attn_few's
     if (block * kTileRows >= count) return;
     const int row0 = block * kTileRows + wave * (16 * QT);
     Rows<D, BIAS, QT, TREE> rows;
@@ -1196,7 +1309,10 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     // keys of the workgroup's rows (this split's part) and of the wave's
     const KeyRange kf = first_range<TREE>(a, block * kTileRows / a.group, qr.count, kv);
     const KeyRange kl = last_range<TREE>(a, (min((block + 1) * kTileRows, count) - 1) / a.group, qr.count, kv);
-    const KeyRange seen{kf.lo, kl.hi}, mine = tile_part(kf, kl, T::kKeys, split, a.chunk);
+    const KeyRange seen{kf.lo, kl.hi};
+    KeyRange mine;
+    if constexpr (TREE) mine = tree_part(kf, kl, T::kKeys, split, parts);
+    else mine = tile_part(kf, kl, T::kKeys, split, a.chunk);
     const int begin = mine.lo, end = mine.hi;
     const int my_end = row0 < count ? min(rows.last.hi, end) : 0;
 
@@ -1257,7 +1373,10 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
         }
     }
     if (row0 >= count) return;
-    if (a.splits > 1) write_parts<D, BIAS, QT, TREE>(a, rows, sum, (int64_t)split * a.total_q * a.q_heads, true, lane);
+    if (TREE && parts > 1)
+        write_parts<D, BIAS, QT, TREE>(a, rows, sum, (int64_t)blockIdx.x * kTileRows + wave * (16 * QT), false, lane);
+    else if (!TREE && a.splits > 1)
+        write_parts<D, BIAS, QT, TREE>(a, rows, sum, (int64_t)split * a.total_q * a.q_heads, true, lane);
     else write_rows<D, BIAS, QT, FINE, TREE>(a, rows, sum, head, lane);
 }
 
@@ -1332,13 +1451,23 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
     const int64_t rows = (int64_t)a.max_q * a.group;
     if (rows <= 16) return launch_few<D, BIAS, 1, FINE, TREE>(a, s);
     if (rows <= kFewRows) return launch_few<D, BIAS, 2, FINE, TREE>(a, s);
-    if (a.groups) {                                      // a batch may hold sequences of few rows too
+    if (!TREE && a.groups) {                             // a batch may hold sequences of few rows too
         const hipError_t st = launch_few<D, BIAS, 2, FINE, TREE>(a, s);
         if (st != hipSuccess) return st;
     }
     static OncePerDevice once;
     const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_attn_tiles<D, BIAS, FINE, TREE>), T::kLds);
     if (st != hipSuccess) return st;
+    if constexpr (TREE) {
+        AttnArgs t = a;
+        t.part_o = a.few_o;
+        t.part_ml = a.few_ml;
+        hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), dim3((uint32_t)a.groups), dim3(64 * T::kWaves), T::kLds, s, t);
+        if (a.slots)
+            hipLaunchKernelGGL((k_attn_tree_join<D>), dim3((uint32_t)((rows + 3) / 4), (uint32_t)a.kv.heads, (uint32_t)a.batch),
+                               dim3(256), 0, s, t, Dec<BIAS>::kUnshift);
+        return hipGetLastError();
+    }
     const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
     hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
     if (a.splits > 1) {

@@ -774,8 +774,9 @@ int check_attn(const KvView& kv, const fp4q_attn* a)
 
 size_t attn_bytes(const AttnPlan& p) { return p.o + p.few_o + p.ml + p.few_ml; }
 
-AttnPlan plan_of(const KvView& kv, const fp4q_attn* a)
+AttnPlan plan_of(const KvView& kv, const fp4q_attn* a, bool tree)
 {
+    if (tree) return plan_attn_tree(kv, a->batch, a->q_heads, a->max_q, a->max_kv, a->table_cols, a->window);
     return plan_attn(kv, a->batch, a->total_q, a->q_heads, a->max_q, a->max_kv, a->table_cols, a->window);
 }
 
@@ -888,8 +889,15 @@ size_t fp4q_attn_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache
     Resolved r;
     KvView kv;
     if (resolve_cache(cfg, cache, r, kv) || check_attn(kv, attn)) return 0;
-    const AttnPlan p = plan_of(kv, attn);
-    return attn_bytes(p);
+    return attn_bytes(plan_of(kv, attn, false));
+}
+
+size_t fp4q_attn_tree_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn)
+{
+    Resolved r;
+    KvView kv;
+    if (resolve_cache(cfg, cache, r, kv) || check_attn(kv, attn)) return 0;
+    return attn_bytes(plan_of(kv, attn, true));
 }
 
 namespace {
@@ -915,7 +923,7 @@ int attn_call(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* 
         misaligned(attn->kv_lens, 4) || misaligned(attn->q_starts, 4) || misaligned(attn->sinks, 4) ||
         misaligned(attn->lse, 4) || (attn->total_q > 1 && attn->ld_q % 8))
         return FP4Q_ERR_ALIGN;
-    const AttnPlan p = plan_of(a.kv, attn);
+    const AttnPlan p = plan_of(a.kv, attn, is_tree);
     const size_t need = attn_bytes(p);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_ERR_WORKSPACE;
     if (need > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;

@@ -48,6 +48,39 @@ AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_h
     return p;
 }
 
+// Trees of more rows than a wave's (k_attn_tiles with TREE).
+static void plan_trees(AttnPlan& p, const KvView& kv, int64_t batch, int64_t rows, int64_t keys)
+{
+    // workgroups that the chip holds at once, by their LDS.  Keys are not cut where every sequence is
+    // short or the tiles alone fill the chip twice.
+    const int64_t slots = kv.dim == 256 ? 256 : 512, round = kv_round(kv.dim);
+    const int64_t tiles = batch * ((rows + kTileRows - 1) / kTileRows), units = keys / round + 2;
+    p.groups = (int32_t)(tiles * kv.heads);
+    if (keys <= round * kMinRounds || tiles * kv.heads >= 2 * slots) return;
+    if (tiles * units >= (int64_t)1 << 30) return;               // rounds are counted in 32 bits
+    // no share makes more parts than these: a part is a share, or the last of its tile
+    const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
+    const int64_t parts = std::min(per_head + tiles, tiles * (units / kMinRounds + 1));
+    p.slots = (int32_t)slots;
+    p.groups = (int32_t)(parts * kv.heads);
+    const size_t n = (size_t)p.groups * kTileRows;
+    p.few_ml = n * 2 * sizeof(float);
+    p.few_o = n * kv.dim * sizeof(float);
+}
+
+AttnPlan plan_attn_tree(const KvView& kv, int64_t batch, int64_t q_heads, int64_t max_q, int64_t max_kv,
+                        int64_t table_cols, int64_t window)
+{
+    AttnPlan p{1, 1 << 30, 0, 0, 0, 0, 0, 0};
+    const int64_t rows = max_q * (q_heads / kv.heads);
+    if (rows == 0 || batch == 0) return p;
+    const int64_t all = std::min(max_kv, table_cols * kv.page_size);
+    const int64_t keys = window ? std::min(all, window + max_q + kv_round(kv.dim)) : all;
+    if (rows <= kFewRows) plan_few(p, kv, batch, rows, keys);
+    else plan_trees(p, kv, batch, rows, keys);
+    return p;
+}
+
 hipError_t launch_attn(int bias, const AttnArgs& a, hipStream_t s)
 {
     if (bias == 0) return launch_bias<0, false>(a, s);

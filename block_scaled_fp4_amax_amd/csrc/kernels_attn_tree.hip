@@ -1,5 +1,5 @@
 // kernels_attn_tree.hip -- fp4_attn_tree: attn_kernels.h's kernels with a mask of the drafted keys.
-// Calls are planned as fp4_attn's are (plan_attn).
+// plan_attn_tree (kernels_attn.hip) plans these calls.
 #include "attn_kernels.h"
 
 namespace fp4q {

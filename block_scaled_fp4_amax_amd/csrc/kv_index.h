@@ -161,6 +161,16 @@ FP4Q_HD KeyRange tile_part(const KeyRange& first, const KeyRange& last, int32_t 
     return KeyRange{lo, last.hi < lo + chunk ? last.hi : lo + chunk};
 }
 
+// The same for part `part` of `parts` even ones, in whole rounds.
+FP4Q_HD KeyRange tree_part(const KeyRange& first, const KeyRange& last, int32_t round, int32_t part, int32_t parts)
+{
+    const int32_t lo = first.lo / round * round;
+    const int64_t units = (last.hi - lo + round - 1) / round;
+    const int32_t from = lo + (int32_t)(units * part / parts) * round;
+    const int64_t to = lo + units * (part + 1) / parts * round;
+    return KeyRange{from, to < last.hi ? (int32_t)to : last.hi};
+}
+
 struct TilePlan {
     int32_t splits, chunk;
 };

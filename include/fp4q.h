@@ -590,9 +590,10 @@ int fp4_attn(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* a
  * only its last keys, as many as make `window` with the c drafted keys that its row of the mask names
  * (c of 0 counts as 1, and all c are seen even where they are more).  Where n is more than
  * kv_lens[b], the first of the drafted tokens have no key.
- * causal has to be 1 (FP4Q_ERR_MODE), max_q * tree_cols < 2^31 (FP4Q_ERR_UNSUPPORTED).  Everything else as in
- * fp4_attn, the workspace's size too.
+ * causal has to be 1 (FP4Q_ERR_MODE), max_q * tree_cols < 2^31 (FP4Q_ERR_UNSUPPORTED), workspace:
+ * fp4q_attn_tree_workspace_bytes() bytes.  Everything else as in fp4_attn.
  */
+size_t fp4q_attn_tree_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn);
 int fp4_attn_tree(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, const uint8_t* tree,
                   int32_t tree_cols, void* workspace, size_t workspace_bytes, void* stream);
 

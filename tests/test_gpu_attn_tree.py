@@ -162,8 +162,8 @@ def test_masks_of_other_widths(cols):
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "amdfp4"])
 @pytest.mark.parametrize("n", [4, 50])
 def test_a_chain_is_a_causal_chunk(fmt, n):
-    """The same keys, in the same steps: equal bits."""
-    s = Setup(fmt, 128, 2, 4, 16, [300, 1000, n], [n, n, n]).device()
+    """The same keys, in the same steps (up to 256 keys of many rows are cut by neither call): equal bits."""
+    s = Setup(fmt, 128, 2, 4, 16, [300, 1000, n] if n == 4 else [256, 131, n], [n, n, n]).device()
     chain = np.tile(np.tril(np.ones((n, n), bool)), (3, 1))
     a, al = run(s, chain, max_q=n)
     b, bl = s.run(max_q=n)
