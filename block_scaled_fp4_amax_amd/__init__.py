@@ -3,7 +3,7 @@ block-scaled FP4 quantisation library.
 
 The functions carry the C-ABI names (fp4_quantize, fp4_dequantize, fp4_qdq,
 fp4_cast_transpose, fp4_cast_transpose_grouped, fp4_mm, fp4_linear,
-fp4_kv_append, fp4_kv_append_rope, fp4_kv_read, fp4_attn, fp4_attn_tree, fp4_add_rms_norm,
+fp4_kv_append, fp4_kv_append_rope, fp4_kv_read, fp4_attn, fp4_attn_tree, fp4_moe, fp4_add_rms_norm,
 fp4_add_rms_norm_backward and the fp4q_* helpers).  They
 only marshal arguments: torch supplies device memory and the current HIP
 stream, every step of the computation runs in the library's HIP kernels.  If
@@ -19,7 +19,7 @@ __all__ = [
     "fp4q_workspace_bytes", "fp4q_cast_transpose_workspace_bytes", "fp4_quantize", "fp4_dequantize", "fp4_qdq", "fp4_cast_transpose",
     "fp4_cast_transpose_grouped", "fp4_mx_project_fp8", "fp4_mm", "fp4_mx_scales_tiled",
     "fp4q_mx_scales_tiled_bytes", "fp4_qdq_noalloc", "ErrorFeedback", "fp4_linear", "fp4q_linear_workspace_bytes", "KVCache", "fp4_kv_append",
-    "fp4_kv_append_rope", "fp4_kv_read", "fp4_attn", "fp4_attn_tree", "fp4_attn_workspace", "fp4_add_rms_norm", "fp4_add_rms_norm_backward",
+    "fp4_kv_append_rope", "fp4_kv_read", "fp4_attn", "fp4_attn_tree", "fp4_attn_workspace", "fp4_moe", "fp4_moe_workspace", "fp4q_moe_workspace_bytes", "fp4_add_rms_norm", "fp4_add_rms_norm_backward",
     "fp4q_add_rms_norm_backward_workspace_bytes", "LIB_PATH",
 ]
 
@@ -74,6 +74,15 @@ class _KvRope(ct.Structure):
         (n, ct.c_void_p) for n in ("slots", "positions", "cos", "sin")] + [
         ("tokens", ct.c_int64), ("table_rows", ct.c_int64)] + [
         (n, ct.c_int32) for n in ("rot_dim", "q_heads", "interleaved", "reserved")]
+
+
+class _Moe(ct.Structure):
+    _fields_ = [("x", ct.c_void_p), ("ld_x", ct.c_int64)] + [
+        (n, ct.c_void_p) for n in ("logits", "w1_codes", "w1_scales", "w1_outer", "w2_codes", "w2_scales", "w2_outer", "b1", "b2",
+                                   "y")] + [
+        (n, ct.c_int64) for n in ("ld_y", "tokens", "experts", "hidden", "inter")] + [
+        (n, ct.c_int32) for n in ("top_k", "renormalize", "interleaved", "reserved")] + [
+        (n, ct.c_float) for n in ("alpha", "limit", "shift")]
 
 
 class _AddRmsNorm(ct.Structure):
@@ -165,6 +174,10 @@ def lib():
         L.fp4_kv_append.argtypes = [C, KV, P, I64, P, I64, P, I64, P]
         L.fp4_kv_append_rope.restype = ct.c_int
         L.fp4_kv_append_rope.argtypes = [C, KV, ct.POINTER(_KvRope), P]
+        L.fp4_moe.restype = ct.c_int
+        L.fp4_moe.argtypes = [C, ct.POINTER(_Moe), P, SZ, P]
+        L.fp4q_moe_workspace_bytes.restype = SZ
+        L.fp4q_moe_workspace_bytes.argtypes = [I64] * 5
         L.fp4_add_rms_norm.restype = ct.c_int
         L.fp4_add_rms_norm.argtypes = [ct.POINTER(_AddRmsNorm), P]
         L.fp4_add_rms_norm_backward.restype = ct.c_int
@@ -947,6 +960,100 @@ def fp4_attn_tree(q, cache, page_table, kv_lens, q_starts, tree, **kw):
         raise TypeError("fp4_attn_tree takes no causal")
     _ints32("fp4_attn_tree", tree.shape[1])
     return fp4_attn(q, cache, page_table, kv_lens, q_starts, _tree=tree, **kw)
+
+
+# ------------------------------------------------------------------ mixture of experts
+def fp4q_moe_workspace_bytes(tokens, experts, top_k, hidden, inter):
+    return lib().fp4q_moe_workspace_bytes(int(tokens), int(experts), int(top_k), int(hidden), int(inter))
+
+
+def fp4_moe_workspace(tokens, experts, top_k, hidden, inter, *, device="cuda"):
+    """Scratch for fp4_moe calls of this size, to keep between calls (one call at a time)."""
+    torch = _torch()
+    return torch.empty(fp4q_moe_workspace_bytes(tokens, experts, top_k, hidden, inter), dtype=torch.uint8, device=device)
+
+
+def _expert_weight(w, what, experts, rows, cols, cfg, device):
+    """Addresses of stacked experts' codes, scale bytes and outer scales."""
+    codes, scales, outer = w["codes"], w["scales"], w.get("outer")
+    if codes.element_size() != 1 or scales.element_size() != 1:
+        raise ValueError("%s codes and scales must hold bytes, got %s and %s" % (what, codes.dtype, scales.dtype))
+    if codes.numel() != experts * rows * cols // 2:
+        raise ValueError("%s codes must be [%d, %d, %d], got %s" % (what, experts, rows, cols // 2, list(codes.shape)))
+    _need(codes, experts * rows * cols // 2, what + " codes")
+    _need(scales, experts * rows * (cols // _inner(cfg)), what + " scales")
+    n = 0
+    if cfg.two_level == TWO_LEVEL["tensorwise"]:
+        n = experts
+    elif cfg.two_level == TWO_LEVEL["outer_block"] and cfg.outer_block_size > 0:
+        n = experts * rows * (cols // cfg.outer_block_size) // (cfg.outer_block_size if cfg.outer_2d else 1)
+    if n:
+        if outer is None:
+            raise ValueError("%s needs outer scales" % what)
+        if outer.dtype != _torch().float32:
+            raise ValueError("%s outer must be float32" % what)
+        _need(outer, 4 * n, what + " outer")
+    for t in (codes, scales, outer):
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s" % (what, device))
+    return codes.data_ptr(), scales.data_ptr(), None if outer is None else outer.data_ptr()
+
+
+def fp4_moe(x, logits, w1, w2, cfg, *, top_k, renormalize=True, b1=None, b2=None, interleaved=False, alpha=1.0, limit=None,
+            shift=0.0, out_dtype=None, y=None, workspace=None, stream=None):
+    """A mixture-of-experts layer with 4-bit experts for a few tokens (at most 128), from the
+    router's logits (see include/fp4q.h for ties, empty rows, rounding and limits).
+
+    x            bf16 [tokens, hidden], a view with a row pitch is accepted; logits float32 [tokens, experts].
+    w1, w2       {"codes", "scales", "outer"} of the stacked experts in cfg's format: gate and up rows [experts * 2 inter,
+                 hidden] and [experts * hidden, inter], in these shapes or any others of the same memory.
+                 Outer scales as in fp4_linear, but one for each expert where cfg is "tensorwise".
+    top_k        experts of a token, by the largest logits; renormalize: shares are the softmax of those,
+                 else of all logits.
+    b1, b2       float32 [experts, 2 inter] and [experts, hidden], or None.
+    interleaved  gate and up rows alternate; else each expert's gate rows come first.
+    alpha, limit, shift  g sigmoid(alpha g) (u + shift), with g at most limit and u within +-limit first.
+    Returns y [tokens, hidden], bf16 unless out_dtype (or a given y) is float32.  workspace: from
+    fp4_moe_workspace, else one is allocated."""
+    torch = _torch()
+    if x.dtype != torch.bfloat16:
+        raise Fp4Error(ERR_DTYPE, "x dtype %s" % x.dtype)
+    if x.dim() != 2 or logits.dim() != 2 or logits.shape[0] != x.shape[0]:
+        raise ValueError("x must be [tokens, hidden] and logits [tokens, experts]")
+    (T, H), E, dev = x.shape, logits.shape[1], x.device
+    if H > 1 and x.stride(1) != 1:
+        raise ValueError("x rows must be contiguous (stride(1) == 1)")
+    if logits.dtype != torch.float32 or not logits.is_contiguous():
+        raise ValueError("logits must be contiguous float32")
+    if not E or not H or (w2["codes"].numel() * 2) % (E * H):
+        raise ValueError("w2 codes do not hold %d experts of %d rows" % (E, H))
+    inter = w2["codes"].numel() * 2 // (E * H)
+    p1 = _expert_weight(w1, "w1", E, 2 * inter, H, cfg, dev)
+    p2 = _expert_weight(w2, "w2", E, H, inter, cfg, dev)
+    for n, t, shape in (("b1", b1, (E, 2 * inter)), ("b2", b2, (E, H))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous float32 %s" % (n, list(shape)))
+    if not x.is_cuda:
+        raise ValueError("fp4q takes device tensors; got one on %s" % dev)
+    _same_device(dev, logits=logits, b1=b1, b2=b2, y=y, workspace=workspace)
+    if y is None:
+        y = _new((T, H), out_dtype if out_dtype is not None else torch.bfloat16, dev, stream)
+    elif tuple(y.shape) != (T, H) or (H > 1 and y.stride(1) != 1):
+        raise ValueError("y must be a [%d, %d] view with contiguous rows" % (T, H))
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise Fp4Error(ERR_DTYPE, "y dtype %s" % y.dtype)
+    if workspace is None:
+        workspace = _new(lib().fp4q_moe_workspace_bytes(T, E, top_k, H, inter), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _ints32("fp4_moe", top_k)
+    a = _Moe(x.data_ptr(), x.stride(0) if T > 1 else H, logits.data_ptr(), *p1, *p2, None if b1 is None else b1.data_ptr(),
+             None if b2 is None else b2.data_ptr(), y.data_ptr(), y.stride(0) if T > 1 else H, T, E, H, inter, top_k,
+             1 if renormalize else 0, 1 if interleaved else 0, 0, alpha, 0.0 if limit is None else limit, shift)
+    ycfg = _with_dtypes(cfg, "bf16", _dtype_name(y))
+    _launch("fp4_moe", lib().fp4_moe, dev, ct.byref(ycfg), ct.byref(a), workspace.data_ptr(), workspace.nbytes,
+            _raw_stream(stream, dev))
+    return y
 
 
 # ------------------------------------------------------------------ residual and norm

@@ -371,6 +371,52 @@ struct NormGradPlan {
 NormGradPlan plan_rms_norm_backward(int64_t rows, int64_t hidden);
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s);
 
+// A mixture-of-experts layer: limits, a run of pairs of one expert, one of its weights
+// (all experts' rows one after another).
+constexpr int kMoeMaxTokens = 128, kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+
+struct MoeGroup {
+    int32_t expert, first, count, reserved;   // pairs first .. first + count - 1
+};
+
+struct MoeWeight {
+    const uint8_t *codes, *scales;
+    const float* outer;        // null; [experts]; per 64 x 64 values; per row and obs values
+    int32_t outer_kind, obs;
+};
+
+struct MoeArgs {
+    const uint16_t* x;         // bf16 [tokens, ld_x]
+    int64_t ld_x;
+    const float* logits;       // [tokens, experts]
+    MoeWeight w1, w2;          // [experts * 2 inter, hidden], [experts * hidden, inter]
+    const float *b1, *b2;      // [experts, 2 inter], [experts, hidden] or null
+    void* y;                   // bf16 or FP32 [tokens, ld_y]
+    int64_t ld_y;
+    int32_t tokens, experts, top_k, hidden, inter, renormalize, interleaved, y_f32;
+    float alpha, limit, shift;
+    // scratch
+    int32_t* counts;           // groups, pairs
+    MoeGroup* groups;          // [max_groups]
+    int32_t* expert;           // [tokens, top_k], -1: none
+    float* share;
+    int32_t* pair_token;       // [tokens * top_k] in the order of the experts
+    float* pair_share;
+    uint16_t *mid, *mid_rest;  // bf16 [tokens * top_k, inter]: the activations, and what they leave
+    float* parts;              // FP32 [splits][tokens][parts_ld], null with one split
+    int64_t parts_ld;
+    int32_t max_groups, splits;
+};
+
+struct MoePlan {
+    int32_t max_groups, splits;
+    int64_t parts_ld;
+    size_t counts, groups, expert, share, pair_token, pair_share, mid, mid_rest, parts, bytes;
+};
+
+MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);
+hipError_t launch_moe(int bias, const MoeArgs& a, hipStream_t s);
+
 // partial maxima used by the tensorwise amax pass
 constexpr int kAmaxPartials = 512;
 

@@ -597,6 +597,55 @@ size_t fp4q_attn_tree_workspace_bytes(const fp4q_cfg* cfg, const fp4q_kv_cache* 
 int fp4_attn_tree(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_attn* attn, const uint8_t* tree,
                   int32_t tree_cols, void* workspace, size_t workspace_bytes, void* stream);
 
+/* One call of fp4_moe (device pointers; the struct is read during the call). */
+typedef struct {
+    const uint16_t* x;         /* bf16 [tokens, hidden], row pitch ld_x (>= hidden, % 8 == 0; ignored
+                                  for one token), 16-byte aligned                               */
+    int64_t ld_x;
+    const float* logits;       /* FP32 [tokens, experts]                                        */
+    const uint8_t *w1_codes, *w1_scales;
+    const float* w1_outer;     /* W1 [experts * 2 inter, hidden]: every expert's gate and up rows   */
+    const uint8_t *w2_codes, *w2_scales;
+    const float* w2_outer;     /* W2 [experts * hidden, inter]                                  */
+    const float *b1, *b2;      /* FP32 [experts, 2 inter] (in the order of W1's rows) and [experts,
+                                  hidden], each or both NULL                                    */
+    void* y;                   /* bf16 or FP32 (cfg->output_dtype) [tokens, hidden], row pitch ld_y
+                                  (>= hidden), written                                          */
+    int64_t ld_y;
+    int64_t tokens, experts, hidden, inter;
+    int32_t top_k;
+    int32_t renormalize;       /* 1: shares are the softmax of the chosen logits, 0: of all         */
+    int32_t interleaved;       /* 1: gate row i and up row i are rows 2 i and 2 i + 1 of an expert;
+                                  0: rows i and inter + i                                        */
+    int32_t reserved;
+    float alpha, limit, shift; /* of the activation                                             */
+} fp4q_moe;
+
+/*
+ * fp4_moe -- a mixture-of-experts layer with 4-bit experts for a few tokens, from the
+ * router's logits.
+ *   y_t = sum_e a_te (W2_e act(W1_e x_t + b1_e) + b2_e)
+ * over the top_k experts with token t's largest logits (ties go to the lower expert; a logit of
+ * -infinity or NaN is never taken, so a token may have fewer, or none and zeros), with
+ * a_te = exp(logit_te) over the sum of exp of the chosen (or of all) logits, and
+ *   act(g, u) = g sigmoid(alpha g) (u + shift),
+ * g at most limit and u within +-limit first where limit is not 0 (alpha 1, limit 0, shift 0: SwiGLU).
+ * A logit of +infinity makes its token NaN.
+ *   W1, W2   rowwise buffers as fp4_quantize or fp4_cast_transpose_grouped write them for the stacked
+ *            rows, codes 16-byte aligned.  Outer scales: none, 2D of 64, 1D of a multiple of 64 (as in
+ *            fp4_linear), or TENSORWISE with one FP32 scale for each expert ([experts]).
+ * W enters the products exactly, sums are binary32.  a_te act is rounded to bf16 before W2 (a
+ * relative 2^-8); with FP32 y it enters as two such terms (2^-16).  How sums are shared among workgroups depends
+ * on the call's sizes and the tokens' choices alone: equal calls give equal bits.
+ * workspace: fp4q_moe_workspace_bytes() bytes, 16-byte aligned; no initial value, nothing kept.
+ * Needs hidden % 32 == 0 and inter % 32 == 0, 1 <= top_k <= experts (FP4Q_ERR_SHAPE); tokens <= 128, experts <= 512,
+ * top_k <= 32, hidden and inter <= 2^16 and fewer than 2^31 rows of W1 and W2 (FP4Q_ERR_UNSUPPORTED).
+ * cfg: input_dtype FP32 is FP4Q_ERR_UNSUPPORTED; rounding, outer_mode, seed, step, index_base and
+ * inner_2d are ignored.
+ */
+size_t fp4q_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);
+int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t workspace_bytes, void* stream);
+
 /* One call of fp4_add_rms_norm (device pointers; the struct is read during the call). */
 typedef struct {
     const void *x, *residual;  /* [rows, hidden], row pitches ld_x and ld_residual elements
