@@ -1001,7 +1001,7 @@ def _expert_weight(w, what, experts, rows, cols, cfg, device):
 
 def fp4_moe(x, logits, w1, w2, cfg, *, top_k, renormalize=True, b1=None, b2=None, interleaved=False, alpha=1.0, limit=None,
             shift=0.0, out_dtype=None, y=None, workspace=None, stream=None):
-    """A mixture-of-experts layer with 4-bit experts for a few tokens (at most 128), from the
+    """A mixture-of-experts layer with 4-bit experts for a few tokens (64 at a time, at most 1024), from the
     router's logits (see include/fp4q.h for ties, empty rows, rounding and limits).
 
     x            bf16 [tokens, hidden], a view with a row pitch is accepted; logits float32 [tokens, experts].

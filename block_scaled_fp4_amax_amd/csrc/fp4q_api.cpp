@@ -1146,7 +1146,7 @@ int check_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, in
 {
     if (tokens < 0 || experts < 1 || top_k < 1 || top_k > experts || hidden < 32 || inter < 32 || hidden % 32 || inter % 32)
         return FP4Q_ERR_SHAPE;
-    if (tokens > kMoeMaxTokens || experts > kMoeMaxExperts || top_k > kMoeMaxTopK || hidden > (1 << 16) || inter > (1 << 16))
+    if (tokens > 1024 || experts > kMoeMaxExperts || top_k > kMoeMaxTopK || hidden > (1 << 16) || inter > (1 << 16))
         return FP4Q_ERR_UNSUPPORTED;
     return FP4Q_OK;
 }
@@ -1156,7 +1156,10 @@ int check_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, in
 size_t fp4q_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter)
 {
     if (check_moe(tokens, experts, top_k, hidden, inter) || tokens == 0) return 0;
-    return plan_moe(tokens, experts, top_k, hidden, inter).bytes;
+    // launches of up to kMoeMaxTokens tokens, and of the rest of them
+    const int64_t rest = tokens % kMoeMaxTokens;
+    const size_t whole = tokens >= kMoeMaxTokens ? plan_moe(kMoeMaxTokens, experts, top_k, hidden, inter).bytes : 0;
+    return std::max(whole, rest ? plan_moe(rest, experts, top_k, hidden, inter).bytes : 0);
 }
 
 int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t workspace_bytes, void* stream)
@@ -1172,6 +1175,7 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
     if ((o.renormalize != 0 && o.renormalize != 1) || (o.interleaved != 0 && o.interleaved != 1)) return FP4Q_ERR_MODE;
     if (!(o.limit >= 0.0f) || o.alpha != o.alpha || o.shift != o.shift) return FP4Q_ERR_MODE;
     if (o.tokens > 1 && (o.ld_x < o.hidden || o.ld_y < o.hidden)) return FP4Q_ERR_SHAPE;
+    if (o.tokens > 1 && o.ld_x > ((int64_t)1 << 22)) return FP4Q_ERR_UNSUPPORTED;   // byte offsets below 2^31 within x
     if (r.obs && (o.hidden % r.obs || o.inter % r.obs)) return FP4Q_ERR_SHAPE;
     if ((r.outer_kind == kOuter2D && r.obs != 64) || (r.outer_kind == kOuter1D && r.obs % 64)) return FP4Q_ERR_UNSUPPORTED;
     if (o.tokens == 0) return FP4Q_OK;
@@ -1181,21 +1185,17 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
         misaligned(o.w1_outer, 4) || misaligned(o.w2_outer, 4) || misaligned(o.b1, 4) || misaligned(o.b2, 4) ||
         misaligned(o.y, r.y_f32 ? 4 : 2) || (o.tokens > 1 && o.ld_x % 8))
         return FP4Q_ERR_ALIGN;
-    const MoePlan p = plan_moe(o.tokens, o.experts, o.top_k, o.hidden, o.inter);
-    if (!workspace || workspace_bytes < p.bytes) return FP4Q_ERR_WORKSPACE;
+    const size_t need = fp4q_moe_workspace_bytes(o.tokens, o.experts, o.top_k, o.hidden, o.inter);
+    if (!workspace || workspace_bytes < need) return FP4Q_ERR_WORKSPACE;
     if (misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;
     MoeArgs a;
-    a.x = o.x;
-    a.ld_x = o.ld_x;
-    a.logits = o.logits;
+    a.ld_x = o.tokens > 1 ? o.ld_x : 0;
     const bool outer = r.outer_kind != kOuterNone;
     a.w1 = MoeWeight{o.w1_codes, o.w1_scales, outer ? o.w1_outer : nullptr, r.outer_kind, r.obs};
     a.w2 = MoeWeight{o.w2_codes, o.w2_scales, outer ? o.w2_outer : nullptr, r.outer_kind, r.obs};
     a.b1 = o.b1;
     a.b2 = o.b2;
-    a.y = o.y;
     a.ld_y = o.ld_y;
-    a.tokens = (int32_t)o.tokens;
     a.experts = (int32_t)o.experts;
     a.top_k = o.top_k;
     a.hidden = (int32_t)o.hidden;
@@ -1206,20 +1206,31 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
     a.alpha = o.alpha;
     a.limit = o.limit;
     a.shift = o.shift;
-    char* const ws = (char*)workspace;
-    a.counts = (int32_t*)(ws + p.counts);
-    a.groups = (MoeGroup*)(ws + p.groups);
-    a.expert = (int32_t*)(ws + p.expert);
-    a.share = (float*)(ws + p.share);
-    a.pair_token = (int32_t*)(ws + p.pair_token);
-    a.pair_share = (float*)(ws + p.pair_share);
-    a.mid = (uint16_t*)(ws + p.mid);
-    a.mid_rest = (uint16_t*)(ws + p.mid_rest);
-    a.parts = p.splits > 1 ? (float*)(ws + p.parts) : nullptr;
-    a.parts_ld = p.parts_ld;
-    a.max_groups = p.max_groups;
-    a.splits = p.splits;
-    return hip_status(launch_moe(r.bias, a, (hipStream_t)stream));
+    // so many tokens at a time, one after another in the same scratch
+    for (int64_t t = 0; t < o.tokens; t += kMoeMaxTokens) {
+        a.tokens = (int32_t)std::min<int64_t>(o.tokens - t, kMoeMaxTokens);
+        a.x = o.x + t * a.ld_x;
+        a.logits = o.logits + t * o.experts;
+        a.y = (char*)o.y + t * o.ld_y * (r.y_f32 ? 4 : 2);
+        const MoePlan p = plan_moe(a.tokens, o.experts, o.top_k, o.hidden, o.inter);
+        char* const ws = (char*)workspace;
+        a.counts = (int32_t*)(ws + p.counts);
+        a.groups = (MoeGroup*)(ws + p.groups);
+        a.expert = (int32_t*)(ws + p.expert);
+        a.share = (float*)(ws + p.share);
+        a.pair_token = (int32_t*)(ws + p.pair_token);
+        a.pair_share = (float*)(ws + p.pair_share);
+        a.mid = (uint16_t*)(ws + p.mid);
+        a.mid_rest = (uint16_t*)(ws + p.mid_rest);
+        a.parts = p.splits > 1 ? (float*)(ws + p.parts) : nullptr;
+        a.parts_ld = p.parts_ld;
+        a.group = p.group;
+        a.max_groups = p.max_groups;
+        a.splits = p.splits;
+        st = hip_status(launch_moe(r.bias, a, (hipStream_t)stream));
+        if (st) return st;
+    }
+    return FP4Q_OK;
 }
 
 }  // extern "C"

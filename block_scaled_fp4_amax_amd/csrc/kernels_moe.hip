@@ -6,18 +6,18 @@
 // Every expert that a token reached is read once, which is what bounds the layer: 4 bits
 // and a scale's share a weight, for few tokens each.  Three launches:
 //   k_moe_route  one workgroup: each token's experts and their shares, then the (token, expert)
-//                pairs in the order of the experts and their groups of up to kGroup
+//                pairs in the order of the experts and their groups of up to 16 MT
 //                pairs of one expert;
-//   k_moe_up     a workgroup takes 16 gate and 16 up rows of W1 for one group; its waves share K
+//   k_moe_up     a workgroup takes 32 gate and 32 up rows of W1 for one group; its waves share K
 //                and join through LDS; a times the activation goes to the scratch in bf16;
-//   k_moe_down   a workgroup takes 16 rows of W2 for all groups: its waves share the
-//                groups' K, each adding its sums to its own [tokens][16] of LDS, joined at the
-//                end in order.  Where 16 rows a workgroup leave compute units idle the groups are
+//   k_moe_down   a workgroup takes 32 rows of W2 for all groups: its waves share the
+//                groups' K, each adding its sums to its own [tokens][32] of LDS, joined at the
+//                end in order.  Where 32 rows a workgroup leave compute units idle the groups are
 //                split over workgroups too, whose sums k_moe_join adds in order.
 //
 // Products as in kernels_linear.hip: v_mfma_f32_16x16x32_bf16 with rows of W decoded to bf16,
-// exactly, as the A operand and tokens as the B operand; a step is two times 64 values of K, of
-// which lane l holds 16 (l / 16) .. + 15 of row l % 16.  Sums are binary32.
+// exactly, as the A operand and tokens as the B operand; a unit is 128 values of K, of which
+// lane l loads 32 (l / 16) .. + 31 of row l % 16.  Sums are binary32.
 //
 // Rounding.  a act is rounded to bf16 before W2, as an activation between two products is;
 // where the result is asked for in binary32 (FINE) it enters as two such terms, good to 2^-16.
@@ -32,8 +32,12 @@ namespace {
 
 enum { kInnerOnly = 0, kPerTile = 1, kPerRow = 2 };      // outer scales inside the sum: none (or one an expert), 2D, 1D
 
-constexpr int kGroup = 64;                               // pairs of a group, at most
-constexpr int kUpWaves = 4, kDownWaves = 16;
+constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpChunk = 4096, kDownChunk = 1024;        // values of K whose scale bytes LDS holds
+// Units of the weights on their way, as many as the registers hold.
+constexpr int kUpDepth = 2;
+template <int MT>
+constexpr int kDownDepth = MT == 4 ? 2 : 4;
 constexpr int kRouteThreads = 1024;
 
 // ---------------------------------------------------------------- routing
@@ -47,62 +51,55 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, m, 64);
-        v = v > o ? v : o;
-    }
-    return v;
-}
-
-constexpr int kMaxPerLane = kMoeMaxExperts / 64;
-
+// One workgroup.  PER: experts of a lane, expert j 64 + lane in place j.
+template <int PER>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
 {
-    __shared__ uint32_t member[kMoeMaxExperts][kMoeMaxTokens / 32];
-    __shared__ int first_pair[kMoeMaxExperts], first_group[kMoeMaxExperts];
+    __shared__ uint32_t member[PER * 64][kMoeMaxTokens / 32];
+    __shared__ int first_group[PER * 64];
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-    for (int i = (int)threadIdx.x; i < kMoeMaxExperts * (kMoeMaxTokens / 32); i += kRouteThreads) (&member[0][0])[i] = 0;
+    for (int i = (int)threadIdx.x; i < PER * 64 * (kMoeMaxTokens / 32); i += kRouteThreads) (&member[0][0])[i] = 0;
+    // places of the groups that no pair takes
+    for (int i = (int)threadIdx.x; i < a.max_groups * a.group; i += kRouteThreads) a.pair_token[i] = -1;
     __syncthreads();
     for (int t = wave; t < a.tokens; t += kRouteThreads / 64) {
-        float l[kMaxPerLane];
-        uint32_t key[kMaxPerLane];
+        float l[PER];
+        uint32_t key[PER];
 #pragma unroll
-        for (int j = 0; j < kMaxPerLane; ++j) {
+        for (int j = 0; j < PER; ++j) {
             const int e = j * 64 + lane;
             l[j] = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
             key[j] = order_key(l[j]);
         }
-        float top = 0.0f, sum = 0.0f, mine = 0.0f;       // lane s keeps slot s's logit
+        float top = 0.0f, sum = 0.0f, mine = 0.0f;       // lane s keeps slot s's logit and expert
         int chosen = -1;
         for (int s = 0; s < a.top_k; ++s) {
-            uint64_t best = 0;
+            uint32_t most = key[0];
 #pragma unroll
-            for (int j = 0; j < kMaxPerLane; ++j) {
-                const uint64_t c = (uint64_t)key[j] << 32 | (uint32_t)~(j * 64 + lane);
-                best = key[j] != 0 && c > best ? c : best;
-            }
-            best = wave_max_u64(best);
-            if (best == 0) break;                        // nothing left to take
-            const int e = (int)~(uint32_t)best;
+            for (int j = 1; j < PER; ++j) most = max(most, key[j]);
+            most = wave_max_u32(most);
+            if (most == 0) break;                        // nothing left to take
+            // the lowest expert that has it
+            int e = -1;
             float v = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kMaxPerLane; ++j)
-                if (j == e >> 6) {
-                    v = l[j];
-                    if ((e & 63) == lane) key[j] = 0;
-                }
-            v = __shfl(v, e & 63, 64);
+            for (int j = PER - 1; j >= 0; --j) {
+                const uint64_t has = __ballot(key[j] == most);
+                const int at = has ? __ffsll((unsigned long long)has) - 1 : 0;
+                e = has ? j * 64 + at : e;
+                v = has ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(l[j]), at)) : v;
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j) key[j] = j * 64 + lane == e ? 0u : key[j];
             if (s == 0) top = v;
             sum += expf(v - top);
-            if (lane == s) mine = v, chosen = e;
+            mine = lane == s ? v : mine;
+            chosen = lane == s ? e : chosen;
         }
         if (!a.renormalize) {                            // the softmax of all logits
             sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kMaxPerLane; ++j) sum += l[j] > -__builtin_inff() ? expf(l[j] - top) : 0.0f;
+            for (int j = 0; j < PER; ++j) sum += l[j] > -__builtin_inff() ? expf(l[j] - top) : 0.0f;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
         }
@@ -113,7 +110,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
         }
     }
     __syncthreads();
-    // pairs and groups before each expert's: wave 0, experts in runs of 64
+    // groups before each expert's: wave 0, experts in runs of 64
     const auto count_of = [&](int e) {
         int n = 0;
 #pragma unroll
@@ -121,116 +118,236 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
         return n;
     };
     if (wave == 0) {
-        int pairs = 0, groups = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 64) {
-            const int e = e0 + lane, n = e < a.experts ? count_of(e) : 0, g = (n + kGroup - 1) / kGroup;
-            int pn = n, gn = g;
+        int groups = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = j * 64 + lane, n = count_of(e), g = (n + a.group - 1) / a.group;
+            int before = g;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
-                const int p = __shfl_up(pn, m, 64), q = __shfl_up(gn, m, 64);
-                pn += lane >= m ? p : 0;
-                gn += lane >= m ? q : 0;
+                const int q = __shfl_up(before, m, 64);
+                before += lane >= m ? q : 0;
             }
-            if (e < a.experts) {
-                first_pair[e] = pairs + pn - n;
-                first_group[e] = groups + gn - g;
-            }
-            pairs += __shfl(pn, 63, 64);
-            groups += __shfl(gn, 63, 64);
+            const int first = groups + before - g;
+            first_group[e] = first;
+            for (int i = 0; i < g; ++i) a.groups[first + i] = MoeGroup{e, min(a.group, n - i * a.group)};
+            groups += __builtin_amdgcn_readlane(before, 63);
         }
-        if (lane == 0) a.counts[0] = groups, a.counts[1] = pairs;
+        for (int i = groups + lane; i < a.max_groups; i += 64) a.groups[i] = MoeGroup{0, 0};
+        if (lane == 0) a.counts[0] = groups;
     }
     __syncthreads();
-    for (int e = (int)threadIdx.x; e < a.experts; e += kRouteThreads) {
-        const int n = count_of(e);
-        for (int g = 0; g * kGroup < n; ++g)
-            a.groups[first_group[e] + g] = MoeGroup{e, first_pair[e] + g * kGroup, min(kGroup, n - g * kGroup), 0};
-    }
     for (int p = (int)threadIdx.x; p < a.tokens * a.top_k; p += kRouteThreads) {
         const int e = a.expert[p], t = p / a.top_k;      // written by this workgroup before the barriers
         if (e < 0) continue;
-        int at = first_pair[e];
-        for (int w = 0; w < t >> 5; ++w) at += __popc(member[e][w]);
-        at += __popc(member[e][t >> 5] & ((1u << (t & 31)) - 1));
+        int rank = __popc(member[e][t >> 5] & ((1u << (t & 31)) - 1));
+        for (int w = 0; w < t >> 5; ++w) rank += __popc(member[e][w]);
+        const int at = first_group[e] * a.group + rank;  // an expert's groups follow one another
         a.pair_token[at] = t;
         a.pair_share[at] = a.share[p];
     }
 }
 
 // ---------------------------------------------------------------- products
-// Sixteen rows of one expert's weight, the lane's row among them, and their outer scales.
-struct WRows {
-    const uint8_t *codes, *scales;                       // at the lane's place of the row's first step
-    const float* outer;                                  // 2D: the tile's first; 1D: of the first of the lane's four results
-    int64_t outer_row;                                   // 1D: from one result's row to the next
+// NT tiles of sixteen rows of one expert's weight, through buffer descriptors at their first
+// rows: a lane's offsets are the same for every unit (128 values of K), what moves is a scalar, and
+// lanes beyond K load zeros without a branch, so the compiler's waits count exactly and units
+// stay in flight while earlier ones are used.
+template <int BIAS, int OUTER, int NT>
+struct Weights {
+    static constexpr int B = Dec<BIAS>::kBlock;
+    rsrc_t codes[NT], row_outer[OUTER == kPerRow ? NT : 1];
+    const float* tile_outer[OUTER == kPerTile ? NT / 2 : 1];   // of two neighbouring tiles, which lie in one of 64 rows
+    uint32_t code_off, outer_off;                        // of the lane
+    int obs, last;
+
+    // One unit of a lane: 32 values of K of its row in each tile, and outer scales.
+    struct Unit {
+        uint4 c[NT];
+        float o[OUTER == kPerTile ? NT / 2 : OUTER == kPerRow ? NT : 1][2];
+    };
+
+    // Tile n: rows first[n] + stride 0 .. 15 of expert e's N (a multiple of 32).
+    __device__ __forceinline__ Weights(const MoeWeight& w, int e, const int (&first)[NT], int stride, int N, int K, int lane)
+    {
+        const int row = lane & 15, quarter = lane >> 4;
+        code_off = (uint32_t)(stride * row) * (uint32_t)(K / 2) + quarter * 16;
+        outer_off = 0;
+        obs = w.obs;
+        last = (K >> 6) - 1;
+        // of the lane's results, 4 quarter + 0 .. 3, each lane of a quad loads one
+        if constexpr (OUTER == kPerRow) outer_off = (uint32_t)(stride * (4 * quarter + (lane & 3))) * (uint32_t)(K / obs) * 4;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int64_t r = (int64_t)e * N + first[n];
+            codes[n] = make_rsrc(w.codes + r * (K / 2));
+            if constexpr (OUTER == kPerTile) tile_outer[n >> 1] = w.outer + (r >> 6) * (K >> 6);
+            if constexpr (OUTER == kPerRow) row_outer[n] = make_rsrc(w.outer + r * (K / obs));
+        }
+    }
+
+    // Values k .. k + 127 of K, zeros from `end` on (a multiple of 32).
+    __device__ __forceinline__ void load(int k, int end, int quarter, Unit& u) const
+    {
+        const bool in = k + 32 * quarter < end;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const u32x4_t c = __builtin_amdgcn_raw_buffer_load_b128(codes[n], in ? code_off : kOff, k / 2, 0);
+            u.c[n] = make_uint4(c[0], c[1], c[2], c[3]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if constexpr (OUTER == kPerTile)
+                    if (n % 2 == 0) u.o[n >> 1][b] = tile_outer[n >> 1][min((k >> 6) + b, last)];
+                if constexpr (OUTER == kPerRow)
+                    u.o[n][b] = buf_load_f32(row_outer[n], k + 64 * b < end ? outer_off + (k + 64 * b) / obs * 4 : kOff);
+            }
+        }
+    }
 };
 
-// A lane's part of a step: 128 values of K in halves.
-template <int OUTER>
-struct WStep {
-    uint2 c[2];
-    uint32_t s[2];
-    float o[OUTER == kInnerOnly ? 1 : 2][OUTER == kPerRow ? 4 : 1];
+// Inner scale bytes in LDS.  Loaded a unit at a time they cost the cache a line's access for
+// each row and two bytes, more than the codes do (48 tokens through 32 experts of 2880 x 2880, MXFP4: 97 us in k_moe_up,
+// as many accesses as cycles); so a row's bytes of a whole chunk of K are loaded side by side, a row
+// an instruction, and stay in LDS while the chunk is multiplied.
+template <int BIAS, int CHUNK>
+struct Scales {
+    static constexpr int B = Dec<BIAS>::kBlock;
+    static constexpr int kPiece = B == 32 ? 1 : 2;       // bytes of a load: rows have no better alignment
+    static constexpr int kPieces = CHUNK / B / kPiece;   // of a row
+    static constexpr int kStride = CHUNK / B + 4;        // of a row in LDS; rows lie in different banks
+    static_assert((kPieces & (kPieces - 1)) == 0, "rows in whole loads of a wave, or loads of whole rows");
+
+    // ROWS rows from descriptor r's place, `pitch` bytes apart, bytes at .. of a row, to LDS rows `to`; `bytes` of
+    // the chunk are there.
+    template <int ROWS>
+    static __device__ __forceinline__ void stage(rsrc_t r, uint32_t pitch, int at, int bytes, lds_t* to, int lane)
+    {
+        constexpr int kLoads = ROWS * kPieces / 64;
+        uint32_t v[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t row = (i * 64 + lane) / kPieces, o = (i * 64 + lane) % kPieces * kPiece;
+            const uint32_t from = o < (uint32_t)bytes ? row * pitch + o : kOff;
+            if constexpr (kPiece == 1) v[i] = __builtin_amdgcn_raw_buffer_load_b8(r, from, at, 0);
+            else v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, from, at, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            lds_t* const p = to + (i * 64 + lane) / kPieces * kStride + (i * 64 + lane) % kPieces * kPiece;
+            if constexpr (kPiece == 1) *p = (unsigned char)v[i];
+            else *(__attribute__((address_space(3))) uint16_t*)p = (uint16_t)v[i];
+        }
+    }
+
+    // Of the lane's row at `row`, unit u of the chunk: the scales of 64 b .. + 63 that the lane multiplies
+    // (place_of), for NVFP4 and AMD-FP4 one byte for each h.
+    static __device__ __forceinline__ uint32_t read(const lds_t* row, int u, int b, int quarter)
+    {
+        const lds_t* const p = row + u * (128 / B) + b * (64 / B) + (quarter & 1) * (32 / B);
+        if constexpr (kPiece == 1) return *p;
+        else return *(const __attribute__((address_space(3))) uint16_t*)p;
+    }
 };
 
-template <int BIAS, int OUTER>
-__device__ __forceinline__ void load_step(const WRows& w, int k0, int K, int obs, int quarter, WStep<OUTER>& v)
+// A lane's part of a unit of the tokens, for each tile of them: of its column's token the eight values of
+// each 64 that its place in the products takes (multiply).
+template <int MT>
+struct Tokens {
+    uint4 x[MT][2][2];
+
+    __device__ __forceinline__ void load(rsrc_t r, const uint32_t (&off)[MT], int k, int end, int place)
+    {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool in = k + 64 * b + 16 * h + place < end;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, in ? off[m] : kOff, (k + 64 * b + 16 * h) * 2, 0);
+                    x[m][b][h] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+    }
+};
+
+// A lane's place among 64 values of K: 16 h + 32 (quarter % 2) + 8 (quarter / 2), h = 0 and 1.
+__device__ __forceinline__ int place_of(int quarter) { return 32 * (quarter & 1) + 8 * (quarter >> 1); }
+
+// The two halves of a wave hold different 64 values of K (16-byte loads, whole 64-byte runs of a row),
+// and swap words so that a product's lanes hold the same 64, under one outer scale.
+template <int BIAS, int OUTER, int NT, int MT>
+__device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>::Unit& u, const uint32_t (&scale)[NT][2],
+                                         const Tokens<MT>& x, f32x4_t (&acc)[NT][MT])
 {
-    constexpr int B = Dec<BIAS>::kBlock;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int k = k0 + 64 * h;
-        const bool in = k + 16 * quarter < K;            // values beyond K are zeros
-        v.c[h] = in ? *(const uint2*)(w.codes + k / 2) : make_uint2(0, 0);
-        v.s[h] = in ? w.scales[k / B] : 0;
-        if constexpr (OUTER == kPerTile) v.o[h][0] = k < K ? w.outer[k >> 6] : 0.0f;
-        if constexpr (OUTER == kPerRow) {
+    for (int n = 0; n < NT; ++n) {
+        const auto a = __builtin_amdgcn_permlane32_swap(u.c[n].x, u.c[n].y, false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(u.c[n].z, u.c[n].w, false, false);
+        const uint32_t code[2][2] = {{a[0], b[0]}, {a[1], b[1]}};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v.o[h][r] = k < K ? w.outer[r * w.outer_row + k / obs] : 0.0f;
+        for (int d = 0; d < 2; ++d) {
+            float o[4];
+            if constexpr (OUTER == kPerTile) o[0] = o[1] = o[2] = o[3] = u.o[n >> 1][d];
+            if constexpr (OUTER == kPerRow) {            // from the quad's lanes
+                const int v = __float_as_int(u.o[n][d]);
+                o[0] = __int_as_float(__builtin_amdgcn_mov_dpp(v, 0x00, 0xF, 0xF, true));
+                o[1] = __int_as_float(__builtin_amdgcn_mov_dpp(v, 0x55, 0xF, 0xF, true));
+                o[2] = __int_as_float(__builtin_amdgcn_mov_dpp(v, 0xAA, 0xF, 0xF, true));
+                o[3] = __int_as_float(__builtin_amdgcn_mov_dpp(v, 0xFF, 0xF, 0xF, true));
+            }
+            uint4 w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t byte = Dec<BIAS>::kBlock == 32 ? scale[n][d] : __builtin_amdgcn_ubfe(scale[n][d], 8 * h, 8);
+                w[h] = DecBf16<BIAS>::octet(code[d][h], DecBf16<BIAS>::scale(byte));
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                f32x4_t p = OUTER == kInnerOnly ? acc[n][m] : f32x4_t{0, 0, 0, 0};
+                p = Dec<0>::mfma(w[0], x.x[m][d][0], p);
+                p = Dec<0>::mfma(w[1], x.x[m][d][1], p);
+                if constexpr (OUTER == kInnerOnly) {
+                    acc[n][m] = p;
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[n][m][r] = __builtin_fmaf(p[r], o[r], acc[n][m][r]);
+                }
+            }
         }
     }
 }
 
-template <int BIAS, int OUTER>
-__device__ __forceinline__ void decode_half(const WStep<OUTER>& v, int h, uint4& w0, uint4& w1)
+// Units k, k + stride, ... before end, DEPTH of the weights' and one of the tokens' on their way.  `ready` is
+// called when the first of them are; then scale rows are in LDS, those of tile n at rows + n * apart, from value k0 on.
+template <int DEPTH, int CHUNK, int BIAS, int OUTER, int NT, int MT, class Ready>
+__device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, rsrc_t x, const uint32_t (&off)[MT], int k, int end,
+                                       int stride, const lds_t* rows, int apart, int k0, int quarter, f32x4_t (&acc)[NT][MT],
+                                       Ready ready)
 {
-    const float sc = DecBf16<BIAS>::scale(v.s[h]);
-    w0 = DecBf16<BIAS>::octet(v.c[h].x, sc);
-    w1 = DecBf16<BIAS>::octet(v.c[h].y, sc);
-}
-
-template <int OUTER>
-__device__ __forceinline__ void multiply_half(const WStep<OUTER>& v, int h, uint4 w0, uint4 w1, uint4 x0, uint4 x1, f32x4_t& acc)
-{
-    f32x4_t p = OUTER == kInnerOnly ? acc : f32x4_t{0, 0, 0, 0};
-    p = Dec<0>::mfma(w0, x0, p);
-    p = Dec<0>::mfma(w1, x1, p);
-    if constexpr (OUTER == kInnerOnly) {
-        acc = p;
-    } else {
+    static_assert(DEPTH % 2 == 0, "the tokens' two places alternate");
+    using S = Scales<BIAS, CHUNK>;
+    const int place = place_of(quarter);
+    typename Weights<BIAS, OUTER, NT>::Unit u[DEPTH];
+    Tokens<MT> t[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(p[r], v.o[h][OUTER == kPerRow ? r : 0], acc[r]);
+    for (int j = 0; j < DEPTH; ++j) w.load(k + j * stride, end, quarter, u[j]);
+    t[0].load(x, off, k, end, place);
+    ready();
+    for (; k < end; k += DEPTH * stride) {
+#pragma unroll
+        for (int j = 0; j < DEPTH; ++j) {                // units beyond the end are zeros
+            const int at = min(k + j * stride, end - 1) - k0;
+            uint32_t scale[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) scale[n][b] = S::read(rows + n * apart, at >> 7, b, quarter);
+            t[(j + 1) & 1].load(x, off, k + (j + 1) * stride, end, place);
+            multiply<BIAS, OUTER, NT, MT>(u[j], scale, t[j & 1], acc);
+            w.load(k + (j + DEPTH) * stride, end, quarter, u[j]);
+        }
     }
-}
-
-// Rows first + stride 0 .. 15 of expert e's weight of N rows (N is a multiple of 32).
-template <int BIAS, int OUTER>
-__device__ __forceinline__ WRows rows_of(const MoeWeight& w, int e, int first, int stride, int N, int K, int lane)
-{
-    constexpr int B = Dec<BIAS>::kBlock;
-    const int row = lane & 15, quarter = lane >> 4;
-    const int64_t r = (int64_t)e * N + first + stride * row;
-    WRows v;
-    v.codes = w.codes + r * (K / 2) + quarter * 8;
-    v.scales = w.scales + r * (K / B) + (B == 16 ? quarter : quarter >> 1);
-    v.outer = nullptr;
-    v.outer_row = 0;
-    if constexpr (OUTER == kPerTile) v.outer = w.outer + (((int64_t)e * N + first) >> 6) * (K >> 6);
-    if constexpr (OUTER == kPerRow) {
-        v.outer = w.outer + ((int64_t)e * N + first + stride * 4 * quarter) * (K / w.obs);   // results 4 quarter + 0 .. 3
-        v.outer_row = (int64_t)stride * (K / w.obs);
-    }
-    return v;
 }
 
 __device__ __forceinline__ float gated(const MoeArgs& a, float g, float u)
@@ -245,80 +362,82 @@ __device__ __forceinline__ float gated(const MoeArgs& a, float g, float u)
 template <int BIAS, int OUTER, int MT, bool FINE>
 __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeArgs a)
 {
-    __shared__ float join[kUpWaves][2 * MT * 4][64];
-    if ((int)blockIdx.y >= a.counts[0]) return;
+    using S = Scales<BIAS, kUpChunk>;
+    constexpr int kJoin = kUpWaves * 16 * MT * 64 * 4, kScales = 64 * S::kStride;
+    __shared__ __align__(16) unsigned char smem[kJoin > kScales ? kJoin : kScales];
+    float(*const join)[16 * MT][64] = reinterpret_cast<float(*)[16 * MT][64]>(smem);
+    lds_t* const lds = (lds_t*)smem;
     const MoeGroup group = a.groups[blockIdx.y];
+    if (group.count == 0) return;
+    const int first_pair = (int)blockIdx.y * a.group;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int i0 = (int)blockIdx.x * 16, K = a.hidden, N = 2 * a.inter;
-    const int stride = a.interleaved ? 2 : 1;
-    const WRows wg = rows_of<BIAS, OUTER>(a.w1, group.expert, i0 * stride, stride, N, K, lane);
-    const WRows wu = rows_of<BIAS, OUTER>(a.w1, group.expert, a.interleaved ? 2 * i0 + 1 : a.inter + i0, stride, N, K, lane);
-    const uint16_t* x[MT];
+    const int i0 = (int)blockIdx.x * 32, K = a.hidden, N = 2 * a.inter;
+    // tiles: gate rows i0 .. + 15 and + 16 .. + 31, the same up rows
+    const int s = a.interleaved ? 2 : 1, up = a.interleaved ? 1 : a.inter;
+    const int first[4] = {s * i0, s * (i0 + 16), s * i0 + up, s * (i0 + 16) + up};
+    const Weights<BIAS, OUTER, 4> w(a.w1, group.expert, first, s, N, K, lane);
+    uint32_t off[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-        x[m] = 16 * m + col < group.count
-                   ? a.x + (int64_t)a.pair_token[group.first + 16 * m + col] * a.ld_x + quarter * 16 : nullptr;
-
-    f32x4_t acc[2][MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[0][m] = acc[1][m] = f32x4_t{0, 0, 0, 0};
-    int k = wave * 128;
-    WStep<OUTER> g, u;
-    load_step<BIAS, OUTER>(wg, k, K, a.w1.obs, quarter, g);
-    load_step<BIAS, OUTER>(wu, k, K, a.w1.obs, quarter, u);
-    for (; k < K; k += kUpWaves * 128) {
-        WStep<OUTER> gn, un;
-        load_step<BIAS, OUTER>(wg, k + kUpWaves * 128, K, a.w1.obs, quarter, gn);
-        load_step<BIAS, OUTER>(wu, k + kUpWaves * 128, K, a.w1.obs, quarter, un);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 g0, g1, u0, u1;
-            decode_half<BIAS, OUTER>(g, h, g0, g1);
-            decode_half<BIAS, OUTER>(u, h, u0, u1);
-            const int at = k + 64 * h;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (16 * m >= group.count) break;        // uniform
-                const bool in = x[m] != nullptr && at + 16 * quarter < K;
-                const uint4* p = (const uint4*)(x[m] + at);
-                const uint4 x0 = in ? p[0] : make_uint4(0, 0, 0, 0), x1 = in ? p[1] : make_uint4(0, 0, 0, 0);
-                multiply_half<OUTER>(g, h, g0, g1, x0, x1, acc[0][m]);
-                multiply_half<OUTER>(u, h, u0, u1, x0, x1, acc[1][m]);
-            }
-        }
-        g = gn;
-        u = un;
+    {
+        const int token = a.pair_token[first_pair + 16 * m + col];   // -1: none
+        off[m] = token >= 0 ? (uint32_t)token * (uint32_t)(a.ld_x * 2) + place_of(quarter) * 2 : kOff;
     }
+    f32x4_t acc[4][MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) join[wave][m * 8 + i][lane] = acc[i >> 2][m][i & 3];
+        for (int m = 0; m < MT; ++m) acc[n][m] = f32x4_t{0, 0, 0, 0};
+    // a wave stages the scale bytes of 64 / kUpWaves of the rows
+    constexpr int kRows = 64 / kUpWaves, kOf = 16 / kRows;   // waves of a tile
+    const int tile = wave / kOf, row0 = wave % kOf * kRows;
+    const int first_row = tile == 0 ? first[0] : tile == 1 ? first[1] : tile == 2 ? first[2] : first[3];
+    const rsrc_t sr = make_rsrc(a.w1.scales + ((int64_t)group.expert * N + first_row + s * row0) * (K / S::B));
+    for (int k0 = 0; k0 < K; k0 += kUpChunk) {
+        const int end = min(K, k0 + kUpChunk);
+        if (k0) __syncthreads();                         // everybody is done with the chunk before
+        S::template stage<kRows>(sr, s * (K / S::B), k0 / S::B, (end - k0) / S::B, lds + (16 * tile + row0) * S::kStride, lane);
+        stream<kUpDepth, kUpChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(a.x), off, k0 + wave * 128, end, kUpWaves * 128, lds + col * S::kStride,
+                                                       16 * S::kStride, k0, quarter, acc, [] { lds_barrier(); });
+    }
     __syncthreads();
-    // wave m finishes token tile m
-    if (wave >= MT || 16 * wave + col >= group.count) return;
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = join[0][wave * 8 + i][lane];
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int w = 1; w < kUpWaves; ++w) v[i] += join[w][wave * 8 + i][lane];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) join[wave][(n * MT + m) * 4 + r][lane] = acc[n][m][r];
+    __syncthreads();
+    const float whole = a.w1.outer_kind == kOuterTensor ? a.w1.outer[group.expert] : 1.0f;
+    // a wave finishes every fourth pair of 16 rows and 16 tokens
+    for (int p = wave; p < 2 * MT; p += kUpWaves) {
+        const int n = p & 1, m = p >> 1;
+        if (16 * m + col >= group.count) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = ((n + (i & 4 ? 2 : 0)) * MT + m) * 4 + (i & 3);
+            v[i] = join[0][at][lane];
+#pragma unroll
+            for (int w = 1; w < kUpWaves; ++w) v[i] += join[w][at][lane];
+        }
+        const int pair = first_pair + 16 * m + col, i = i0 + 16 * n + 4 * quarter;
+        const float share = a.pair_share[pair];
+        float y[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t b = (int64_t)group.expert * N + s * (i + r);
+            const float gate = v[r] * whole + (a.b1 ? a.b1[b] : 0.0f);
+            const float upper = v[4 + r] * whole + (a.b1 ? a.b1[b + up] : 0.0f);
+            y[r] = share * gated(a, gate, upper);
+        }
+        const uint2 hi = make_uint2(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]));
+        *(uint2*)(a.mid + (int64_t)pair * a.inter + i) = hi;
+        if constexpr (FINE)
+            *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
+                make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
     }
-    const int pair = group.first + 16 * wave + col, i = i0 + 4 * quarter;
-    const float whole = a.w1.outer_kind == kOuterTensor ? a.w1.outer[group.expert] : 1.0f, share = a.pair_share[pair];
-    float y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int64_t b = (int64_t)group.expert * N + (a.interleaved ? 2 * (i + r) : i + r);
-        const float gate = v[r] * whole + (a.b1 ? a.b1[b] : 0.0f);
-        const float up = v[4 + r] * whole + (a.b1 ? a.b1[b + (a.interleaved ? 1 : a.inter)] : 0.0f);
-        y[r] = share * gated(a, gate, up);
-    }
-    const uint2 hi = make_uint2(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]));
-    *(uint2*)(a.mid + (int64_t)pair * a.inter + i) = hi;
-    if constexpr (FINE)
-        *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
-            make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
 }
 
 // Four neighbouring values of y.
@@ -353,70 +472,62 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a)
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * 16, K = a.inter;
-    const int groups = a.counts[0], steps = (K + 127) / 128;
-    f32x4_t* const sums = (f32x4_t*)smem + wave * a.tokens * 4;   // [tokens][4 quarters of the 16 rows]
-    for (int i = lane; i < a.tokens * 4; i += 64) sums[i] = f32x4_t{0, 0, 0, 0};
+    const int n0 = (int)blockIdx.x * 32, K = a.inter;
+    using S = Scales<BIAS, kDownChunk>;
+    MoeGroup* const list = (MoeGroup*)(smem + kDownWaves * (a.tokens * 128 + 32 * S::kStride));
+    lds_t* const scales = (lds_t*)smem + kDownWaves * a.tokens * 128 + wave * (32 * S::kStride);
+    const int steps = (K + 127) / 128;
+    const int groups = a.counts[0];
+    for (int i = (int)threadIdx.x; i < a.max_groups; i += 64 * kDownWaves) list[i] = a.groups[i];
+    f32x4_t* const sums = (f32x4_t*)smem + wave * a.tokens * 8;   // [tokens][8 fours of the 32 rows]
+    for (int i = lane; i < a.tokens * 8; i += 64) sums[i] = f32x4_t{0, 0, 0, 0};
+    __syncthreads();
 
     const int parts = kDownWaves * (int)gridDim.y, part = (int)blockIdx.y * kDownWaves + wave;
     const int64_t total = (int64_t)groups * steps;
     const int from = (int)(total * part / parts), to = (int)(total * (part + 1) / parts);
     int at = from;
     while (at < to) {
-        // the part's steps of one group
-        const int gi = at / steps, s0 = at - gi * steps, s1 = min(steps, s0 + to - at);
+        // the part's units of one group, as many as their scales have places
+        const int gi = at / steps, s0 = at - gi * steps, s1 = min(min(steps, s0 + to - at), s0 + kDownChunk / 128);
         at += s1 - s0;
-        const MoeGroup group = a.groups[gi];
-        const WRows w = rows_of<BIAS, OUTER>(a.w2, group.expert, n0, 1, a.hidden, K, lane);
-        const uint16_t* x[MT];
+        const MoeGroup group{__builtin_amdgcn_readfirstlane(list[gi].expert), __builtin_amdgcn_readfirstlane(list[gi].count)};
+        const int first[2] = {n0, n0 + 16};
+        const Weights<BIAS, OUTER, 2> w(a.w2, group.expert, first, 1, a.hidden, K, lane);
+        uint32_t off[MT];
         int token[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int pair = group.first + 16 * m + col;
+            const int pair = gi * a.group + 16 * m + col;
             const bool live = 16 * m + col < group.count;
-            token[m] = live ? a.pair_token[pair] : -1;
-            x[m] = live ? a.mid + (int64_t)pair * K + quarter * 16 : nullptr;
+            token[m] = a.pair_token[pair];               // -1: none
+            off[m] = live ? (uint32_t)pair * (uint32_t)(K * 2) + place_of(quarter) * 2 : kOff;
         }
-        f32x4_t acc[MT];
+        f32x4_t acc[2][MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0, 0, 0, 0};
-        WStep<OUTER> v;
-        load_step<BIAS, OUTER>(w, s0 * 128, K, a.w2.obs, quarter, v);
-        for (int s = s0; s < s1; ++s) {
-            WStep<OUTER> vn;
-            load_step<BIAS, OUTER>(w, (s + 1 < s1 ? s + 1 : s) * 128, K, a.w2.obs, quarter, vn);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint4 w0, w1;
-                decode_half<BIAS, OUTER>(v, h, w0, w1);
-                const int k = s * 128 + 64 * h;
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (16 * m >= group.count) break;
-                    const bool in = x[m] != nullptr && k + 16 * quarter < K;
-                    const uint4* p = (const uint4*)(x[m] + k);
-                    uint4 x0 = in ? p[0] : make_uint4(0, 0, 0, 0), x1 = in ? p[1] : make_uint4(0, 0, 0, 0);
-                    multiply_half<OUTER>(v, h, w0, w1, x0, x1, acc[m]);
-                    if constexpr (FINE) {
-                        const uint4* q = (const uint4*)(a.mid_rest + (x[m] - a.mid) + k);
-                        x0 = in ? q[0] : make_uint4(0, 0, 0, 0), x1 = in ? q[1] : make_uint4(0, 0, 0, 0);
-                        multiply_half<OUTER>(v, h, w0, w1, x0, x1, acc[m]);
-                    }
-                }
-            }
-            v = vn;
-        }
+        for (int m = 0; m < MT; ++m) acc[0][m] = acc[1][m] = f32x4_t{0, 0, 0, 0};
+        const int k0 = s0 * 128, k1 = min(K, s1 * 128);
+        S::template stage<32>(make_rsrc(a.w2.scales + ((int64_t)group.expert * a.hidden + n0) * (K / S::B)), K / S::B, k0 / S::B,
+                              (k1 - k0) / S::B, scales, lane);
+        stream<kDownDepth<MT>, kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid), off, k0, k1, 128, scales + col * S::kStride,
+                                                               16 * S::kStride, k0, quarter, acc, [] {});
+        if constexpr (FINE)
+            stream<kDownDepth<MT>, kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid_rest), off, k0, k1, 128, scales + col * S::kStride,
+                                                                   16 * S::kStride, k0, quarter, acc, [] {});
         const float whole = a.w2.outer_kind == kOuterTensor ? a.w2.outer[group.expert] : 1.0f;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            if (token[m] >= 0) sums[token[m] * 4 + quarter] += acc[m] * whole;   // a token is once in a group
+            if (token[m] >= 0) {                         // a token is once in a group
+                sums[token[m] * 8 + quarter] += acc[0][m] * whole;
+                sums[token[m] * 8 + 4 + quarter] += acc[1][m] * whole;
+            }
     }
     __syncthreads();
-    for (int i = (int)threadIdx.x; i < a.tokens * 4; i += 64 * kDownWaves) {
+    for (int i = (int)threadIdx.x; i < a.tokens * 8; i += 64 * kDownWaves) {
         const f32x4_t* p = (const f32x4_t*)smem + i;
         f32x4_t v = p[0];
-        for (int w = 1; w < kDownWaves; ++w) v += p[w * a.tokens * 4];
-        const int t = i >> 2, n = n0 + 4 * (i & 3);
+        for (int w = 1; w < kDownWaves; ++w) v += p[w * a.tokens * 8];
+        const int t = i >> 3, n = n0 + 4 * (i & 7);
         if (a.parts) *(f32x4_t*)(a.parts + ((int64_t)blockIdx.y * a.tokens + t) * a.parts_ld + n) = v;
         else store_y4(a, t, n, add_bias(a, t, n, v));
     }
@@ -436,14 +547,14 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 template <int BIAS, int O1, int O2, int MT, bool FINE>
 hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 {
-    const int lds = kDownWaves * a.tokens * 64;
+    const int lds = kDownWaves * (a.tokens * 128 + 32 * Scales<BIAS, kDownChunk>::kStride) + a.max_groups * (int)sizeof(MoeGroup);
     static OncePerDevice once;
     const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_moe_down<BIAS, O2, MT, FINE>),
-                                    kDownWaves * kMoeMaxTokens * 64);
+                                    160 * 1024);
     if (st != hipSuccess) return st;
-    hipLaunchKernelGGL((k_moe_up<BIAS, O1, MT, FINE>), dim3((uint32_t)(a.inter / 16), (uint32_t)a.max_groups),
+    hipLaunchKernelGGL((k_moe_up<BIAS, O1, MT, FINE>), dim3((uint32_t)(a.inter / 32), (uint32_t)a.max_groups),
                        dim3(64 * kUpWaves), 0, s, a);
-    const int tiles = a.hidden / 16;
+    const int tiles = a.hidden / 32;
     hipLaunchKernelGGL((k_moe_down<BIAS, O2, MT, FINE>), dim3((uint32_t)tiles, (uint32_t)a.splits), dim3(64 * kDownWaves), lds, s, a);
     if (a.splits > 1)
         hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)((a.parts_ld / 4 * a.tokens + 255) / 256)), dim3(256), 0, s, a);
@@ -453,8 +564,8 @@ hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 template <int BIAS, int OUTER, bool FINE>
 hipError_t launch_tokens(const MoeArgs& a, hipStream_t s)
 {
-    if (a.tokens <= 16) return launch_products<BIAS, OUTER, OUTER, 1, FINE>(a, s);
-    if (a.tokens <= 32) return launch_products<BIAS, OUTER, OUTER, 2, FINE>(a, s);
+    if (a.group == 16) return launch_products<BIAS, OUTER, OUTER, 1, FINE>(a, s);
+    if (a.group == 32) return launch_products<BIAS, OUTER, OUTER, 2, FINE>(a, s);
     return launch_products<BIAS, OUTER, OUTER, 4, FINE>(a, s);
 }
 
@@ -482,14 +593,16 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
 {
     MoePlan p;
     const int64_t pairs = tokens * top_k;
-    // an expert's pairs are at most the tokens
-    const int64_t reached = experts < pairs ? experts : pairs, extra = pairs / kGroup;
-    p.max_groups = (int32_t)(reached + (tokens > kGroup ? extra : 0));
-    // Workgroups of k_moe_down: 16 rows of W2 each; few of them split the groups until they
-    // fill the chip once, while each wave keeps four steps.
-    const int64_t tiles = hidden / 16, steps = (inter + 127) / 128;
-    int64_t splits = 256 / tiles;
-    if (splits > p.max_groups * steps / (kDownWaves * 4)) splits = p.max_groups * steps / (kDownWaves * 4);
+    // Pairs of a group: an expert of more is read again for each further group (from the caches), one of
+    // fewer pays for tiles of tokens that it has not.  An expert's pairs are at most the tokens.
+    p.group = tokens <= 16 || pairs <= 8 * experts ? 16 : tokens <= 32 || pairs <= 20 * experts ? 32 : 64;
+    const int64_t reached = experts < pairs ? experts : pairs;
+    p.max_groups = (int32_t)(reached + (tokens > p.group ? pairs / p.group : 0));
+    // Workgroups of k_moe_down: 32 rows of W2 each; few of them split the groups until there are
+    // two a compute unit, while each wave keeps two units.
+    const int64_t tiles = hidden / 32, steps = (inter + 127) / 128;
+    int64_t splits = 512 / tiles;
+    if (splits > reached * steps / (kDownWaves * 2)) splits = reached * steps / (kDownWaves * 2);
     p.splits = (int32_t)(splits < 1 ? 1 : splits);
     p.parts_ld = hidden;
     size_t at = 0;
@@ -498,10 +611,11 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     p.groups = take(p.max_groups * sizeof(MoeGroup));
     p.expert = take(pairs * 4);
     p.share = take(pairs * 4);
-    p.pair_token = take(pairs * 4);
-    p.pair_share = take(pairs * 4);
-    p.mid = take(pairs * inter * 2);
-    p.mid_rest = take(pairs * inter * 2);
+    const int64_t places = (int64_t)p.max_groups * p.group;
+    p.pair_token = take(places * 4);
+    p.pair_share = take(places * 4);
+    p.mid = take(places * inter * 2);
+    p.mid_rest = take(places * inter * 2);
     p.parts = take(p.splits > 1 ? p.splits * tokens * p.parts_ld * 4 : 0);
     p.bytes = at;
     return p;
@@ -509,7 +623,9 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
 
 hipError_t launch_moe(int bias, const MoeArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_moe_route, dim3(1), dim3(kRouteThreads), 0, s, a);
+    if (a.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
     if (bias == 0) return launch_bias<0>(a, s);
     if (bias == 7) return launch_bias<7>(a, s);
     return launch_bias<15>(a, s);

@@ -371,12 +371,12 @@ struct NormGradPlan {
 NormGradPlan plan_rms_norm_backward(int64_t rows, int64_t hidden);
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s);
 
-// A mixture-of-experts layer: limits, a run of pairs of one expert, one of its weights
+// A mixture-of-experts layer: limits, a group of pairs of one expert, one of its weights
 // (all experts' rows one after another).
-constexpr int kMoeMaxTokens = 128, kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;   // tokens of a launch
 
 struct MoeGroup {
-    int32_t expert, first, count, reserved;   // pairs first .. first + count - 1
+    int32_t expert, count;     // pairs in the first `count` places of the group; 0: nothing here
 };
 
 struct MoeWeight {
@@ -396,20 +396,20 @@ struct MoeArgs {
     int32_t tokens, experts, top_k, hidden, inter, renormalize, interleaved, y_f32;
     float alpha, limit, shift;
     // scratch
-    int32_t* counts;           // groups, pairs
+    int32_t* counts;           // groups
     MoeGroup* groups;          // [max_groups]
     int32_t* expert;           // [tokens, top_k], -1: none
     float* share;
-    int32_t* pair_token;       // [tokens * top_k] in the order of the experts
+    int32_t* pair_token;       // [max_groups * group] by place, -1: none
     float* pair_share;
-    uint16_t *mid, *mid_rest;  // bf16 [tokens * top_k, inter]: the activations, and what they leave
+    uint16_t *mid, *mid_rest;  // bf16 [max_groups * group, inter]: the activations, and what they leave
     float* parts;              // FP32 [splits][tokens][parts_ld], null with one split
     int64_t parts_ld;
-    int32_t max_groups, splits;
+    int32_t group, max_groups, splits;   // pairs of a group at most, groups at most, splits of k_moe_down
 };
 
 struct MoePlan {
-    int32_t max_groups, splits;
+    int32_t group, max_groups, splits;
     int64_t parts_ld;
     size_t counts, groups, expert, share, pair_token, pair_share, mid, mid_rest, parts, bytes;
 };

@@ -213,6 +213,16 @@ def test_logits_that_exclude_experts_and_rows():
     assert y[7].isnan().all() and not y[:7].isnan().any()
 
 
+@pytest.mark.parametrize("T", [65, 129, 200, 1024])
+def test_more_tokens_than_a_launch_takes(T):
+    rng = np.random.default_rng(T)
+    layer = Layer("amdfp4", "none", 5, 64, 64, bias=True)
+    x, l = tokens(rng, T, 64), logits_of(rng, T, 5)
+    y = layer.check(x, l, 2)
+    for at in range(0, T, 64):
+        assert torch.equal(y[at:at + 64], layer.run(x[at:at + 64], l[at:at + 64], 2))
+
+
 def test_infinities_and_nan_stay_with_their_tokens():
     rng = np.random.default_rng(3)
     layer = Layer("mxfp4", "none", 4, 96, 64)

@@ -27,9 +27,9 @@ def moe(cfg=None, ws=FAKE, wsb=1 << 30, **kw):
     (dict(x=None), fq.ERR_NULL), (dict(logits=None), fq.ERR_NULL), (dict(w1_codes=None), fq.ERR_NULL), (dict(w2_scales=None), fq.ERR_NULL),
     (dict(y=None), fq.ERR_NULL), (dict(x=MIS), fq.ERR_ALIGN), (dict(w1_codes=MIS), fq.ERR_ALIGN), (dict(w2_codes=MIS), fq.ERR_ALIGN),
     (dict(logits=FAKE + 2), fq.ERR_ALIGN), (dict(y=FAKE + 1), fq.ERR_ALIGN), (dict(b1=FAKE + 2), fq.ERR_ALIGN), (dict(ld_x=132), fq.ERR_ALIGN),
-    (dict(ld_x=120), fq.ERR_SHAPE), (dict(ld_y=127), fq.ERR_SHAPE), (dict(hidden=48), fq.ERR_SHAPE), (dict(inter=16), fq.ERR_SHAPE),
+    (dict(ld_x=120), fq.ERR_SHAPE), (dict(ld_x=(1 << 22) + 8), fq.ERR_UNSUPPORTED), (dict(ld_y=127), fq.ERR_SHAPE), (dict(hidden=48), fq.ERR_SHAPE), (dict(inter=16), fq.ERR_SHAPE),
     (dict(hidden=0), fq.ERR_SHAPE), (dict(inter=-32), fq.ERR_SHAPE), (dict(experts=0), fq.ERR_SHAPE), (dict(top_k=0), fq.ERR_SHAPE),
-    (dict(top_k=9), fq.ERR_SHAPE), (dict(tokens=-1), fq.ERR_SHAPE), (dict(tokens=129), fq.ERR_UNSUPPORTED),
+    (dict(top_k=9), fq.ERR_SHAPE), (dict(tokens=-1), fq.ERR_SHAPE), (dict(tokens=1025), fq.ERR_UNSUPPORTED),
     (dict(experts=513), fq.ERR_UNSUPPORTED), (dict(experts=64, top_k=33), fq.ERR_UNSUPPORTED), (dict(hidden=65568, ld_x=65568, ld_y=65568), fq.ERR_UNSUPPORTED),
     (dict(inter=65568), fq.ERR_UNSUPPORTED), (dict(renormalize=2), fq.ERR_MODE), (dict(interleaved=-1), fq.ERR_MODE),
     (dict(limit=-1.0), fq.ERR_MODE), (dict(limit=float("nan")), fq.ERR_MODE), (dict(alpha=float("nan")), fq.ERR_MODE),
@@ -52,7 +52,7 @@ def test_configurations():
 
 def test_workspace_sizes():
     f = fq.fp4q_moe_workspace_bytes
-    assert f(0, 8, 2, 128, 64) == 0 and f(129, 8, 2, 128, 64) == 0 and f(4, 8, 9, 128, 64) == 0 and f(4, 8, 2, 100, 64) == 0
+    assert f(0, 8, 2, 128, 64) == 0 and f(1025, 8, 2, 128, 64) == 0 and f(4, 8, 9, 128, 64) == 0 and f(4, 8, 2, 100, 64) == 0
     assert f(4, 8, 2, 128, 64) >= 2 * 4 * 2 * 64 * 2
 
 
