@@ -1191,8 +1191,10 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
     MoeArgs a;
     a.ld_x = o.tokens > 1 ? o.ld_x : 0;
     const bool outer = r.outer_kind != kOuterNone;
-    a.w1 = MoeWeight{o.w1_codes, o.w1_scales, outer ? o.w1_outer : nullptr, r.outer_kind, r.obs};
-    a.w2 = MoeWeight{o.w2_codes, o.w2_scales, outer ? o.w2_outer : nullptr, r.outer_kind, r.obs};
+    a.w1 = MoeWeight{o.w1_codes, o.w1_scales, outer ? o.w1_outer : nullptr, r.outer_kind, r.obs,
+                     make_div(r.obs ? (uint32_t)(r.obs / 64) : 1)};
+    a.w2 = MoeWeight{o.w2_codes, o.w2_scales, outer ? o.w2_outer : nullptr, r.outer_kind, r.obs,
+                     make_div(r.obs ? (uint32_t)(r.obs / 64) : 1)};
     a.b1 = o.b1;
     a.b2 = o.b2;
     a.ld_y = o.ld_y;
@@ -1224,6 +1226,7 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
         a.mid_rest = (uint16_t*)(ws + p.mid_rest);
         a.parts = p.splits > 1 ? (float*)(ws + p.parts) : nullptr;
         a.parts_ld = p.parts_ld;
+        a.few = p.few;
         a.group = p.group;
         a.max_groups = p.max_groups;
         a.splits = p.splits;

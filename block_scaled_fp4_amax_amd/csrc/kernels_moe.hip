@@ -34,10 +34,6 @@ enum { kInnerOnly = 0, kPerTile = 1, kPerRow = 2 };      // outer scales inside 
 
 constexpr int kUpWaves = 4, kDownWaves = 8;
 constexpr int kUpChunk = 4096, kDownChunk = 1024;        // values of K whose scale bytes LDS holds
-// Units of the weights on their way, as many as the registers hold.
-constexpr int kUpDepth = 2;
-template <int MT>
-constexpr int kDownDepth = MT == 4 ? 2 : 4;
 constexpr int kRouteThreads = 1024;
 
 // ---------------------------------------------------------------- routing
@@ -51,7 +47,60 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup.  PER: experts of a lane, expert j 64 + lane in place j.
+struct Choice {
+    int expert;                                          // of slot `lane`, -1: none
+    float share;
+};
+
+// The experts of a token and their shares, slot s in lane s.  PER: experts of a lane, expert j 64 + lane in place j.
+template <int PER>
+__device__ __forceinline__ Choice choose(const MoeArgs& a, int t, int lane)
+{
+    float l[PER];
+    uint32_t key[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = j * 64 + lane;
+        l[j] = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
+        key[j] = order_key(l[j]);
+    }
+    float top = 0.0f, sum = 0.0f, mine = 0.0f;
+    int chosen = -1;
+#pragma unroll 1
+    for (int s = 0; s < a.top_k; ++s) {
+        uint32_t most = key[0];
+#pragma unroll
+        for (int j = 1; j < PER; ++j) most = max(most, key[j]);
+        most = wave_max_u32(most);
+        if (most == 0) break;                            // nothing left to take
+        // the lowest expert that has it
+        int e = -1;
+        float v = 0.0f;
+#pragma unroll
+        for (int j = PER - 1; j >= 0; --j) {
+            const uint64_t has = __ballot(key[j] == most);
+            const int at = has ? __ffsll((unsigned long long)has) - 1 : 0;
+            e = has ? j * 64 + at : e;
+            v = has ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(l[j]), at)) : v;
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) key[j] = j * 64 + lane == e ? 0u : key[j];
+        if (s == 0) top = v;
+        sum += expf(v - top);
+        mine = lane == s ? v : mine;
+        chosen = lane == s ? e : chosen;
+    }
+    if (!a.renormalize) {                                // the softmax of all logits
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sum += l[j] > -__builtin_inff() ? expf(l[j] - top) : 0.0f;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
+    }
+    return Choice{chosen, chosen >= 0 ? expf(mine - top) / sum : 0.0f};
+}
+
+// One workgroup.
 template <int PER>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
 {
@@ -63,50 +112,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
     for (int i = (int)threadIdx.x; i < a.max_groups * a.group; i += kRouteThreads) a.pair_token[i] = -1;
     __syncthreads();
     for (int t = wave; t < a.tokens; t += kRouteThreads / 64) {
-        float l[PER];
-        uint32_t key[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = j * 64 + lane;
-            l[j] = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
-            key[j] = order_key(l[j]);
-        }
-        float top = 0.0f, sum = 0.0f, mine = 0.0f;       // lane s keeps slot s's logit and expert
-        int chosen = -1;
-        for (int s = 0; s < a.top_k; ++s) {
-            uint32_t most = key[0];
-#pragma unroll
-            for (int j = 1; j < PER; ++j) most = max(most, key[j]);
-            most = wave_max_u32(most);
-            if (most == 0) break;                        // nothing left to take
-            // the lowest expert that has it
-            int e = -1;
-            float v = 0.0f;
-#pragma unroll
-            for (int j = PER - 1; j >= 0; --j) {
-                const uint64_t has = __ballot(key[j] == most);
-                const int at = has ? __ffsll((unsigned long long)has) - 1 : 0;
-                e = has ? j * 64 + at : e;
-                v = has ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(l[j]), at)) : v;
-            }
-#pragma unroll
-            for (int j = 0; j < PER; ++j) key[j] = j * 64 + lane == e ? 0u : key[j];
-            if (s == 0) top = v;
-            sum += expf(v - top);
-            mine = lane == s ? v : mine;
-            chosen = lane == s ? e : chosen;
-        }
-        if (!a.renormalize) {                            // the softmax of all logits
-            sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) sum += l[j] > -__builtin_inff() ? expf(l[j] - top) : 0.0f;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
-        }
+        const Choice c = choose<PER>(a, t, lane);
         if (lane < a.top_k) {
-            a.expert[t * a.top_k + lane] = chosen;
-            a.share[t * a.top_k + lane] = chosen >= 0 ? expf(mine - top) / sum : 0.0f;
-            if (chosen >= 0) atomicOr(&member[chosen][t >> 5], 1u << (t & 31));
+            a.expert[t * a.top_k + lane] = c.expert;
+            a.share[t * a.top_k + lane] = c.share;
+            if (c.expert >= 0) atomicOr(&member[c.expert][t >> 5], 1u << (t & 31));
         }
     }
     __syncthreads();
@@ -318,35 +328,36 @@ __device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>
     }
 }
 
-// Units k, k + stride, ... before end, DEPTH of the weights' and one of the tokens' on their way.  `ready` is
-// called when the first of them are; then scale rows are in LDS, those of tile n at rows + n * apart, from value k0 on.
-template <int DEPTH, int CHUNK, int BIAS, int OUTER, int NT, int MT, class Ready>
+// Units k, k + stride, ... before end, the next one on its way while one is used.  `ready` is called when the first of
+// them is; then scale rows are in LDS, those of tile n at rows + n * apart, from value k0 on.  The loop stays rolled: a
+// kernel of ten thousand bytes of code takes longer to fetch than a token's weights (k_moe_down of one
+// token, unrolled four times 16.6 us, rolled 9.9).
+template <int CHUNK, int BIAS, int OUTER, int NT, int MT, class Ready>
 __device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, rsrc_t x, const uint32_t (&off)[MT], int k, int end,
                                        int stride, const lds_t* rows, int apart, int k0, int quarter, f32x4_t (&acc)[NT][MT],
                                        Ready ready)
 {
-    static_assert(DEPTH % 2 == 0, "the tokens' two places alternate");
     using S = Scales<BIAS, CHUNK>;
     const int place = place_of(quarter);
-    typename Weights<BIAS, OUTER, NT>::Unit u[DEPTH];
-    Tokens<MT> t[2];
-#pragma unroll
-    for (int j = 0; j < DEPTH; ++j) w.load(k + j * stride, end, quarter, u[j]);
-    t[0].load(x, off, k, end, place);
+    typename Weights<BIAS, OUTER, NT>::Unit u;
+    Tokens<MT> t;
+    w.load(k, end, quarter, u);
+    t.load(x, off, k, end, place);
     ready();
-    for (; k < end; k += DEPTH * stride) {
+#pragma unroll 1
+    for (; k < end; k += stride) {
+        typename Weights<BIAS, OUTER, NT>::Unit next;
+        Tokens<MT> then;
+        w.load(k + stride, end, quarter, next);          // zeros beyond the end
+        then.load(x, off, k + stride, end, place);
+        uint32_t scale[NT][2];
 #pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {                // units beyond the end are zeros
-            const int at = min(k + j * stride, end - 1) - k0;
-            uint32_t scale[NT][2];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) scale[n][b] = S::read(rows + n * apart, at >> 7, b, quarter);
-            t[(j + 1) & 1].load(x, off, k + (j + 1) * stride, end, place);
-            multiply<BIAS, OUTER, NT, MT>(u[j], scale, t[j & 1], acc);
-            w.load(k + (j + DEPTH) * stride, end, quarter, u[j]);
-        }
+            for (int b = 0; b < 2; ++b) scale[n][b] = S::read(rows + n * apart, (k - k0) >> 7, b, quarter);
+        multiply<BIAS, OUTER, NT, MT>(u, scale, t, acc);
+        u = next;
+        t = then;
     }
 }
 
@@ -398,7 +409,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeArgs a)
         const int end = min(K, k0 + kUpChunk);
         if (k0) __syncthreads();                         // everybody is done with the chunk before
         S::template stage<kRows>(sr, s * (K / S::B), k0 / S::B, (end - k0) / S::B, lds + (16 * tile + row0) * S::kStride, lane);
-        stream<kUpDepth, kUpChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(a.x), off, k0 + wave * 128, end, kUpWaves * 128, lds + col * S::kStride,
+        stream<kUpChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(a.x), off, k0 + wave * 128, end, kUpWaves * 128, lds + col * S::kStride,
                                                        16 * S::kStride, k0, quarter, acc, [] { lds_barrier(); });
     }
     __syncthreads();
@@ -509,10 +520,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a)
         const int k0 = s0 * 128, k1 = min(K, s1 * 128);
         S::template stage<32>(make_rsrc(a.w2.scales + ((int64_t)group.expert * a.hidden + n0) * (K / S::B)), K / S::B, k0 / S::B,
                               (k1 - k0) / S::B, scales, lane);
-        stream<kDownDepth<MT>, kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid), off, k0, k1, 128, scales + col * S::kStride,
+        stream<kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid), off, k0, k1, 128, scales + col * S::kStride,
                                                                16 * S::kStride, k0, quarter, acc, [] {});
         if constexpr (FINE)
-            stream<kDownDepth<MT>, kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid_rest), off, k0, k1, 128, scales + col * S::kStride,
+            stream<kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid_rest), off, k0, k1, 128, scales + col * S::kStride,
                                                                    16 * S::kStride, k0, quarter, acc, [] {});
         const float whole = a.w2.outer_kind == kOuterTensor ? a.w2.outer[group.expert] : 1.0f;
 #pragma unroll
@@ -544,6 +555,190 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
     store_y4(a, t, n, add_bias(a, t, n, v));
 }
 
+// ---------------------------------------------------------------- a few tokens
+// A wave takes rows of W as they lie, 16 values a lane and 1024 a pass, and multiplies them with its token's
+// values in binary32: G[m] x is exact, each block of 16 is summed and its scales (inner times outer) multiply the
+// sum.  No product is wasted on tokens that are not there, a row is read in whole lines, and waves need neither
+// LDS nor a launch to join.  Each wave finds its token's experts itself.
+constexpr int kFewUpRows = 4, kFewDownRows = 2;          // of a wave: gate and up pairs, rows of W2
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    const auto add = [&v](auto moved) { v += __int_as_float(moved(__float_as_int(v))); };
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor1, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor2, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppHalfMirror, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppMirror, 0xF, 0xF, false); });
+    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)), b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)), d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+    return (a + b) + (c + d);
+}
+
+// One pass of a lane over R rows: codes, scale bytes, outer scales; and the token's values.  Each RUN of
+// the rows lies in one tile of 64.
+template <int BIAS, int OUTER, int R, int RUN>
+struct Pass {
+    static constexpr int B = Dec<BIAS>::kBlock;
+    uint2 c[R];
+    uint32_t s[R];
+    float o[OUTER == kPerTile ? R / RUN : OUTER == kPerRow ? R : 1];
+    uint4 x[2];
+
+    // rows: the rows' numbers in W; x: the token's values; k: the lane's first value, from `K` on zeros
+    __device__ __forceinline__ void load(const MoeWeight& w, const int64_t (&rows)[R], const uint16_t* token, int k, int K)
+    {
+        const bool in = k < K;
+        x[0] = in ? ((const uint4*)(token + k))[0] : make_uint4(0, 0, 0, 0);
+        x[1] = in ? ((const uint4*)(token + k))[1] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            c[r] = in ? *(const uint2*)(w.codes + rows[r] * (K / 2) + k / 2) : make_uint2(0, 0);
+            s[r] = in ? w.scales[rows[r] * (K / B) + k / B] : 0;
+            if constexpr (OUTER == kPerTile)
+                if (r % RUN == 0) o[r / RUN] = in ? w.outer[(rows[r] >> 6) * (K >> 6) + (k >> 6)] : 0.0f;
+            if constexpr (OUTER == kPerRow) o[r] = in ? w.outer[rows[r] * (K / w.obs) + div_by((uint32_t)k >> 6, w.per_outer)] : 0.0f;
+        }
+    }
+
+    __device__ __forceinline__ void add(float whole, float (&acc)[R]) const
+    {
+        float v[16];
+        const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float sum = 0.0f;
+            const auto eight = [&](uint32_t code, const float* p) {
+                const auto two = [&](auto g, const float* q) { sum = __builtin_fmaf(g[1], q[1], __builtin_fmaf(g[0], q[0], sum)); };
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0), p);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 1), p + 2);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2), p + 4);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3), p + 6);
+            };
+            eight(c[r].x, v);
+            eight(c[r].y, v + 8);
+            // MXFP4's byte 0 is 2^-127, 0xFF NaN
+            float d = BIAS != 0 ? DecBf16<BIAS>::scale(s[r])
+                                : s[r] == 0 ? 0x1p-127f : s[r] == 0xFFu ? __builtin_nanf("") : __uint_as_float(s[r] << 23);
+            d *= OUTER == kInnerOnly ? whole : o[OUTER == kPerTile ? r / RUN : r];
+            acc[r] = __builtin_fmaf(sum, d, acc[r]);
+        }
+    }
+};
+
+template <int BIAS, int OUTER, int PER, bool FINE>
+__global__ __launch_bounds__(256) void k_moe_few_up(MoeArgs a)
+{
+    constexpr int R = 2 * kFewUpRows;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int pair = (int)blockIdx.y, t = pair / a.top_k, slot = pair - t * a.top_k;
+    const int i0 = ((int)blockIdx.x * 4 + wave) * kFewUpRows, K = a.hidden, N = 2 * a.inter;
+    if (i0 >= a.inter) return;
+    const Choice mine = choose<PER>(a, t, lane);
+    const int e = __builtin_amdgcn_readlane(mine.expert, slot);
+    if (e < 0) return;
+    int64_t rows[R];
+    const int s = a.interleaved ? 2 : 1, up = a.interleaved ? 1 : a.inter;
+#pragma unroll
+    for (int r = 0; r < kFewUpRows; ++r) {
+        rows[r] = (int64_t)e * N + s * (i0 + r);         // the intermediate size is a multiple of four
+        rows[kFewUpRows + r] = rows[r] + up;
+    }
+    const float whole = a.w1.outer_kind == kOuterTensor ? a.w1.outer[e] : 1.0f;
+    const uint16_t* const x = a.x + (int64_t)t * a.ld_x;
+    float acc[R] = {};
+    Pass<BIAS, OUTER, R, kFewUpRows> p;
+    p.load(a.w1, rows, x, lane * 16, K);
+    // results r and r + kFewUpRows are finished by lane r
+    const int i = i0 + (lane & (kFewUpRows - 1));
+    const float* const b1 = a.b1 ? a.b1 + (int64_t)e * N + s * i : nullptr;
+    const float bg = b1 ? b1[0] : 0.0f, bu = b1 ? b1[up] : 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < K; k += 1024) {
+        Pass<BIAS, OUTER, R, kFewUpRows> next;
+        next.load(a.w1, rows, x, k + 1024 + lane * 16, K);
+        p.add(whole, acc);
+        p = next;
+    }
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kFewUpRows; ++r) {
+        const float gr = wave_sum(acc[r]), ur = wave_sum(acc[kFewUpRows + r]);
+        g = lane == r ? gr : g;
+        u = lane == r ? ur : u;
+    }
+    if (lane >= kFewUpRows) return;
+    const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.share), slot)) * gated(a, g + bg, u + bu);
+    const uint32_t hi = Dec<0>::round2(y, 0.0f);
+    a.mid[(int64_t)pair * a.inter + i] = (uint16_t)hi;
+    if constexpr (FINE) a.mid_rest[(int64_t)pair * a.inter + i] = (uint16_t)Dec<0>::rest2(y, 0.0f, hi);
+}
+
+template <int BIAS, int OUTER, int PER, bool FINE>
+__global__ __launch_bounds__(256) void k_moe_few_down(MoeArgs a)
+{
+    constexpr int R = kFewDownRows;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int t = (int)blockIdx.y, n0 = ((int)blockIdx.x * 4 + wave) * R, K = a.inter;
+    if (n0 >= a.hidden) return;
+    const Choice mine = choose<PER>(a, t, lane);
+    const int taken = __popcll(__ballot(mine.expert >= 0));   // slots 0 .. taken - 1
+    const int n = n0 + (lane & (R - 1));
+    float acc[R] = {}, offset = 0.0f;
+    Pass<BIAS, OUTER, R, R> p;
+    int64_t rows[R];
+    const uint16_t* x = nullptr;
+    const auto at = [&](int step, int passes) {          // the expert and the token's values of a step
+        const int s = step / passes, e = __builtin_amdgcn_readlane(mine.expert, s);
+#pragma unroll
+        for (int r = 0; r < R; ++r) rows[r] = (int64_t)e * a.hidden + n0 + r;
+        x = a.mid + (int64_t)(t * a.top_k + s) * K;
+        return a.w2.outer_kind == kOuterTensor ? a.w2.outer[e] : 1.0f;
+    };
+    const int passes = (K + 1023) / 1024, steps = taken * passes;
+    if (steps > 0) {
+        float whole = at(0, passes);
+        p.load(a.w2, rows, x, lane * 16, K);
+#pragma unroll 1
+        for (int step = 0; step < steps; ++step) {
+            const int after = step + 1 < steps ? step + 1 : step;
+            Pass<BIAS, OUTER, R, R> next;
+            if constexpr (FINE) {
+                // the second terms of the step's activations
+                Pass<BIAS, OUTER, R, R> rest = p;
+                const int s = step / passes, k = (step - s * passes) * 1024 + lane * 16;
+                const uint16_t* const xr = a.mid_rest + (int64_t)(t * a.top_k + s) * K;
+                rest.x[0] = k < K ? ((const uint4*)(xr + k))[0] : make_uint4(0, 0, 0, 0);
+                rest.x[1] = k < K ? ((const uint4*)(xr + k))[1] : make_uint4(0, 0, 0, 0);
+                rest.add(whole, acc);
+            }
+            const float next_whole = at(after, passes);
+            next.load(a.w2, rows, x, (after - after / passes * passes) * 1024 + lane * 16, K);
+            p.add(whole, acc);
+            p = next;
+            whole = next_whole;
+        }
+    }
+    float y = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float v = wave_sum(acc[r]);
+        y = lane == r ? v : y;
+    }
+    if (a.b2)                                            // in the order of the token's choices
+        for (int s = 0; s < taken; ++s) {
+            const int e = __builtin_amdgcn_readlane(mine.expert, s);
+            offset = __builtin_fmaf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.share), s)),
+                                    a.b2[(int64_t)e * a.hidden + n], offset);
+        }
+    if (lane >= R) return;
+    y += offset;
+    const int64_t out = (int64_t)t * a.ld_y + n;
+    if (a.y_f32) ((float*)a.y)[out] = y;
+    else ((uint16_t*)a.y)[out] = (uint16_t)Dec<0>::round2(y, 0.0f);
+}
+
 template <int BIAS, int O1, int O2, int MT, bool FINE>
 hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 {
@@ -561,9 +756,24 @@ hipError_t launch_products(const MoeArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int BIAS, int OUTER, int PER, bool FINE>
+hipError_t launch_few(const MoeArgs& a, hipStream_t s)
+{
+    const auto blocks = [](int rows, int of_wave) { return (uint32_t)((rows + 4 * of_wave - 1) / (4 * of_wave)); };
+    hipLaunchKernelGGL((k_moe_few_up<BIAS, OUTER, PER, FINE>), dim3(blocks(a.inter, kFewUpRows), (uint32_t)(a.tokens * a.top_k)),
+                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_moe_few_down<BIAS, OUTER, PER, FINE>), dim3(blocks(a.hidden, kFewDownRows), (uint32_t)a.tokens), dim3(256), 0,
+                       s, a);
+    return hipGetLastError();
+}
+
 template <int BIAS, int OUTER, bool FINE>
 hipError_t launch_tokens(const MoeArgs& a, hipStream_t s)
 {
+    if (a.few) return a.experts <= 64 ? launch_few<BIAS, OUTER, 1, FINE>(a, s) : launch_few<BIAS, OUTER, 8, FINE>(a, s);
+    if (a.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
     if (a.group == 16) return launch_products<BIAS, OUTER, OUTER, 1, FINE>(a, s);
     if (a.group == 32) return launch_products<BIAS, OUTER, OUTER, 2, FINE>(a, s);
     return launch_products<BIAS, OUTER, OUTER, 4, FINE>(a, s);
@@ -595,6 +805,7 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     const int64_t pairs = tokens * top_k;
     // Pairs of a group: an expert of more is read again for each further group (from the caches), one of
     // fewer pays for tiles of tokens that it has not.  An expert's pairs are at most the tokens.
+    p.few = pairs <= kMoeFewPairs ? 1 : 0;
     p.group = tokens <= 16 || pairs <= 8 * experts ? 16 : tokens <= 32 || pairs <= 20 * experts ? 32 : 64;
     const int64_t reached = experts < pairs ? experts : pairs;
     p.max_groups = (int32_t)(reached + (tokens > p.group ? pairs / p.group : 0));
@@ -623,9 +834,6 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
 
 hipError_t launch_moe(int bias, const MoeArgs& a, hipStream_t s)
 {
-    if (a.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), dim3(1), dim3(kRouteThreads), 0, s, a);
-    else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
     if (bias == 0) return launch_bias<0>(a, s);
     if (bias == 7) return launch_bias<7>(a, s);
     return launch_bias<15>(a, s);

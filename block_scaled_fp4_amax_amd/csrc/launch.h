@@ -375,6 +375,8 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s);
 // (all experts' rows one after another).
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;   // tokens of a launch
 
+constexpr int kMoeFewPairs = 16;   // of a token and an expert, that whole waves take row by row
+
 struct MoeGroup {
     int32_t expert, count;     // pairs in the first `count` places of the group; 0: nothing here
 };
@@ -383,6 +385,7 @@ struct MoeWeight {
     const uint8_t *codes, *scales;
     const float* outer;        // null; [experts]; per 64 x 64 values; per row and obs values
     int32_t outer_kind, obs;
+    DivBy per_outer;           // 64s of a 1D outer block
 };
 
 struct MoeArgs {
@@ -405,11 +408,12 @@ struct MoeArgs {
     uint16_t *mid, *mid_rest;  // bf16 [max_groups * group, inter]: the activations, and what they leave
     float* parts;              // FP32 [splits][tokens][parts_ld], null with one split
     int64_t parts_ld;
+    int32_t few;               // 1: k_moe_few_up and k_moe_few_down
     int32_t group, max_groups, splits;   // pairs of a group at most, groups at most, splits of k_moe_down
 };
 
 struct MoePlan {
-    int32_t group, max_groups, splits;
+    int32_t few, group, max_groups, splits;
     int64_t parts_ld;
     size_t counts, groups, expert, share, pair_token, pair_share, mid, mid_rest, parts, bytes;
 };
