@@ -47,6 +47,19 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The sum over a wave's lanes, in all of them.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    const auto add = [&v](auto moved) { v += __int_as_float(moved(__float_as_int(v))); };
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor1, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor2, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppHalfMirror, 0xF, 0xF, false); });
+    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppMirror, 0xF, 0xF, false); });
+    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)), b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)), d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+    return (a + b) + (c + d);
+}
+
 struct Choice {
     int expert;                                          // of slot `lane`, -1: none
     float share;
@@ -64,7 +77,7 @@ __device__ __forceinline__ Choice choose(const MoeArgs& a, int t, int lane)
         l[j] = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
         key[j] = order_key(l[j]);
     }
-    float top = 0.0f, sum = 0.0f, mine = 0.0f;
+    float top = 0.0f, mine = 0.0f;
     int chosen = -1;
 #pragma unroll 1
     for (int s = 0; s < a.top_k; ++s) {
@@ -86,18 +99,18 @@ __device__ __forceinline__ Choice choose(const MoeArgs& a, int t, int lane)
 #pragma unroll
         for (int j = 0; j < PER; ++j) key[j] = j * 64 + lane == e ? 0u : key[j];
         if (s == 0) top = v;
-        sum += expf(v - top);
         mine = lane == s ? v : mine;
         chosen = lane == s ? e : chosen;
     }
+    const float weight = chosen >= 0 ? expf(mine - top) : 0.0f;
+    float sum = weight;
     if (!a.renormalize) {                                // the softmax of all logits
         sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) sum += l[j] > -__builtin_inff() ? expf(l[j] - top) : 0.0f;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
     }
-    return Choice{chosen, chosen >= 0 ? expf(mine - top) / sum : 0.0f};
+    sum = wave_sum(sum);
+    return Choice{chosen, chosen >= 0 ? weight / sum : 0.0f};
 }
 
 // One workgroup.
@@ -560,19 +573,8 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 // values in binary32: G[m] x is exact, each block of 16 is summed and its scales (inner times outer) multiply the
 // sum.  No product is wasted on tokens that are not there, a row is read in whole lines, and waves need neither
 // LDS nor a launch to join.  Each wave finds its token's experts itself.
-constexpr int kFewUpRows = 4, kFewDownRows = 2;          // of a wave: gate and up pairs, rows of W2
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    const auto add = [&v](auto moved) { v += __int_as_float(moved(__float_as_int(v))); };
-    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor1, 0xF, 0xF, false); });
-    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppXor2, 0xF, 0xF, false); });
-    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppHalfMirror, 0xF, 0xF, false); });
-    add([](int x) { return __builtin_amdgcn_update_dpp(0, x, kDppMirror, 0xF, 0xF, false); });
-    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)), b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
-    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)), d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
-    return (a + b) + (c + d);
-}
+constexpr int kFewUpRows = 4, kFewDownRows = 8;          // of a wave: gate and up rows each, rows of W2
+constexpr int kFewWaves = 4;
 
 // One pass of a lane over R rows: codes, scale bytes, outer scales; and the token's values.  Each RUN of
 // the rows lies in one tile of 64.
@@ -627,13 +629,30 @@ struct Pass {
     }
 };
 
+// Steps 0 .. steps - 1 (`load` fetches one), two on their way while one is added.
+template <class P, class Load, class Add>
+__device__ __forceinline__ void passes(int steps, Load load, Add add)
+{
+    P p, next, then;
+    load(0, p);
+    load(1, next);
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+        load(i + 2, then);
+        add(i, p);
+        p = next;
+        next = then;
+    }
+}
+
 template <int BIAS, int OUTER, int PER, bool FINE>
-__global__ __launch_bounds__(256) void k_moe_few_up(MoeArgs a)
+__global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_up(MoeArgs a)
 {
     constexpr int R = 2 * kFewUpRows;
+    using P = Pass<BIAS, OUTER, R, kFewUpRows>;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int pair = (int)blockIdx.y, t = pair / a.top_k, slot = pair - t * a.top_k;
-    const int i0 = ((int)blockIdx.x * 4 + wave) * kFewUpRows, K = a.hidden, N = 2 * a.inter;
+    const int i0 = ((int)blockIdx.x * kFewWaves + wave) * kFewUpRows, K = a.hidden, N = 2 * a.inter;
     if (i0 >= a.inter) return;
     const Choice mine = choose<PER>(a, t, lane);
     const int e = __builtin_amdgcn_readlane(mine.expert, slot);
@@ -647,20 +666,13 @@ __global__ __launch_bounds__(256) void k_moe_few_up(MoeArgs a)
     }
     const float whole = a.w1.outer_kind == kOuterTensor ? a.w1.outer[e] : 1.0f;
     const uint16_t* const x = a.x + (int64_t)t * a.ld_x;
-    float acc[R] = {};
-    Pass<BIAS, OUTER, R, kFewUpRows> p;
-    p.load(a.w1, rows, x, lane * 16, K);
     // results r and r + kFewUpRows are finished by lane r
     const int i = i0 + (lane & (kFewUpRows - 1));
     const float* const b1 = a.b1 ? a.b1 + (int64_t)e * N + s * i : nullptr;
     const float bg = b1 ? b1[0] : 0.0f, bu = b1 ? b1[up] : 0.0f;
-#pragma unroll 1
-    for (int k = 0; k < K; k += 1024) {
-        Pass<BIAS, OUTER, R, kFewUpRows> next;
-        next.load(a.w1, rows, x, k + 1024 + lane * 16, K);
-        p.add(whole, acc);
-        p = next;
-    }
+    float acc[R] = {};
+    passes<P>((K + 1023) / 1024, [&](int j, P& p) { p.load(a.w1, rows, x, j * 1024 + lane * 16, K); },
+              [&](int, const P& p) { p.add(whole, acc); });
     float g = 0.0f, u = 0.0f;
 #pragma unroll
     for (int r = 0; r < kFewUpRows; ++r) {
@@ -675,50 +687,49 @@ __global__ __launch_bounds__(256) void k_moe_few_up(MoeArgs a)
     if constexpr (FINE) a.mid_rest[(int64_t)pair * a.inter + i] = (uint16_t)Dec<0>::rest2(y, 0.0f, hi);
 }
 
+// The waves of a workgroup take the passes of all of its token's experts over the same rows in turn, and join through
+// LDS in order.
 template <int BIAS, int OUTER, int PER, bool FINE>
-__global__ __launch_bounds__(256) void k_moe_few_down(MoeArgs a)
+__global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
 {
     constexpr int R = kFewDownRows;
+    using P = Pass<BIAS, OUTER, R, R>;
+    __shared__ float join[kFewWaves][R];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = (int)blockIdx.y, n0 = ((int)blockIdx.x * 4 + wave) * R, K = a.inter;
-    if (n0 >= a.hidden) return;
+    const int t = (int)blockIdx.y, n0 = (int)blockIdx.x * R, K = a.inter;
     const Choice mine = choose<PER>(a, t, lane);
     const int taken = __popcll(__ballot(mine.expert >= 0));   // slots 0 .. taken - 1
-    const int n = n0 + (lane & (R - 1));
-    float acc[R] = {}, offset = 0.0f;
-    Pass<BIAS, OUTER, R, R> p;
-    int64_t rows[R];
-    const uint16_t* x = nullptr;
-    const auto at = [&](int step, int passes) {          // the expert and the token's values of a step
-        const int s = step / passes, e = __builtin_amdgcn_readlane(mine.expert, s);
-#pragma unroll
-        for (int r = 0; r < R; ++r) rows[r] = (int64_t)e * a.hidden + n0 + r;
-        x = a.mid + (int64_t)(t * a.top_k + s) * K;
-        return a.w2.outer_kind == kOuterTensor ? a.w2.outer[e] : 1.0f;
-    };
-    const int passes = (K + 1023) / 1024, steps = taken * passes;
+    const int of_slot = (K + 1023) / 1024, all = taken * of_slot;
+    const int steps = wave < all ? (all - wave + kFewWaves - 1) / kFewWaves : 0;
+    float acc[R] = {};
     if (steps > 0) {
-        float whole = at(0, passes);
-        p.load(a.w2, rows, x, lane * 16, K);
-#pragma unroll 1
-        for (int step = 0; step < steps; ++step) {
-            const int after = step + 1 < steps ? step + 1 : step;
-            Pass<BIAS, OUTER, R, R> next;
-            if constexpr (FINE) {
-                // the second terms of the step's activations
-                Pass<BIAS, OUTER, R, R> rest = p;
-                const int s = step / passes, k = (step - s * passes) * 1024 + lane * 16;
-                const uint16_t* const xr = a.mid_rest + (int64_t)(t * a.top_k + s) * K;
-                rest.x[0] = k < K ? ((const uint4*)(xr + k))[0] : make_uint4(0, 0, 0, 0);
-                rest.x[1] = k < K ? ((const uint4*)(xr + k))[1] : make_uint4(0, 0, 0, 0);
+        // the slot and the first value of the wave's step j (K, where nothing is loaded, for a step beyond the last)
+        const auto place = [&](int j, int& s, int& k) {
+            const int at = wave + kFewWaves * min(j, steps - 1);
+            s = at / of_slot;
+            k = j < steps ? (at - s * of_slot) * 1024 + lane * 16 : K;
+        };
+        passes<P>(steps, [&](int j, P& p) {
+            int s, k;
+            place(j, s, k);
+            const int64_t first = (int64_t)__builtin_amdgcn_readlane(mine.expert, s) * a.hidden + n0;
+            int64_t rows[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[r] = first + r;
+            p.load(a.w2, rows, a.mid + (int64_t)(t * a.top_k + s) * K, k, K);
+        }, [&](int j, const P& p) {
+            int s, k;
+            place(j, s, k);
+            const float whole = a.w2.outer_kind == kOuterTensor ? a.w2.outer[__builtin_amdgcn_readlane(mine.expert, s)] : 1.0f;
+            p.add(whole, acc);
+            if constexpr (FINE) {                        // the activations' second terms
+                P rest = p;
+                const uint4* const x = (const uint4*)(a.mid_rest + (int64_t)(t * a.top_k + s) * K + k);
+                rest.x[0] = k < K ? x[0] : make_uint4(0, 0, 0, 0);
+                rest.x[1] = k < K ? x[1] : make_uint4(0, 0, 0, 0);
                 rest.add(whole, acc);
             }
-            const float next_whole = at(after, passes);
-            next.load(a.w2, rows, x, (after - after / passes * passes) * 1024 + lane * 16, K);
-            p.add(whole, acc);
-            p = next;
-            whole = next_whole;
-        }
+        });
     }
     float y = 0.0f;
 #pragma unroll
@@ -726,14 +737,17 @@ __global__ __launch_bounds__(256) void k_moe_few_down(MoeArgs a)
         const float v = wave_sum(acc[r]);
         y = lane == r ? v : y;
     }
+    if (lane < R) join[wave][lane] = y;
+    __syncthreads();
+    if (wave != 0 || lane >= R) return;
+    const int n = n0 + lane;
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) y += join[w][lane];
     if (a.b2)                                            // in the order of the token's choices
         for (int s = 0; s < taken; ++s) {
             const int e = __builtin_amdgcn_readlane(mine.expert, s);
-            offset = __builtin_fmaf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.share), s)),
-                                    a.b2[(int64_t)e * a.hidden + n], offset);
+            y = __builtin_fmaf(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.share), s)), a.b2[(int64_t)e * a.hidden + n], y);
         }
-    if (lane >= R) return;
-    y += offset;
     const int64_t out = (int64_t)t * a.ld_y + n;
     if (a.y_f32) ((float*)a.y)[out] = y;
     else ((uint16_t*)a.y)[out] = (uint16_t)Dec<0>::round2(y, 0.0f);
@@ -759,11 +773,11 @@ hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 template <int BIAS, int OUTER, int PER, bool FINE>
 hipError_t launch_few(const MoeArgs& a, hipStream_t s)
 {
-    const auto blocks = [](int rows, int of_wave) { return (uint32_t)((rows + 4 * of_wave - 1) / (4 * of_wave)); };
-    hipLaunchKernelGGL((k_moe_few_up<BIAS, OUTER, PER, FINE>), dim3(blocks(a.inter, kFewUpRows), (uint32_t)(a.tokens * a.top_k)),
-                       dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_moe_few_down<BIAS, OUTER, PER, FINE>), dim3(blocks(a.hidden, kFewDownRows), (uint32_t)a.tokens), dim3(256), 0,
-                       s, a);
+    const int i = kFewWaves * kFewUpRows;
+    hipLaunchKernelGGL((k_moe_few_up<BIAS, OUTER, PER, FINE>), dim3((uint32_t)((a.inter + i - 1) / i), (uint32_t)(a.tokens * a.top_k)),
+                       dim3(64 * kFewWaves), 0, s, a);
+    hipLaunchKernelGGL((k_moe_few_down<BIAS, OUTER, PER, FINE>), dim3((uint32_t)(a.hidden / kFewDownRows), (uint32_t)a.tokens),
+                       dim3(64 * kFewWaves), 0, s, a);
     return hipGetLastError();
 }
 
