@@ -1183,7 +1183,8 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
     if (r.outer_kind != kOuterNone && (!o.w1_outer || !o.w2_outer)) return FP4Q_ERR_NULL;
     if (misaligned(o.x, 16) || misaligned(o.logits, 4) || misaligned(o.w1_codes, 16) || misaligned(o.w2_codes, 16) ||
         misaligned(o.w1_outer, 4) || misaligned(o.w2_outer, 4) || misaligned(o.b1, 4) || misaligned(o.b2, 4) ||
-        misaligned(o.y, r.y_f32 ? 4 : 2) || (o.tokens > 1 && o.ld_x % 8))
+        misaligned(o.y, r.y_f32 ? 4 : 2) || (o.tokens > 1 && o.ld_x % 8) ||
+        (r.bias != 0 && (misaligned(o.w1_scales, 2) || misaligned(o.w2_scales, 2))))   // two blocks' bytes a load
         return FP4Q_ERR_ALIGN;
     const size_t need = fp4q_moe_workspace_bytes(o.tokens, o.experts, o.top_k, o.hidden, o.inter);
     if (!workspace || workspace_bytes < need) return FP4Q_ERR_WORKSPACE;
@@ -1216,20 +1217,18 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
         a.y = (char*)o.y + t * o.ld_y * (r.y_f32 ? 4 : 2);
         const MoePlan p = plan_moe(a.tokens, o.experts, o.top_k, o.hidden, o.inter);
         char* const ws = (char*)workspace;
-        a.counts = (int32_t*)(ws + p.counts);
         a.groups = (MoeGroup*)(ws + p.groups);
         a.expert = (int32_t*)(ws + p.expert);
         a.share = (float*)(ws + p.share);
+        a.place = (int32_t*)(ws + p.place);
         a.pair_token = (int32_t*)(ws + p.pair_token);
         a.pair_share = (float*)(ws + p.pair_share);
         a.mid = (uint16_t*)(ws + p.mid);
         a.mid_rest = (uint16_t*)(ws + p.mid_rest);
-        a.parts = p.splits > 1 ? (float*)(ws + p.parts) : nullptr;
-        a.parts_ld = p.parts_ld;
+        a.parts = (float*)(ws + p.parts);
         a.few = p.few;
         a.group = p.group;
         a.max_groups = p.max_groups;
-        a.splits = p.splits;
         st = hip_status(launch_moe(r.bias, a, (hipStream_t)stream));
         if (st) return st;
     }

@@ -4,16 +4,19 @@
 //         a_te (W2_e act(W1_e x_t + b1_e) + b2_e),   a_te the softmax of the logits
 //
 // Every expert that a token reached is read once, which is what bounds the layer: 4 bits
-// and a scale's share a weight, for few tokens each.  Three launches:
+// and a scale's share a weight, for few tokens each.  Four launches:
 //   k_moe_route  one workgroup: each token's experts and their shares, then the (token, expert)
 //                pairs in the order of the experts and their groups of up to 16 MT
 //                pairs of one expert;
 //   k_moe_up     a workgroup takes 32 gate and 32 up rows of W1 for one group; its waves share K
 //                and join through LDS; a times the activation goes to the scratch in bf16;
-//   k_moe_down   a workgroup takes 32 rows of W2 for all groups: its waves share the
-//                groups' K, each adding its sums to its own [tokens][32] of LDS, joined at the
-//                end in order.  Where 32 rows a workgroup leave compute units idle the groups are
-//                split over workgroups too, whose sums k_moe_join adds in order.
+//   k_moe_down   the same for 64 rows of W2; each pair's products go to the scratch in binary32;
+//   k_moe_join   adds a token's pairs in the order of its choices, so its result does not depend on
+//                which other tokens are there.  (W2's sums kept in LDS for all tokens, a workgroup
+//                going through all groups with no scratch, took 58 us for 48 tokens of 32 experts of
+//                2880 x 2880 where k_moe_down and k_moe_join take 44: parts of K a wave end at
+//                every group.)
+// Up to kMoeFewPairs pairs take two launches instead, rows of W as they lie (below).
 //
 // Products as in kernels_linear.hip: v_mfma_f32_16x16x32_bf16 with rows of W decoded to bf16,
 // exactly, as the A operand and tokens as the B operand; a unit is 128 values of K, of which
@@ -32,8 +35,6 @@ namespace {
 
 enum { kInnerOnly = 0, kPerTile = 1, kPerRow = 2 };      // outer scales inside the sum: none (or one an expert), 2D, 1D
 
-constexpr int kUpWaves = 4, kDownWaves = 8;
-constexpr int kUpChunk = 4096, kDownChunk = 1024;        // values of K whose scale bytes LDS holds
 constexpr int kRouteThreads = 1024;
 
 // ---------------------------------------------------------------- routing
@@ -157,7 +158,6 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
             groups += __builtin_amdgcn_readlane(before, 63);
         }
         for (int i = groups + lane; i < a.max_groups; i += 64) a.groups[i] = MoeGroup{0, 0};
-        if (lane == 0) a.counts[0] = groups;
     }
     __syncthreads();
     for (int p = (int)threadIdx.x; p < a.tokens * a.top_k; p += kRouteThreads) {
@@ -168,6 +168,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
         const int at = first_group[e] * a.group + rank;  // an expert's groups follow one another
         a.pair_token[at] = t;
         a.pair_share[at] = a.share[p];
+        a.place[p] = at;
     }
 }
 
@@ -343,8 +344,8 @@ __device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>
 
 // Units k, k + stride, ... before end, the next one on its way while one is used.  `ready` is called when the first of
 // them is; then scale rows are in LDS, those of tile n at rows + n * apart, from value k0 on.  The loop stays rolled: a
-// kernel of ten thousand bytes of code takes longer to fetch than a token's weights (k_moe_down of one
-// token, unrolled four times 16.6 us, rolled 9.9).
+// kernel of ten thousand bytes of code takes longer to fetch than a token's weights (W2 of one
+// token, 4 experts of 2880 x 2880, unrolled four times 16.6 us, rolled 9.9).
 template <int CHUNK, int BIAS, int OUTER, int NT, int MT, class Ready>
 __device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, rsrc_t x, const uint32_t (&off)[MT], int k, int end,
                                        int stride, const lds_t* rows, int apart, int k0, int quarter, f32x4_t (&acc)[NT][MT],
@@ -383,47 +384,40 @@ __device__ __forceinline__ float gated(const MoeArgs& a, float g, float u)
     return g / (1.0f + expf(-a.alpha * g)) * (u + a.shift);
 }
 
-template <int BIAS, int OUTER, int MT, bool FINE>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeArgs a)
+// 64 rows of W times a group's tokens: the waves of a workgroup share K, and join through LDS in order.  `finish(n, m,
+// v)` gets the sums of tiles n and n + 2 for tile m of the tokens.
+constexpr int kWaves = 4, kChunk = 4096;                 // values of K whose scale bytes LDS holds
+
+template <int BIAS, int OUTER, int MT, class Finish>
+__device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, const int (&first)[4], int stride, int N, int K, const uint16_t* x,
+                                       const uint16_t* rest, const uint32_t (&off)[MT], Finish finish)
 {
-    using S = Scales<BIAS, kUpChunk>;
-    constexpr int kJoin = kUpWaves * 16 * MT * 64 * 4, kScales = 64 * S::kStride;
+    using S = Scales<BIAS, kChunk>;
+    constexpr int kJoin = kWaves * 16 * MT * 64 * 4, kScales = 64 * S::kStride;
     __shared__ __align__(16) unsigned char smem[kJoin > kScales ? kJoin : kScales];
     float(*const join)[16 * MT][64] = reinterpret_cast<float(*)[16 * MT][64]>(smem);
     lds_t* const lds = (lds_t*)smem;
-    const MoeGroup group = a.groups[blockIdx.y];
-    if (group.count == 0) return;
-    const int first_pair = (int)blockIdx.y * a.group;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int i0 = (int)blockIdx.x * 32, K = a.hidden, N = 2 * a.inter;
-    // tiles: gate rows i0 .. + 15 and + 16 .. + 31, the same up rows
-    const int s = a.interleaved ? 2 : 1, up = a.interleaved ? 1 : a.inter;
-    const int first[4] = {s * i0, s * (i0 + 16), s * i0 + up, s * (i0 + 16) + up};
-    const Weights<BIAS, OUTER, 4> w(a.w1, group.expert, first, s, N, K, lane);
-    uint32_t off[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-    {
-        const int token = a.pair_token[first_pair + 16 * m + col];   // -1: none
-        off[m] = token >= 0 ? (uint32_t)token * (uint32_t)(a.ld_x * 2) + place_of(quarter) * 2 : kOff;
-    }
+    const Weights<BIAS, OUTER, 4> w(weight, expert, first, stride, N, K, lane);
     f32x4_t acc[4][MT];
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[n][m] = f32x4_t{0, 0, 0, 0};
-    // a wave stages the scale bytes of 64 / kUpWaves of the rows
-    constexpr int kRows = 64 / kUpWaves, kOf = 16 / kRows;   // waves of a tile
-    const int tile = wave / kOf, row0 = wave % kOf * kRows;
-    const int first_row = tile == 0 ? first[0] : tile == 1 ? first[1] : tile == 2 ? first[2] : first[3];
-    const rsrc_t sr = make_rsrc(a.w1.scales + ((int64_t)group.expert * N + first_row + s * row0) * (K / S::B));
-    for (int k0 = 0; k0 < K; k0 += kUpChunk) {
-        const int end = min(K, k0 + kUpChunk);
+    // a wave stages the scale bytes of a tile
+    static_assert(kWaves == 4, "a tile's scale rows for each wave");
+    const int first_row = wave == 0 ? first[0] : wave == 1 ? first[1] : wave == 2 ? first[2] : first[3];
+    const rsrc_t sr = make_rsrc(weight.scales + ((int64_t)expert * N + first_row) * (K / S::B));
+    for (int k0 = 0; k0 < K; k0 += kChunk) {
+        const int end = min(K, k0 + kChunk);
         if (k0) __syncthreads();                         // everybody is done with the chunk before
-        S::template stage<kRows>(sr, s * (K / S::B), k0 / S::B, (end - k0) / S::B, lds + (16 * tile + row0) * S::kStride, lane);
-        stream<kUpChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(a.x), off, k0 + wave * 128, end, kUpWaves * 128, lds + col * S::kStride,
-                                                       16 * S::kStride, k0, quarter, acc, [] { lds_barrier(); });
+        S::template stage<16>(sr, stride * (K / S::B), k0 / S::B, (end - k0) / S::B, lds + 16 * wave * S::kStride, lane);
+        stream<kChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(x), off, k0 + wave * 128, end, kWaves * 128, lds + col * S::kStride,
+                                           16 * S::kStride, k0, quarter, acc, [] { lds_barrier(); });
+        if (rest)
+            stream<kChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(rest), off, k0 + wave * 128, end, kWaves * 128, lds + col * S::kStride,
+                                               16 * S::kStride, k0, quarter, acc, [] {});
     }
     __syncthreads();
 #pragma unroll
@@ -433,27 +427,50 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeArgs a)
 #pragma unroll
             for (int r = 0; r < 4; ++r) join[wave][(n * MT + m) * 4 + r][lane] = acc[n][m][r];
     __syncthreads();
-    const float whole = a.w1.outer_kind == kOuterTensor ? a.w1.outer[group.expert] : 1.0f;
-    // a wave finishes every fourth pair of 16 rows and 16 tokens
-    for (int p = wave; p < 2 * MT; p += kUpWaves) {
+    const float whole = weight.outer_kind == kOuterTensor ? weight.outer[expert] : 1.0f;
+    // a wave finishes every fourth of the pairs of two tiles of rows and 16 tokens
+    for (int p = wave; p < 2 * MT; p += kWaves) {
         const int n = p & 1, m = p >> 1;
-        if (16 * m + col >= group.count) continue;
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = ((n + (i & 4 ? 2 : 0)) * MT + m) * 4 + (i & 3);
             v[i] = join[0][at][lane];
 #pragma unroll
-            for (int w = 1; w < kUpWaves; ++w) v[i] += join[w][at][lane];
+            for (int w = 1; w < kWaves; ++w) v[i] += join[w][at][lane];
+            v[i] *= whole;
         }
+        finish(n, m, v);
+    }
+}
+
+// 32 gate rows and the same 32 up rows of W1.
+template <int BIAS, int OUTER, int MT, bool FINE>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
+{
+    const MoeGroup group = a.groups[blockIdx.y];
+    if (group.count == 0) return;
+    const int first_pair = (int)blockIdx.y * a.group, lane = (int)threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
+    const int i0 = (int)blockIdx.x * 32, N = 2 * a.inter;
+    // tiles: gate rows i0 .. + 15 and + 16 .. + 31, the same up rows
+    const int s = a.interleaved ? 2 : 1, up = a.interleaved ? 1 : a.inter;
+    const int first[4] = {s * i0, s * (i0 + 16), s * i0 + up, s * (i0 + 16) + up};
+    uint32_t off[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int token = a.pair_token[first_pair + 16 * m + col];   // -1: none
+        off[m] = token >= 0 ? (uint32_t)token * (uint32_t)(a.ld_x * 2) + place_of(quarter) * 2 : kOff;
+    }
+    rows64<BIAS, OUTER, MT>(a.w1, group.expert, first, s, N, a.hidden, a.x, nullptr, off, [&](int n, int m, const float (&v)[8]) {
+        if (16 * m + col >= group.count) return;
         const int pair = first_pair + 16 * m + col, i = i0 + 16 * n + 4 * quarter;
         const float share = a.pair_share[pair];
         float y[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t b = (int64_t)group.expert * N + s * (i + r);
-            const float gate = v[r] * whole + (a.b1 ? a.b1[b] : 0.0f);
-            const float upper = v[4 + r] * whole + (a.b1 ? a.b1[b + up] : 0.0f);
+            const float gate = v[r] + (a.b1 ? a.b1[b] : 0.0f);
+            const float upper = v[4 + r] + (a.b1 ? a.b1[b + up] : 0.0f);
             y[r] = share * gated(a, gate, upper);
         }
         const uint2 hi = make_uint2(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]));
@@ -461,111 +478,54 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeArgs a)
         if constexpr (FINE)
             *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
                 make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
-    }
+    });
 }
 
-// Four neighbouring values of y.
-__device__ __forceinline__ void store_y4(const MoeArgs& a, int t, int n, f32x4_t v)
-{
-    const int64_t at = (int64_t)t * a.ld_y + n;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (a.y_f32) ((float*)a.y)[at + i] = v[i];
-        else ((uint16_t*)a.y)[at + i] = (uint16_t)Dec<0>::round2(v[i], 0.0f);
-    }
-}
-
-// The token's shares of its experts' second biases, in the order of its choices.
-__device__ __forceinline__ f32x4_t add_bias(const MoeArgs& a, int t, int n, f32x4_t v)
-{
-    if (!a.b2) return v;
-    for (int s = 0; s < a.top_k; ++s) {
-        const int e = a.expert[t * a.top_k + s];
-        if (e < 0) break;
-        const float share = a.share[t * a.top_k + s];
-        const float* b = a.b2 + (int64_t)e * a.hidden;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(share, b[n + i], v[i]);
-    }
-    return v;
-}
-
+// 64 rows of W2, as many as there are in the last workgroup.
 template <int BIAS, int OUTER, int MT, bool FINE>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeArgs a)
+__global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeArgs a)
 {
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int col = lane & 15, quarter = lane >> 4;
-    const int n0 = (int)blockIdx.x * 32, K = a.inter;
-    using S = Scales<BIAS, kDownChunk>;
-    MoeGroup* const list = (MoeGroup*)(smem + kDownWaves * (a.tokens * 128 + 32 * S::kStride));
-    lds_t* const scales = (lds_t*)smem + kDownWaves * a.tokens * 128 + wave * (32 * S::kStride);
-    const int steps = (K + 127) / 128;
-    const int groups = a.counts[0];
-    for (int i = (int)threadIdx.x; i < a.max_groups; i += 64 * kDownWaves) list[i] = a.groups[i];
-    f32x4_t* const sums = (f32x4_t*)smem + wave * a.tokens * 8;   // [tokens][8 fours of the 32 rows]
-    for (int i = lane; i < a.tokens * 8; i += 64) sums[i] = f32x4_t{0, 0, 0, 0};
-    __syncthreads();
-
-    const int parts = kDownWaves * (int)gridDim.y, part = (int)blockIdx.y * kDownWaves + wave;
-    const int64_t total = (int64_t)groups * steps;
-    const int from = (int)(total * part / parts), to = (int)(total * (part + 1) / parts);
-    int at = from;
-    while (at < to) {
-        // the part's units of one group, as many as their scales have places
-        const int gi = at / steps, s0 = at - gi * steps, s1 = min(min(steps, s0 + to - at), s0 + kDownChunk / 128);
-        at += s1 - s0;
-        const MoeGroup group{__builtin_amdgcn_readfirstlane(list[gi].expert), __builtin_amdgcn_readfirstlane(list[gi].count)};
-        const int first[2] = {n0, n0 + 16};
-        const Weights<BIAS, OUTER, 2> w(a.w2, group.expert, first, 1, a.hidden, K, lane);
-        uint32_t off[MT];
-        int token[MT];
+    const MoeGroup group = a.groups[blockIdx.y];
+    if (group.count == 0) return;
+    const int first_pair = (int)blockIdx.y * a.group, lane = (int)threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
+    const int n0 = (int)blockIdx.x * 64, further = min(n0 + 32, a.hidden - 32);   // a multiple of 32
+    const int first[4] = {n0, n0 + 16, further, further + 16};
+    uint32_t off[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int pair = gi * a.group + 16 * m + col;
-            const bool live = 16 * m + col < group.count;
-            token[m] = a.pair_token[pair];               // -1: none
-            off[m] = live ? (uint32_t)pair * (uint32_t)(K * 2) + place_of(quarter) * 2 : kOff;
-        }
-        f32x4_t acc[2][MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[0][m] = acc[1][m] = f32x4_t{0, 0, 0, 0};
-        const int k0 = s0 * 128, k1 = min(K, s1 * 128);
-        S::template stage<32>(make_rsrc(a.w2.scales + ((int64_t)group.expert * a.hidden + n0) * (K / S::B)), K / S::B, k0 / S::B,
-                              (k1 - k0) / S::B, scales, lane);
-        stream<kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid), off, k0, k1, 128, scales + col * S::kStride,
-                                                               16 * S::kStride, k0, quarter, acc, [] {});
-        if constexpr (FINE)
-            stream<kDownChunk, BIAS, OUTER, 2, MT>(w, make_rsrc(a.mid_rest), off, k0, k1, 128, scales + col * S::kStride,
-                                                                   16 * S::kStride, k0, quarter, acc, [] {});
-        const float whole = a.w2.outer_kind == kOuterTensor ? a.w2.outer[group.expert] : 1.0f;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if (token[m] >= 0) {                         // a token is once in a group
-                sums[token[m] * 8 + quarter] += acc[0][m] * whole;
-                sums[token[m] * 8 + 4 + quarter] += acc[1][m] * whole;
-            }
-    }
-    __syncthreads();
-    for (int i = (int)threadIdx.x; i < a.tokens * 8; i += 64 * kDownWaves) {
-        const f32x4_t* p = (const f32x4_t*)smem + i;
-        f32x4_t v = p[0];
-        for (int w = 1; w < kDownWaves; ++w) v += p[w * a.tokens * 8];
-        const int t = i >> 3, n = n0 + 4 * (i & 7);
-        if (a.parts) *(f32x4_t*)(a.parts + ((int64_t)blockIdx.y * a.tokens + t) * a.parts_ld + n) = v;
-        else store_y4(a, t, n, add_bias(a, t, n, v));
-    }
+    for (int m = 0; m < MT; ++m)
+        off[m] = 16 * m + col < group.count ? (uint32_t)(first_pair + 16 * m + col) * (uint32_t)(a.inter * 2) + place_of(quarter) * 2 : kOff;
+    rows64<BIAS, OUTER, MT>(a.w2, group.expert, first, 1, a.hidden, a.inter, a.mid, FINE ? a.mid_rest : nullptr, off,
+                            [&](int n, int m, const float (&v)[8]) {
+        if (16 * m + col >= group.count) return;
+        float* const to = a.parts + (int64_t)(first_pair + 16 * m + col) * a.hidden + n0 + 16 * n + 4 * quarter;
+        *(f32x4_t*)to = f32x4_t{v[0], v[1], v[2], v[3]};
+        if (n0 + 32 < a.hidden) *(f32x4_t*)(to + 32) = f32x4_t{v[4], v[5], v[6], v[7]};
+    });
 }
 
-// Adds the splits' sums in order: four values of a row a lane.
+// A token's sums over its experts in the order of its choices: four values of a row a lane.
 __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 {
-    const int quads = (int)(a.parts_ld / 4), at = (int)blockIdx.x * 256 + (int)threadIdx.x;
+    const int quads = a.hidden / 4, at = (int)blockIdx.x * 256 + (int)threadIdx.x;
     if (at >= quads * a.tokens) return;
     const int t = at / quads, n = (at - t * quads) * 4;
     f32x4_t v = {0, 0, 0, 0};
-    for (int s = 0; s < a.splits; ++s) v += *(const f32x4_t*)(a.parts + ((int64_t)s * a.tokens + t) * a.parts_ld + n);
-    store_y4(a, t, n, add_bias(a, t, n, v));
+    for (int s = 0; s < a.top_k; ++s) {
+        const int e = a.expert[t * a.top_k + s];
+        if (e < 0) break;
+        v += *(const f32x4_t*)(a.parts + (int64_t)a.place[t * a.top_k + s] * a.hidden + n);
+        if (!a.b2) continue;
+        const float share = a.share[t * a.top_k + s];
+        const float* b = a.b2 + (int64_t)e * a.hidden + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(share, b[i], v[i]);
+    }
+    const int64_t to = (int64_t)t * a.ld_y + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (a.y_f32) ((float*)a.y)[to + i] = v[i];
+        else ((uint16_t*)a.y)[to + i] = (uint16_t)Dec<0>::round2(v[i], 0.0f);
+    }
 }
 
 // ---------------------------------------------------------------- a few tokens
@@ -756,17 +716,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
 template <int BIAS, int O1, int O2, int MT, bool FINE>
 hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 {
-    const int lds = kDownWaves * (a.tokens * 128 + 32 * Scales<BIAS, kDownChunk>::kStride) + a.max_groups * (int)sizeof(MoeGroup);
-    static OncePerDevice once;
-    const hipError_t st = allow_lds(once, reinterpret_cast<const void*>(k_moe_down<BIAS, O2, MT, FINE>),
-                                    160 * 1024);
-    if (st != hipSuccess) return st;
     hipLaunchKernelGGL((k_moe_up<BIAS, O1, MT, FINE>), dim3((uint32_t)(a.inter / 32), (uint32_t)a.max_groups),
-                       dim3(64 * kUpWaves), 0, s, a);
-    const int tiles = a.hidden / 32;
-    hipLaunchKernelGGL((k_moe_down<BIAS, O2, MT, FINE>), dim3((uint32_t)tiles, (uint32_t)a.splits), dim3(64 * kDownWaves), lds, s, a);
-    if (a.splits > 1)
-        hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)((a.parts_ld / 4 * a.tokens + 255) / 256)), dim3(256), 0, s, a);
+                       dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((k_moe_down<BIAS, O2, MT, FINE>), dim3((uint32_t)((a.hidden + 63) / 64), (uint32_t)a.max_groups),
+                       dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)(((int64_t)a.hidden / 4 * a.tokens + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -817,31 +771,27 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
 {
     MoePlan p;
     const int64_t pairs = tokens * top_k;
+    // Row by row an expert is read for each of its pairs.  Against groups, us: 4 pairs of 32 experts of 2880 x 2880
+    // (NVFP4) 24 : 35, 16 65 : 70, 24 91 : 87, 48 156 : 115; 9 pairs of 20 experts of 2048 x 736
+    // (AMD-FP4) 15 : 21, 21 22 : 27, 30 30 : 28.
+    p.few = pairs <= kMoeFewPairs ? 1 : 0;
     // Pairs of a group: an expert of more is read again for each further group (from the caches), one of
     // fewer pays for tiles of tokens that it has not.  An expert's pairs are at most the tokens.
-    p.few = pairs <= kMoeFewPairs ? 1 : 0;
     p.group = tokens <= 16 || pairs <= 8 * experts ? 16 : tokens <= 32 || pairs <= 20 * experts ? 32 : 64;
     const int64_t reached = experts < pairs ? experts : pairs;
     p.max_groups = (int32_t)(reached + (tokens > p.group ? pairs / p.group : 0));
-    // Workgroups of k_moe_down: 32 rows of W2 each; few of them split the groups until there are
-    // two a compute unit, while each wave keeps two units.
-    const int64_t tiles = hidden / 32, steps = (inter + 127) / 128;
-    int64_t splits = 512 / tiles;
-    if (splits > reached * steps / (kDownWaves * 2)) splits = reached * steps / (kDownWaves * 2);
-    p.splits = (int32_t)(splits < 1 ? 1 : splits);
-    p.parts_ld = hidden;
     size_t at = 0;
     const auto take = [&at](size_t n) { const size_t here = at; at += padded(n); return here; };
-    p.counts = take(16);
     p.groups = take(p.max_groups * sizeof(MoeGroup));
     p.expert = take(pairs * 4);
     p.share = take(pairs * 4);
+    p.place = take(pairs * 4);
     const int64_t places = (int64_t)p.max_groups * p.group;
     p.pair_token = take(places * 4);
     p.pair_share = take(places * 4);
     p.mid = take(places * inter * 2);
     p.mid_rest = take(places * inter * 2);
-    p.parts = take(p.splits > 1 ? p.splits * tokens * p.parts_ld * 4 : 0);
+    p.parts = take(p.few ? 0 : places * hidden * 4);
     p.bytes = at;
     return p;
 }

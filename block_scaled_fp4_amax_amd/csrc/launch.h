@@ -375,7 +375,7 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s);
 // (all experts' rows one after another).
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;   // tokens of a launch
 
-constexpr int kMoeFewPairs = 16;   // of a token and an expert, that whole waves take row by row
+constexpr int kMoeFewPairs = 24;   // of a token and an expert, that whole waves take row by row
 
 struct MoeGroup {
     int32_t expert, count;     // pairs in the first `count` places of the group; 0: nothing here
@@ -399,23 +399,21 @@ struct MoeArgs {
     int32_t tokens, experts, top_k, hidden, inter, renormalize, interleaved, y_f32;
     float alpha, limit, shift;
     // scratch
-    int32_t* counts;           // groups
     MoeGroup* groups;          // [max_groups]
     int32_t* expert;           // [tokens, top_k], -1: none
     float* share;
+    int32_t* place;            // of the pair among the groups'
     int32_t* pair_token;       // [max_groups * group] by place, -1: none
     float* pair_share;
     uint16_t *mid, *mid_rest;  // bf16 [max_groups * group, inter]: the activations, and what they leave
-    float* parts;              // FP32 [splits][tokens][parts_ld], null with one split
-    int64_t parts_ld;
+    float* parts;              // FP32 [max_groups * group, hidden]: W2's products
     int32_t few;               // 1: k_moe_few_up and k_moe_few_down
-    int32_t group, max_groups, splits;   // pairs of a group at most, groups at most, splits of k_moe_down
+    int32_t group, max_groups; // pairs of a group at most, groups at most
 };
 
 struct MoePlan {
-    int32_t few, group, max_groups, splits;
-    int64_t parts_ld;
-    size_t counts, groups, expert, share, pair_token, pair_share, mid, mid_rest, parts, bytes;
+    int32_t few, group, max_groups;
+    size_t groups, expert, share, place, pair_token, pair_share, mid, mid_rest, parts, bytes;
 };
 
 MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);

@@ -34,7 +34,8 @@ def moe(cfg=None, ws=FAKE, wsb=1 << 30, **kw):
     (dict(inter=65568), fq.ERR_UNSUPPORTED), (dict(renormalize=2), fq.ERR_MODE), (dict(interleaved=-1), fq.ERR_MODE),
     (dict(limit=-1.0), fq.ERR_MODE), (dict(limit=float("nan")), fq.ERR_MODE), (dict(alpha=float("nan")), fq.ERR_MODE),
     (dict(shift=float("nan")), fq.ERR_MODE), (dict(ws=None), fq.ERR_WORKSPACE), (dict(wsb=1024), fq.ERR_WORKSPACE),
-    (dict(ws=MIS), fq.ERR_ALIGN), (dict(tokens=0, x=None, ws=None), fq.OK)])
+    (dict(ws=MIS), fq.ERR_ALIGN), (dict(tokens=0, x=None, ws=None), fq.OK),
+    (dict(w1_scales=FAKE + 1), fq.ERR_ALIGN), (dict(w2_scales=FAKE + 1), fq.ERR_ALIGN)])
 def test_refusals(kw, st):
     assert moe(**kw) == st
 
