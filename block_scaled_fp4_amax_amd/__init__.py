@@ -1064,17 +1064,20 @@ def _norm_rows(t, shape, what, types):
     """Row pitch of a [rows, hidden] bf16 or float32 tensor whose rows are contiguous."""
     if t.dtype not in types:
         raise Fp4Error(ERR_DTYPE, "%s dtype %s" % (what, t.dtype))
-    if len(t.shape) != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError("%s must be %s, got %s" % (what, "2-D" if shape is None else list(shape), list(t.shape)))
-    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != 1:
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
+        raise ValueError("%s must be %s, got %s" % (what, "2-D" if shape is None else list(shape), list(got)))
+    rows, hidden = got
+    ld, step = t.stride()
+    if rows and hidden > 1 and step != 1:
         raise ValueError("%s rows must be contiguous (stride(1) == 1)" % what)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if rows > 1 else hidden
 
 
 def _norm_weight(weight, hidden, types):
     if weight.dtype not in types:
         raise Fp4Error(ERR_DTYPE, "weight dtype %s" % weight.dtype)
-    if tuple(weight.shape) != (hidden,) or not weight.is_contiguous():
+    if weight.shape != (hidden,) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous [%d]" % hidden)
 
 
@@ -1127,11 +1130,12 @@ def fp4_add_rms_norm(x, weight, residual=None, *, eps=1e-6, fp8=None, y=None, y_
         res["fp8"] = _out(given.get("fp8"), (rows, hidden), torch.uint8, dev, "fp8", stream)
         res["fp8_scales"] = _out(given.get("fp8_scales"), (rows, hidden // 32) if fp8 == "mx" else (rows,),
                                  torch.uint8 if fp8 == "mx" else torch.float32, dev, "fp8_scales", stream)
-    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    f32 = lambda d: 2 if d == torch.float32 else 0  # noqa: E731
-    a = _AddRmsNorm(x.data_ptr(), p(residual), ld_x, ld_r, weight.data_ptr(), None if residual is None else p(res["residual"]),
-                    p(res["rstd"]), p(res["y"]), p(res["fp8"]), p(res["fp8_scales"]), rows, hidden, eps, f32(x.dtype),
-                    0 if residual is None else f32(residual.dtype), f32(weight.dtype), f32(y_dtype), _FP8_MODES[fp8], 0)
+    kind = {torch.bfloat16: 0, torch.float32: 2}
+    added = residual is not None
+    a = _AddRmsNorm(x.data_ptr(), residual.data_ptr() if added else None, ld_x, ld_r, weight.data_ptr(),
+                    res["residual"].data_ptr() if added else None, res["rstd"].data_ptr(), res["y"].data_ptr() if y else None,
+                    res["fp8"].data_ptr() if fp8 else None, res["fp8_scales"].data_ptr() if fp8 else None, rows, hidden, eps,
+                    kind[x.dtype], kind[residual.dtype] if added else 0, kind[weight.dtype], kind[y_dtype], _FP8_MODES[fp8], 0)
     _launch("fp4_add_rms_norm", lib().fp4_add_rms_norm, dev, ct.byref(a), _raw_stream(stream, dev))
     return res
 

@@ -24,6 +24,8 @@ namespace {
 
 template <int W>
 constexpr int kRowThreads = W < 4 ? 256 : 64 * W;
+template <int W>
+constexpr int kGradThreads = W < 16 ? 512 : 64 * W;
 
 // Eight values from memory, bf16 or FP32 (16-byte aligned).
 template <bool F32>
@@ -238,54 +240,102 @@ __global__ __launch_bounds__(kRowThreads<W>) void k_add_rms_norm(NormArgs a)
     }
 }
 
+// A lane's part of a row on its way.
+template <int C, bool YF32, bool HF32>
+struct GradRow {
+    Chunk<YF32> y[C];
+    Chunk<HF32> h[C], r[C];
+    float rstd;
+
+    // A row beyond the last is zeros.
+    __device__ __forceinline__ void load(const NormGradArgs& a, int64_t row, int t, int stride)
+    {
+        const int n = row < a.rows ? (int)(a.hidden >> 3) : 0;
+        const char* const dyr = (const char*)a.dy + row * a.ld_dy * (YF32 ? 4 : 2);
+        const char* const hr = (const char*)a.h + row * a.ld_h * (HF32 ? 4 : 2);
+        const char* const dr = (const char*)a.dres + row * a.ld_dres * (HF32 ? 4 : 2);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = c * stride + t;
+            if (at < n) y[c].load(dyr, 8 * at), h[c].load(hr, 8 * at);
+            else y[c].clear(), h[c].clear();
+            if (a.dres && at < n) r[c].load(dr, 8 * at);
+            else r[c].clear();
+        }
+        rstd = row < a.rows ? a.rstd[row] : 0.0f;
+    }
+};
+
 // Every workgroup takes rows blockIdx.x, + gridDim.x, ... (times the rows it holds at
-// once) and keeps the sums of dy n of its lanes' columns in registers; they join
-// through LDS, then over the workgroups in k_norm_join.
+// once), the next one on its way while one is used, and keeps the sums of dy n of its lanes'
+// columns in registers; they join through LDS, then over the workgroups in k_norm_join.  The weight lies in LDS: its
+// registers hold the next row.  8192 rows of 2880 in bf16 (189 MB): 35 us and k_norm_join 4; a wave a row
+// with the weight in registers and nothing ahead 45, the weight in LDS 39, and the next row's registers spill (76).
 template <int W, int C, bool YF32, bool HF32>
-__global__ __launch_bounds__(kRowThreads<W>) void k_rms_norm_backward(NormGradArgs a)
+__global__ __launch_bounds__(kGradThreads<W>) void k_rms_norm_backward(NormGradArgs a)
 {
-    constexpr int kRows = kRowThreads<W> / (64 * W);
-    __shared__ float sums[2][kRowThreads<W> / 64];
-    __shared__ float join[kRows > 1 ? kRows - 1 : 1][64 * W * 8];
+    constexpr int kRows = kGradThreads<W> / (64 * W);
+    constexpr bool kAhead = W < 16;                      // with 16 waves there are no registers for it
+    __shared__ float sums[2][kGradThreads<W> / 64];
+    // the weight, then the sums' join (W < 16)
+    constexpr bool kShared = W < 16;
+    __shared__ __align__(16) float lds[kShared ? 8 * C * 64 * W : 1];
     const int wave = (int)threadIdx.x >> 6, in_row = wave % W, first = wave - in_row;
     const int t = in_row * 64 + ((int)threadIdx.x & 63);
     const int n = (int)(a.hidden >> 3);
     const float inv_n = 1.0f / (float)a.hidden;
-    float w[C][8], dw[C][8];
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + wave / W;
+    using Row = GradRow<C, YF32, HF32>;
+    Row now;
+    if constexpr (kAhead) now.load(a, row, t, 64 * W);
+    float w[kShared ? 1 : C][8], dw[C][8];
+    const auto weight = [&](int c, float (&v)[8]) {
+        if constexpr (kShared) {                         // two reads of 16 bytes: lanes side by side
+            const float4 lo = *(const float4*)(lds + 2 * c * 256 * W + t * 4), hi = *(const float4*)(lds + (2 * c + 1) * 256 * W + t * 4);
+            v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = w[c][i];
+        }
+    };
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = c * 64 * W + t;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[c][i] = dw[c][i] = 0.0f;
-        if (at < n) load_weight(a.weight, a.w_f32, 8 * at, w[c]);
-    }
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + wave / W; row < a.rows; row += (int64_t)gridDim.x * kRows, turn ^= 1) {
-        const char* const dyr = (const char*)a.dy + row * a.ld_dy * (YF32 ? 4 : 2);
-        const char* const hr = (const char*)a.h + row * a.ld_h * (HF32 ? 4 : 2);
-        const char* const dr = (const char*)a.dres + row * a.ld_dres * (HF32 ? 4 : 2);
-        Chunk<YF32> yc[C];
-        Chunk<HF32> hc[C], rc[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int at = c * 64 * W + t;
-            if (at < n) yc[c].load(dyr, 8 * at), hc[c].load(hr, 8 * at);
-            else yc[c].clear(), hc[c].clear();
-            if (a.dres && at < n) rc[c].load(dr, 8 * at);
-            else rc[c].clear();
+        float v[8] = {};
+        if (at < n) load_weight(a.weight, a.w_f32, 8 * at, v);
+        if constexpr (kShared) {
+            if (wave / W == c % kRows) {
+                *(float4*)(lds + 2 * c * 256 * W + t * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                *(float4*)(lds + (2 * c + 1) * 256 * W + t * 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
         }
-        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dw[c][i] = 0.0f;
+            if constexpr (!kShared) w[c][i] = v[i];
+        }
+    }
+    if constexpr (kShared) __syncthreads();
+    int turn = 0;
+    // all of a workgroup's waves take as many turns, for their barriers
+    for (int64_t head = (int64_t)blockIdx.x * kRows; head < a.rows; head += step, row += step, turn ^= 1) {
+        Row next;
+        if constexpr (kAhead) next.load(a, row + step, t, 64 * W);
+        else now.load(a, row, t, 64 * W);
+        const float rstd = now.rstd;
         float s = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            float dy[8], h[8];
-            yc[c].values(dy);
-            hc[c].values(h);
+            float dy[8], h[8], wc[8];
+            now.y[c].values(dy);
+            now.h[c].values(h);
+            weight(c, wc);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float nv = h[i] * rstd;
                 dw[c][i] = __builtin_fmaf(dy[i], nv, dw[c][i]);
-                s = __builtin_fmaf(dy[i] * w[c][i], nv, s);
+                s = __builtin_fmaf(dy[i] * wc[i], nv, s);
             }
         }
         // two turns' sums have places of their own: a wave that is a row ahead writes others
@@ -293,33 +343,45 @@ __global__ __launch_bounds__(kRowThreads<W>) void k_rms_norm_backward(NormGradAr
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = c * 64 * W + t;
-            float dy[8], h[8], d[8];
-            yc[c].values(dy);
-            hc[c].values(h);
-            rc[c].values(d);
+            float dy[8], h[8], d[8], wc[8];
+            now.y[c].values(dy);
+            now.h[c].values(h);
+            now.r[c].values(d);
+            weight(c, wc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] += rstd * (dy[i] * w[c][i] - h[i] * rstd * s);
-            if (at < n) store8(a.dx, HF32, row * a.hidden + 8 * at, d);
+            for (int i = 0; i < 8; ++i) d[i] += rstd * (dy[i] * wc[i] - h[i] * rstd * s);
+            if (row < a.rows && at < n) store8(a.dx, HF32, row * a.hidden + 8 * at, d);
         }
+        if constexpr (kAhead) now = next;
     }
     if (!a.dw) return;
     float* const out = a.parts ? a.parts + (int64_t)blockIdx.x * a.hidden : a.dw;
+    if constexpr (kRows > 1) {                           // wave after wave adds its sums, in order
+        for (int p = 1; p < kRows; ++p) {
+            __syncthreads();                             // every wave is done with its rows, or with the wave before
+            if (wave / W == p) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    *(float4*)(lds + 2 * c * 256 * W + t * 4) = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+                    *(float4*)(lds + (2 * c + 1) * 256 * W + t * 4) = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+                }
+            }
+            __syncthreads();
+            if (wave < W) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float v[8];
+                    weight(c, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dw[c][i] += v[i];
+                }
+            }
+        }
+        if (wave >= W) return;
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = c * 64 * W + t;
-        if constexpr (kRows > 1) {
-            __syncthreads();                             // every wave is done with its rows, or with the chunk before
-            if (wave >= W) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) join[wave / W - 1][i * 64 * W + t] = dw[c][i];
-            }
-            __syncthreads();
-            if (wave >= W) continue;
-#pragma unroll
-            for (int p = 0; p < kRows - 1; ++p)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dw[c][i] += join[p][i * 64 * W + t];
-        }
         if (at >= n) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -327,28 +389,38 @@ __global__ __launch_bounds__(kRowThreads<W>) void k_rms_norm_backward(NormGradAr
     }
 }
 
-// The weight's gradient from the workgroups' sums: 16 columns a workgroup, whose 16 groups of
-// lanes take every 16th part, in binary64 and in a fixed order.
-__global__ __launch_bounds__(256) void k_norm_join(const float* parts, int count, int64_t hidden, float* dw)
+// The weight's gradient from the workgroups' sums: 16 columns a workgroup, whose 64 groups of
+// lanes take every 64th part, in binary64 and in a fixed order.
+__global__ __launch_bounds__(1024) void k_norm_join(const float* parts, int count, int64_t hidden, float* dw)
 {
-    __shared__ double part[16][16];
+    __shared__ double part[64][16];
     const int lane = (int)threadIdx.x & 15, group = (int)threadIdx.x >> 4;
     const int64_t col = (int64_t)blockIdx.x * 16 + lane;
     double s = 0.0;
     if (col < hidden)
-        for (int p = group; p < count; p += 16) s += (double)parts[p * hidden + col];
+        for (int p = group; p < count; p += 256) {       // four loads on their way
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = p + 64 * i < count ? parts[(p + 64 * i) * hidden + col] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s += (double)v[i];
+        }
     part[group][lane] = s;
     __syncthreads();
-    if (group != 0 || col >= hidden) return;
+    if (group >= 4) return;
+    s = part[group][lane];                               // one wave: groups 4 apart, then its four rows of lanes
 #pragma unroll
-    for (int p = 1; p < 16; ++p) s += part[p][lane];
-    dw[col] = (float)s;
+    for (int p = 1; p < 16; ++p) s += part[4 * p + group][lane];
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (group == 0 && col < hidden) dw[col] = (float)s;
 }
 
-// Waves of a row: one while rows are many and a lane can hold its chunks (forward 8, backward 6), more
-// where few rows would leave lanes idle.
+// Waves of a row.  Forward one while rows are many and a lane can hold its chunks (8); backward two while rows are
+// many and a lane can hold three chunks of this row and three of the next; more where few rows
+// would leave lanes idle.
 int fwd_waves(int64_t rows, int64_t hidden) { return rows >= 1024 && hidden / 8 <= 64 * 8 ? 1 : 4; }
-int bwd_waves(int64_t rows, int64_t hidden) { return hidden / 8 > 256 * 4 ? 16 : rows >= 1024 && hidden / 8 <= 64 * 6 ? 1 : 4; }
+int bwd_waves(int64_t rows, int64_t hidden) { return hidden / 8 > 512 * 2 ? 16 : rows >= 1024 && hidden / 8 <= 128 * 3 ? 2 : 8; }
 
 int chunks_of(int64_t hidden, int waves) { return (int)((hidden / 8 + 64 * waves - 1) / (64 * waves)); }
 
@@ -366,7 +438,7 @@ void launch_fwd(const NormArgs& a, hipStream_t s)
 template <int W, int C>
 void launch_bwd(const NormGradArgs& a, hipStream_t s)
 {
-    const dim3 grid((uint32_t)a.groups), block(kRowThreads<W>);
+    const dim3 grid((uint32_t)a.groups), block(kGradThreads<W>);
     if (a.dy_f32 && a.h_f32) hipLaunchKernelGGL((k_rms_norm_backward<W, C, true, true>), grid, block, 0, s, a);
     else if (a.dy_f32) hipLaunchKernelGGL((k_rms_norm_backward<W, C, true, false>), grid, block, 0, s, a);
     else if (a.h_f32) hipLaunchKernelGGL((k_rms_norm_backward<W, C, false, true>), grid, block, 0, s, a);
@@ -395,9 +467,10 @@ hipError_t launch_add_rms_norm(const NormArgs& a, hipStream_t s)
 NormGradPlan plan_rms_norm_backward(int64_t rows, int64_t hidden)
 {
     const int waves = bwd_waves(rows, hidden);
-    const int64_t at_once = waves < 4 ? 4 / waves : 1, need = (rows + at_once - 1) / at_once;
-    // two workgroups of 256 lanes a compute unit, one of 1024
-    const int64_t most = waves == 16 ? 256 : 512;
+    const int64_t at_once = waves == 2 ? 4 : 1, need = (rows + at_once - 1) / at_once;
+    // one workgroup a compute unit: two leave twice the sums to join, and are not faster (4096 rows of 8192, both
+    // kernels: 52.5 us, with two 56)
+    const int64_t most = 256;
     NormGradPlan p;
     p.groups = (int32_t)(need < 1 ? 1 : need < most ? need : most);
     p.bytes = p.groups > 1 ? (size_t)p.groups * hidden * sizeof(float) : 0;
@@ -407,18 +480,17 @@ NormGradPlan plan_rms_norm_backward(int64_t rows, int64_t hidden)
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s)
 {
     const int waves = bwd_waves(a.rows, a.hidden), chunks = chunks_of(a.hidden, waves);
-    if (waves == 1) {
-        if (chunks <= 2) launch_bwd<1, 2>(a, s);
-        else if (chunks <= 4) launch_bwd<1, 4>(a, s);
-        else launch_bwd<1, 6>(a, s);
-    } else if (waves == 4) {
-        if (chunks <= 2) launch_bwd<4, 2>(a, s);
-        else launch_bwd<4, 4>(a, s);
+    if (waves == 2) {
+        if (chunks <= 2) launch_bwd<2, 2>(a, s);
+        else launch_bwd<2, 3>(a, s);
+    } else if (waves == 8) {
+        if (chunks <= 1) launch_bwd<8, 1>(a, s);
+        else launch_bwd<8, 2>(a, s);
     } else {
         launch_bwd<16, 2>(a, s);
     }
     if (a.parts && a.dw)
-        hipLaunchKernelGGL(k_norm_join, dim3((uint32_t)((a.hidden + 15) / 16)), dim3(256), 0, s, a.parts, a.groups,
+        hipLaunchKernelGGL(k_norm_join, dim3((uint32_t)((a.hidden + 15) / 16)), dim3(1024), 0, s, a.parts, a.groups,
                            a.hidden, a.dw);
     return hipGetLastError();
 }
