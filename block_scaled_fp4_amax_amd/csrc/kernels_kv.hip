@@ -150,22 +150,29 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
 // another chunk, the lane loads that one too (from the caches, where its own lane's
 // load brings it).
 template <bool XF32>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8])
-{
-    const char* q = (const char*)p + at * (XF32 ? 4 : 2);
-    if constexpr (XF32) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 u = ((const float4*)q)[i];
-            v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-        }
-    } else {
-        const uint4 u = *(const uint4*)q;
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+struct Chunk {
+    uint4 w[XF32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void* p, int64_t at)
+    {
+        const uint4* const q = (const uint4*)((const char*)p + at * (XF32 ? 4 : 2));
+        w[0] = q[0];
+        if constexpr (XF32) w[1] = q[1];
     }
-}
+
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < (XF32 ? 2 : 1); ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (XF32) v[4 * i + j] = __uint_as_float(u[j]);
+                else v[2 * j] = bf16_lo(u[j]), v[2 * j + 1] = bf16_hi(u[j]);
+            }
+        }
+    }
+};
 
 // The angles of a chunk of eight values from `at`: eight of each (halves), or four (interleaved).
 struct Angles {
@@ -206,83 +213,133 @@ struct Angles {
     }
 };
 
-// A workgroup takes `per` heads of K, of V or of q (blockIdx.y) for a run of tokens: a lane keeps its
-// angles for all of them.
+// A chunk of one head on its way, with its partners' where they are another one.
+template <bool XF32>
+struct Turned {
+    Chunk<XF32> own, other;
+
+    __device__ __forceinline__ void load(const void* x, int64_t at, const Angles& turn, bool interleaved)
+    {
+        own.load(x, at);
+        if (turn.partner != 0 && !interleaved) other.load(x, at + turn.partner);
+    }
+
+    __device__ __forceinline__ void values(const Angles& turn, bool interleaved, float (&y)[8]) const
+    {
+        float x[8], p[8];
+        own.values(x);
+        if (turn.partner != 0) {
+            if (!interleaved) other.values(p);
+            turn.turn(interleaved, x, p, y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = x[j];
+        }
+    }
+};
+
+constexpr int kRopeAhead = 4;                            // heads of q, and chunks of K or V, that a lane loads together
+
+// Queries: eight values a lane, so that a store of the wave writes whole rows.
+template <bool XF32>
+__device__ __forceinline__ void turn_queries(const KvRopeArgs& a, int64_t token, int part, int h0, int h1)
+{
+    const int64_t position = a.positions[token];
+    const bool known = position >= 0 && position < a.table_rows, interleaved = a.interleaved != 0;
+    Angles turn;
+    turn.partner = 0;
+    if (known) turn.load(a, position, part * 8);
+    for (int h = h0; h < h1; h += kRopeAhead) {
+        Turned<XF32> x[kRopeAhead];
+#pragma unroll
+        for (int u = 0; u < kRopeAhead; ++u)
+            x[u].load(a.q, token * a.ld_q + (int64_t)min(h + u, h1 - 1) * a.kv.dim + part * 8, turn, interleaved);
+        // q_out may be q: every lane of the rows has its values before one of them stores
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int u = 0; u < kRopeAhead; ++u) {
+            if (h + u >= h1) break;
+            float v[8];
+            x[u].values(turn, interleaved, v);
+            if (!known) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            }
+            const int64_t to = token * a.ld_out + (int64_t)(h + u) * a.kv.dim + part * 8;
+            if (XF32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *(float4*)((float*)a.q_out + to + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else {
+                *(uint4*)((uint16_t*)a.q_out + to) = make_uint4(Dec<0>::round2(v[0], v[1]), Dec<0>::round2(v[2], v[3]),
+                                                                Dec<0>::round2(v[4], v[5]), Dec<0>::round2(v[6], v[7]));
+            }
+        }
+    }
+}
+
+// A workgroup takes `per` heads of K, of V or of q (blockIdx.y; q in two halves of its tokens) for a run of tokens: a
+// lane keeps its angles for all of them.
 template <int BIAS, bool XF32>
 __global__ __launch_bounds__(kThreads) void k_kv_append_rope(KvRopeArgs a)
 {
     __shared__ double recip[kRecipTableSize];
     __shared__ float2 rne[BIAS == 0 ? 1 : kRneTableSize];
     int unit = (int)blockIdx.y;
+    const int lanes = a.kv.dim >> 4, run = kThreads / lanes;   // of 16 values; tokens
+    const int64_t token0 = (int64_t)blockIdx.x * run;
     const int kv_units = (a.kv.heads + a.per - 1) / a.per;
-    const bool is_q = unit >= 2 * kv_units, is_v = !is_q && unit >= kv_units;
-    unit -= is_q ? 2 * kv_units : is_v ? kv_units : 0;
-    if constexpr (BIAS != 0) {
-        if (!is_q) {                                     // the same for the whole workgroup
-            fill_recip_table(recip, (int)threadIdx.x);
-            fill_rne_table<BIAS>(rne, (int)threadIdx.x);
-            __syncthreads();
-        }
+    if (unit >= 2 * kv_units) {
+        unit -= 2 * kv_units;
+        const int h0 = (unit >> 1) * a.per;
+        const int64_t token = token0 + (unit & 1) * (run >> 1) + (int)threadIdx.x / (2 * lanes);
+        if (token < a.tokens) turn_queries<XF32>(a, token, (int)threadIdx.x % (2 * lanes), h0, min(a.q_heads, h0 + a.per));
+        return;
     }
-    const int lanes = a.kv.dim >> 4;
-    const int64_t token = (int64_t)blockIdx.x * (kThreads / lanes) + (int)threadIdx.x / lanes;
+    const bool is_v = unit >= kv_units;
+    unit -= is_v ? kv_units : 0;
+    if constexpr (BIAS != 0) {
+        fill_recip_table(recip, (int)threadIdx.x);
+        fill_rne_table<BIAS>(rne, (int)threadIdx.x);
+        __syncthreads();
+    }
+    const int64_t token = token0 + (int)threadIdx.x / lanes;
     const int part = (int)threadIdx.x % lanes;
     if (token >= a.tokens) return;
     const int64_t position = a.positions[token];
-    const bool known = position >= 0 && position < a.table_rows;
-    const int heads = is_q ? a.q_heads : a.kv.heads, h0 = unit * a.per, h1 = min(heads, h0 + a.per);
-    const char* x = (const char*)(is_q ? a.q : is_v ? a.v : a.k);
-    const int64_t ld = is_q ? a.ld_q : is_v ? a.ld_v : a.ld_k;
+    const int h0 = unit * a.per, h1 = min(a.kv.heads, h0 + a.per);
     int64_t row = -1;
-    if (!is_q) {
-        if (known) row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, h0);
-        if (row < 0) return;                             // a row's lanes leave together
-    }
+    if (position >= 0 && position < a.table_rows) row = kv_row_of_slot(a.slots[token], a.num_slots, a.per_page, a.kv.heads, h0);
+    if (row < 0) return;                                 // a row's lanes leave together
+    const void* const x = is_v ? a.v : a.k;
+    const int64_t from = token * (is_v ? a.ld_v : a.ld_k) + part * 16;
+    const bool interleaved = a.interleaved != 0;
     Angles turn[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         turn[i].partner = 0;
-        if (!is_v && known) turn[i].load(a, position, part * 16 + 8 * i);
+        if (!is_v) turn[i].load(a, position, part * 16 + 8 * i);
     }
-    for (int head = h0; head < h1; ++head, row += a.kv.page_size) {
-        const int64_t at = token * ld + (int64_t)head * a.kv.dim + part * 16;
-        float v[16];
+    for (int h = h0; h < h1; h += kRopeAhead / 2) {
+        Turned<XF32> c[kRopeAhead / 2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float own[8], other[8], y[8];
-            load8<XF32>(x, at + 8 * i, own);
-            if (turn[i].partner != 0) {
-                if (!a.interleaved) load8<XF32>(x, at + 8 * i + turn[i].partner, other);
-                turn[i].turn(a.interleaved != 0, own, other, y);
-            } else {
+        for (int u = 0; u < kRopeAhead / 2; ++u)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = own[j];
+            for (int i = 0; i < 2; ++i) c[u][i].load(x, from + (int64_t)min(h + u, h1 - 1) * a.kv.dim + 8 * i, turn[i], interleaved);
+#pragma unroll
+        for (int u = 0; u < kRopeAhead / 2; ++u) {
+            if (h + u >= h1) break;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float y[8];
+                c[u][i].values(turn[i], interleaved, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[8 * i + j] = y[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * i + j] = y[j];
-        }
-        if (!is_q) {
-            quantise_row16<BIAS>(a.kv, is_v, head, part, row, v, recip, rne);
-            continue;
-        }
-        // q_out may be q: every lane of the row has its values before one of them stores
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const int64_t to = token * a.ld_out + (int64_t)head * a.kv.dim + part * 16;
-        if (!known) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-        }
-        if (XF32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *(float4*)((float*)a.q_out + to + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *(uint4*)((uint16_t*)a.q_out + to + 8 * i) =
-                    make_uint4(Dec<0>::round2(v[8 * i], v[8 * i + 1]), Dec<0>::round2(v[8 * i + 2], v[8 * i + 3]),
-                               Dec<0>::round2(v[8 * i + 4], v[8 * i + 5]), Dec<0>::round2(v[8 * i + 6], v[8 * i + 7]));
+            quantise_row16<BIAS>(a.kv, is_v, h + u, part, row, v, recip, rne);
+            row += a.kv.page_size;
         }
     }
 }
@@ -377,7 +434,7 @@ hipError_t launch_kv_append_rope(int bias, bool x_f32, const KvRopeArgs& given, 
     // heads of a workgroup: as many as leave four workgroups a compute unit
     a.per = 1;
     while (a.per < 8 && runs * (2 * a.kv.heads + a.q_heads) / (2 * a.per) >= 1024) a.per *= 2;
-    const int units = 2 * ((a.kv.heads + a.per - 1) / a.per) + (a.q_heads + a.per - 1) / a.per;
+    const int units = 2 * ((a.kv.heads + a.per - 1) / a.per) + 2 * ((a.q_heads + a.per - 1) / a.per);
     const dim3 grid((uint32_t)runs, (uint32_t)units);
 #define FP4Q_ROPE(B)                                                                                    \
     do {                                                                                                \
