@@ -147,8 +147,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(KvAppendArgs a)
 // sum and difference rounded to binary32: value j and j + rot_dim / 2, or 2 j and 2 j + 1
 // (interleaved), with c and s at place j of the token's row of the tables.  rot_dim is a multiple
 // of 16, so a chunk of eight values lies in one half, or beyond; where its partners are
-// another chunk, the lane loads that one too (from the caches, where its own lane's
-// load brings it).
+// another chunk, the lane of q gets them from the lane that holds them, and a lane of K, whose two chunks
+// need not have theirs in one lane, loads that one too (from the caches, where its own lane's load
+// brings it).
 template <bool XF32>
 struct Chunk {
     uint4 w[XF32 ? 2 : 1];
@@ -158,6 +159,23 @@ struct Chunk {
         const uint4* const q = (const uint4*)((const char*)p + at * (XF32 ? 4 : 2));
         w[0] = q[0];
         if constexpr (XF32) w[1] = q[1];
+    }
+
+    __device__ __forceinline__ void load_nt(const void* p, int64_t at)
+    {
+        const uint4* const q = (const uint4*)((const char*)p + at * (XF32 ? 4 : 2));
+        w[0] = ld_nt16(q);
+        if constexpr (XF32) w[1] = ld_nt16(q + 1);
+    }
+
+    // The chunk that `lane` of the wave holds.
+    __device__ __forceinline__ Chunk of_lane(int lane) const
+    {
+        Chunk c;
+#pragma unroll
+        for (int i = 0; i < (XF32 ? 2 : 1); ++i)
+            c.w[i] = make_uint4(__shfl(w[i].x, lane, 64), __shfl(w[i].y, lane, 64), __shfl(w[i].z, lane, 64), __shfl(w[i].w, lane, 64));
+        return c;
     }
 
     __device__ __forceinline__ void values(float (&v)[8]) const
@@ -253,7 +271,7 @@ __device__ __forceinline__ void turn_queries(const KvRopeArgs& a, int64_t token,
         Turned<XF32> x[kRopeAhead];
 #pragma unroll
         for (int u = 0; u < kRopeAhead; ++u)
-            x[u].load(a.q, token * a.ld_q + (int64_t)min(h + u, h1 - 1) * a.kv.dim + part * 8, turn, interleaved);
+            x[u].own.load_nt(a.q, token * a.ld_q + (int64_t)min(h + u, h1 - 1) * a.kv.dim + part * 8);
         // q_out may be q: every lane of the rows has its values before one of them stores
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -261,6 +279,7 @@ __device__ __forceinline__ void turn_queries(const KvRopeArgs& a, int64_t token,
         for (int u = 0; u < kRopeAhead; ++u) {
             if (h + u >= h1) break;
             float v[8];
+            if (!interleaved) x[u].other = x[u].own.of_lane(((int)threadIdx.x & 63) + turn.partner / 8);   // of the same row
             x[u].values(turn, interleaved, v);
             if (!known) {
 #pragma unroll
@@ -281,6 +300,9 @@ __device__ __forceinline__ void turn_queries(const KvRopeArgs& a, int64_t token,
 
 // A workgroup takes `per` heads of K, of V or of q (blockIdx.y; q in two halves of its tokens) for a run of tokens: a
 // lane keeps its angles for all of them.
+// 16001 tokens of 32 heads of q and 8 of K and V, head_dim 128 (MXFP4, half of a head turned, 345 MB): 61 us, 5.7 TB/s.  A head
+// at a time with sixteen values a lane took 92, four heads of q together 77; q read past the caches, which its
+// output then fills, gave the rest.
 template <int BIAS, bool XF32>
 __global__ __launch_bounds__(kThreads) void k_kv_append_rope(KvRopeArgs a)
 {
