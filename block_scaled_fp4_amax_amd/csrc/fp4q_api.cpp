@@ -1224,7 +1224,8 @@ int fp4_moe(const fp4q_cfg* cfg, const fp4q_moe* moe, void* workspace, size_t wo
         a.pair_token = (int32_t*)(ws + p.pair_token);
         a.pair_share = (float*)(ws + p.pair_share);
         a.mid = (uint16_t*)(ws + p.mid);
-        a.mid_rest = (uint16_t*)(ws + p.mid_rest);
+        a.mid_rest = a.mid + (int64_t)p.max_groups * p.group * o.inter;
+        a.mid32 = (float*)(ws + p.mid);
         a.parts = (float*)(ws + p.parts);
         a.few = p.few;
         a.group = p.group;

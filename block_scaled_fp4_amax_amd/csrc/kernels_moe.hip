@@ -9,7 +9,7 @@
 //                pairs in the order of the experts and their groups of up to 16 MT
 //                pairs of one expert;
 //   k_moe_up     a workgroup takes 32 gate and 32 up rows of W1 for one group; its waves share K
-//                and join through LDS; a times the activation goes to the scratch in bf16;
+//                and join through LDS; a times the activation goes to the scratch;
 //   k_moe_down   the same for 64 rows of W2; each pair's products go to the scratch in binary32;
 //   k_moe_join   adds a token's pairs in the order of its choices, so its result does not depend on
 //                which other tokens are there.  (W2's sums kept in LDS for all tokens, a workgroup
@@ -22,8 +22,9 @@
 // exactly, as the A operand and tokens as the B operand; a unit is 128 values of K, of which
 // lane l loads 32 (l / 16) .. + 31 of row l % 16.  Sums are binary32.
 //
-// Rounding.  a act is rounded to bf16 before W2, as an activation between two products is;
-// where the result is asked for in binary32 (FINE) it enters as two such terms, good to 2^-16.
+// Rounding.  a act enters W2 as two bf16 terms (good to 2^-16), which lie side by side in the
+// registers while a unit of W2 is decoded once for both; one term would add its 2^-8 to that of y.  A few tokens' a act
+// stays binary32.
 #include "fp4q_device.h"
 #include "launch.h"
 #include "lds_load.h"
@@ -274,12 +275,13 @@ struct Scales {
 };
 
 // A lane's part of a unit of the tokens, for each tile of them: of its column's token the eight values of
-// each 64 that its place in the products takes (multiply).
-template <int MT>
+// each 64 that its place in the products takes (multiply), as one or two bf16 terms.
+template <int MT, int TERMS>
 struct Tokens {
-    uint4 x[MT][2][2];
+    uint4 x[TERMS][MT][2][2];
 
-    __device__ __forceinline__ void load(rsrc_t r, const uint32_t (&off)[MT], int k, int end, int place)
+    // term i through descriptor r[i]
+    __device__ __forceinline__ void load(const rsrc_t (&r)[TERMS], const uint32_t (&off)[MT], int k, int end, int place)
     {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -287,10 +289,12 @@ struct Tokens {
             for (int h = 0; h < 2; ++h) {
                 const bool in = k + 64 * b + 16 * h + place < end;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, in ? off[m] : kOff, (k + 64 * b + 16 * h) * 2, 0);
-                    x[m][b][h] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < TERMS; ++i) {
+                        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r[i], in ? off[m] : kOff, (k + 64 * b + 16 * h) * 2, 0);
+                        x[i][m][b][h] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
             }
     }
 };
@@ -300,9 +304,9 @@ __device__ __forceinline__ int place_of(int quarter) { return 32 * (quarter & 1)
 
 // The two halves of a wave hold different 64 values of K (16-byte loads, whole 64-byte runs of a row),
 // and swap words so that a product's lanes hold the same 64, under one outer scale.
-template <int BIAS, int OUTER, int NT, int MT>
+template <int BIAS, int OUTER, int NT, int MT, int TERMS>
 __device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>::Unit& u, const uint32_t (&scale)[NT][2],
-                                         const Tokens<MT>& x, f32x4_t (&acc)[NT][MT])
+                                         const Tokens<MT, TERMS>& x, f32x4_t (&acc)[NT][MT])
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -329,8 +333,11 @@ __device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 f32x4_t p = OUTER == kInnerOnly ? acc[n][m] : f32x4_t{0, 0, 0, 0};
-                p = Dec<0>::mfma(w[0], x.x[m][d][0], p);
-                p = Dec<0>::mfma(w[1], x.x[m][d][1], p);
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) {
+                    p = Dec<0>::mfma(w[0], x.x[i][m][d][0], p);
+                    p = Dec<0>::mfma(w[1], x.x[i][m][d][1], p);
+                }
                 if constexpr (OUTER == kInnerOnly) {
                     acc[n][m] = p;
                 } else {
@@ -346,22 +353,22 @@ __device__ __forceinline__ void multiply(const typename Weights<BIAS, OUTER, NT>
 // them is; then scale rows are in LDS, those of tile n at rows + n * apart, from value k0 on.  The loop stays rolled: a
 // kernel of ten thousand bytes of code takes longer to fetch than a token's weights (W2 of one
 // token, 4 experts of 2880 x 2880, unrolled four times 16.6 us, rolled 9.9).
-template <int CHUNK, int BIAS, int OUTER, int NT, int MT, class Ready>
-__device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, rsrc_t x, const uint32_t (&off)[MT], int k, int end,
+template <int CHUNK, int BIAS, int OUTER, int NT, int MT, int TERMS, class Ready>
+__device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, const rsrc_t (&x)[TERMS], const uint32_t (&off)[MT], int k, int end,
                                        int stride, const lds_t* rows, int apart, int k0, int quarter, f32x4_t (&acc)[NT][MT],
                                        Ready ready)
 {
     using S = Scales<BIAS, CHUNK>;
     const int place = place_of(quarter);
     typename Weights<BIAS, OUTER, NT>::Unit u;
-    Tokens<MT> t;
+    Tokens<MT, TERMS> t;
     w.load(k, end, quarter, u);
     t.load(x, off, k, end, place);
     ready();
 #pragma unroll 1
     for (; k < end; k += stride) {
         typename Weights<BIAS, OUTER, NT>::Unit next;
-        Tokens<MT> then;
+        Tokens<MT, TERMS> then;
         w.load(k + stride, end, quarter, next);          // zeros beyond the end
         then.load(x, off, k + stride, end, place);
         uint32_t scale[NT][2];
@@ -369,7 +376,7 @@ __device__ __forceinline__ void stream(const Weights<BIAS, OUTER, NT>& w, rsrc_t
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int b = 0; b < 2; ++b) scale[n][b] = S::read(rows + n * apart, (k - k0) >> 7, b, quarter);
-        multiply<BIAS, OUTER, NT, MT>(u, scale, t, acc);
+        multiply<BIAS, OUTER, NT, MT, TERMS>(u, scale, t, acc);
         u = next;
         t = then;
     }
@@ -388,9 +395,9 @@ __device__ __forceinline__ float gated(const MoeArgs& a, float g, float u)
 // v)` gets the sums of tiles n and n + 2 for tile m of the tokens.
 constexpr int kWaves = 4, kChunk = 4096;                 // values of K whose scale bytes LDS holds
 
-template <int BIAS, int OUTER, int MT, class Finish>
-__device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, const int (&first)[4], int stride, int N, int K, const uint16_t* x,
-                                       const uint16_t* rest, const uint32_t (&off)[MT], Finish finish)
+template <int BIAS, int OUTER, int MT, int TERMS, class Finish>
+__device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, const int (&first)[4], int stride, int N, int K,
+                                       const uint16_t* const (&x)[TERMS], const uint32_t (&off)[MT], Finish finish)
 {
     using S = Scales<BIAS, kChunk>;
     constexpr int kJoin = kWaves * 16 * MT * 64 * 4, kScales = 64 * S::kStride;
@@ -413,11 +420,23 @@ __device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, cons
         const int end = min(K, k0 + kChunk);
         if (k0) __syncthreads();                         // everybody is done with the chunk before
         S::template stage<16>(sr, stride * (K / S::B), k0 / S::B, (end - k0) / S::B, lds + 16 * wave * S::kStride, lane);
-        stream<kChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(x), off, k0 + wave * 128, end, kWaves * 128, lds + col * S::kStride,
-                                           16 * S::kStride, k0, quarter, acc, [] { lds_barrier(); });
-        if (rest)
-            stream<kChunk, BIAS, OUTER, 4, MT>(w, make_rsrc(rest), off, k0 + wave * 128, end, kWaves * 128, lds + col * S::kStride,
-                                               16 * S::kStride, k0, quarter, acc, [] {});
+        const lds_t* const rows = lds + col * S::kStride;
+        const auto go = [&](const auto& terms, auto ready) {
+            stream<kChunk, BIAS, OUTER, 4, MT>(w, terms, off, k0 + wave * 128, end, kWaves * 128, rows, 16 * S::kStride, k0, quarter,
+                                               acc, ready);
+        };
+        const auto scales_in = [] { lds_barrier(); };
+        if constexpr (TERMS == 2 && MT > 1) {
+            // two terms of more than one tile of tokens have no room in the registers beside the next unit's
+            const rsrc_t first_term[1] = {make_rsrc(x[0])}, second[1] = {make_rsrc(x[1])};
+            go(first_term, scales_in);
+            go(second, [] {});
+        } else {
+            rsrc_t terms[TERMS];
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i) terms[i] = make_rsrc(x[i]);
+            go(terms, scales_in);
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -445,7 +464,7 @@ __device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, cons
 }
 
 // 32 gate rows and the same 32 up rows of W1.
-template <int BIAS, int OUTER, int MT, bool FINE>
+template <int BIAS, int OUTER, int MT>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
 {
     const MoeGroup group = a.groups[blockIdx.y];
@@ -461,7 +480,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
         const int token = a.pair_token[first_pair + 16 * m + col];   // -1: none
         off[m] = token >= 0 ? (uint32_t)token * (uint32_t)(a.ld_x * 2) + place_of(quarter) * 2 : kOff;
     }
-    rows64<BIAS, OUTER, MT>(a.w1, group.expert, first, s, N, a.hidden, a.x, nullptr, off, [&](int n, int m, const float (&v)[8]) {
+    rows64<BIAS, OUTER, MT, 1>(a.w1, group.expert, first, s, N, a.hidden, {a.x}, off, [&](int n, int m, const float (&v)[8]) {
         if (16 * m + col >= group.count) return;
         const int pair = first_pair + 16 * m + col, i = i0 + 16 * n + 4 * quarter;
         const float share = a.pair_share[pair];
@@ -475,14 +494,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
         }
         const uint2 hi = make_uint2(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]));
         *(uint2*)(a.mid + (int64_t)pair * a.inter + i) = hi;
-        if constexpr (FINE)
-            *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
-                make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
+        *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
+            make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
     });
 }
 
 // 64 rows of W2, as many as there are in the last workgroup.
-template <int BIAS, int OUTER, int MT, bool FINE>
+template <int BIAS, int OUTER, int MT>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeArgs a)
 {
     const MoeGroup group = a.groups[blockIdx.y];
@@ -494,7 +512,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeArgs a)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
         off[m] = 16 * m + col < group.count ? (uint32_t)(first_pair + 16 * m + col) * (uint32_t)(a.inter * 2) + place_of(quarter) * 2 : kOff;
-    rows64<BIAS, OUTER, MT>(a.w2, group.expert, first, 1, a.hidden, a.inter, a.mid, FINE ? a.mid_rest : nullptr, off,
+    rows64<BIAS, OUTER, MT, 2>(a.w2, group.expert, first, 1, a.hidden, a.inter, {a.mid, a.mid_rest}, off,
                             [&](int n, int m, const float (&v)[8]) {
         if (16 * m + col >= group.count) return;
         float* const to = a.parts + (int64_t)(first_pair + 16 * m + col) * a.hidden + n0 + 16 * n + 4 * quarter;
@@ -538,20 +556,21 @@ constexpr int kFewWaves = 4;
 
 // One pass of a lane over R rows: codes, scale bytes, outer scales; and the token's values.  Each RUN of
 // the rows lies in one tile of 64.
-template <int BIAS, int OUTER, int R, int RUN>
+template <int BIAS, int OUTER, int R, int RUN, bool X32>
 struct Pass {
     static constexpr int B = Dec<BIAS>::kBlock;
     uint2 c[R];
     uint32_t s[R];
     float o[OUTER == kPerTile ? R / RUN : OUTER == kPerRow ? R : 1];
-    uint4 x[2];
+    uint4 x[X32 ? 4 : 2];
 
     // rows: the rows' numbers in W; x: the token's values; k: the lane's first value, from `K` on zeros
-    __device__ __forceinline__ void load(const MoeWeight& w, const int64_t (&rows)[R], const uint16_t* token, int k, int K)
+    __device__ __forceinline__ void load(const MoeWeight& w, const int64_t (&rows)[R], const void* token, int k, int K)
     {
         const bool in = k < K;
-        x[0] = in ? ((const uint4*)(token + k))[0] : make_uint4(0, 0, 0, 0);
-        x[1] = in ? ((const uint4*)(token + k))[1] : make_uint4(0, 0, 0, 0);
+        const uint4* const from = (const uint4*)((const char*)token + k * (X32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < (X32 ? 4 : 2); ++i) x[i] = in ? from[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             c[r] = in ? *(const uint2*)(w.codes + rows[r] * (K / 2) + k / 2) : make_uint2(0, 0);
@@ -565,9 +584,15 @@ struct Pass {
     __device__ __forceinline__ void add(float whole, float (&acc)[R]) const
     {
         float v[16];
-        const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+        for (int i = 0; i < (X32 ? 4 : 2); ++i) {
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (X32) v[4 * i + j] = __uint_as_float(u[j]);
+                else v[8 * i + 2 * j] = bf16_lo(u[j]), v[8 * i + 2 * j + 1] = bf16_hi(u[j]);
+            }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float sum = 0.0f;
@@ -605,11 +630,11 @@ __device__ __forceinline__ void passes(int steps, Load load, Add add)
     }
 }
 
-template <int BIAS, int OUTER, int PER, bool FINE>
+template <int BIAS, int OUTER, int PER>
 __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_up(MoeArgs a)
 {
     constexpr int R = 2 * kFewUpRows;
-    using P = Pass<BIAS, OUTER, R, kFewUpRows>;
+    using P = Pass<BIAS, OUTER, R, kFewUpRows, false>;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int pair = (int)blockIdx.y, t = pair / a.top_k, slot = pair - t * a.top_k;
     const int i0 = ((int)blockIdx.x * kFewWaves + wave) * kFewUpRows, K = a.hidden, N = 2 * a.inter;
@@ -642,18 +667,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_up(MoeArgs a)
     }
     if (lane >= kFewUpRows) return;
     const float y = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.share), slot)) * gated(a, g + bg, u + bu);
-    const uint32_t hi = Dec<0>::round2(y, 0.0f);
-    a.mid[(int64_t)pair * a.inter + i] = (uint16_t)hi;
-    if constexpr (FINE) a.mid_rest[(int64_t)pair * a.inter + i] = (uint16_t)Dec<0>::rest2(y, 0.0f, hi);
+    a.mid32[(int64_t)pair * a.inter + i] = y;
 }
 
 // The waves of a workgroup take the passes of all of its token's experts over the same rows in turn, and join through
 // LDS in order.
-template <int BIAS, int OUTER, int PER, bool FINE>
+template <int BIAS, int OUTER, int PER>
 __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
 {
     constexpr int R = kFewDownRows;
-    using P = Pass<BIAS, OUTER, R, R>;
+    using P = Pass<BIAS, OUTER, R, R, true>;
     __shared__ float join[kFewWaves][R];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int t = (int)blockIdx.y, n0 = (int)blockIdx.x * R, K = a.inter;
@@ -676,19 +699,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
             int64_t rows[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) rows[r] = first + r;
-            p.load(a.w2, rows, a.mid + (int64_t)(t * a.top_k + s) * K, k, K);
+            p.load(a.w2, rows, a.mid32 + (int64_t)(t * a.top_k + s) * K, k, K);
         }, [&](int j, const P& p) {
             int s, k;
             place(j, s, k);
             const float whole = a.w2.outer_kind == kOuterTensor ? a.w2.outer[__builtin_amdgcn_readlane(mine.expert, s)] : 1.0f;
             p.add(whole, acc);
-            if constexpr (FINE) {                        // the activations' second terms
-                P rest = p;
-                const uint4* const x = (const uint4*)(a.mid_rest + (int64_t)(t * a.top_k + s) * K + k);
-                rest.x[0] = k < K ? x[0] : make_uint4(0, 0, 0, 0);
-                rest.x[1] = k < K ? x[1] : make_uint4(0, 0, 0, 0);
-                rest.add(whole, acc);
-            }
         });
     }
     float y = 0.0f;
@@ -713,44 +729,38 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
     else ((uint16_t*)a.y)[out] = (uint16_t)Dec<0>::round2(y, 0.0f);
 }
 
-template <int BIAS, int O1, int O2, int MT, bool FINE>
+template <int BIAS, int OUTER, int MT>
 hipError_t launch_products(const MoeArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_moe_up<BIAS, O1, MT, FINE>), dim3((uint32_t)(a.inter / 32), (uint32_t)a.max_groups),
+    hipLaunchKernelGGL((k_moe_up<BIAS, OUTER, MT>), dim3((uint32_t)(a.inter / 32), (uint32_t)a.max_groups),
                        dim3(64 * kWaves), 0, s, a);
-    hipLaunchKernelGGL((k_moe_down<BIAS, O2, MT, FINE>), dim3((uint32_t)((a.hidden + 63) / 64), (uint32_t)a.max_groups),
+    hipLaunchKernelGGL((k_moe_down<BIAS, OUTER, MT>), dim3((uint32_t)((a.hidden + 63) / 64), (uint32_t)a.max_groups),
                        dim3(64 * kWaves), 0, s, a);
     hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)(((int64_t)a.hidden / 4 * a.tokens + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
-template <int BIAS, int OUTER, int PER, bool FINE>
+template <int BIAS, int OUTER, int PER>
 hipError_t launch_few(const MoeArgs& a, hipStream_t s)
 {
     const int i = kFewWaves * kFewUpRows;
-    hipLaunchKernelGGL((k_moe_few_up<BIAS, OUTER, PER, FINE>), dim3((uint32_t)((a.inter + i - 1) / i), (uint32_t)(a.tokens * a.top_k)),
+    hipLaunchKernelGGL((k_moe_few_up<BIAS, OUTER, PER>), dim3((uint32_t)((a.inter + i - 1) / i), (uint32_t)(a.tokens * a.top_k)),
                        dim3(64 * kFewWaves), 0, s, a);
-    hipLaunchKernelGGL((k_moe_few_down<BIAS, OUTER, PER, FINE>), dim3((uint32_t)(a.hidden / kFewDownRows), (uint32_t)a.tokens),
+    hipLaunchKernelGGL((k_moe_few_down<BIAS, OUTER, PER>), dim3((uint32_t)(a.hidden / kFewDownRows), (uint32_t)a.tokens),
                        dim3(64 * kFewWaves), 0, s, a);
     return hipGetLastError();
-}
-
-template <int BIAS, int OUTER, bool FINE>
-hipError_t launch_tokens(const MoeArgs& a, hipStream_t s)
-{
-    if (a.few) return a.experts <= 64 ? launch_few<BIAS, OUTER, 1, FINE>(a, s) : launch_few<BIAS, OUTER, 8, FINE>(a, s);
-    if (a.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), dim3(1), dim3(kRouteThreads), 0, s, a);
-    else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
-    if (a.group == 16) return launch_products<BIAS, OUTER, OUTER, 1, FINE>(a, s);
-    if (a.group == 32) return launch_products<BIAS, OUTER, OUTER, 2, FINE>(a, s);
-    return launch_products<BIAS, OUTER, OUTER, 4, FINE>(a, s);
 }
 
 template <int BIAS, int OUTER>
 hipError_t launch_outer(const MoeArgs& a, hipStream_t s)
 {
-    return a.y_f32 ? launch_tokens<BIAS, OUTER, true>(a, s) : launch_tokens<BIAS, OUTER, false>(a, s);
+    if (a.few) return a.experts <= 64 ? launch_few<BIAS, OUTER, 1>(a, s) : launch_few<BIAS, OUTER, 8>(a, s);
+    if (a.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
+    if (a.group == 16) return launch_products<BIAS, OUTER, 1>(a, s);
+    if (a.group == 32) return launch_products<BIAS, OUTER, 2>(a, s);
+    return launch_products<BIAS, OUTER, 4>(a, s);
 }
 
 template <int BIAS>
@@ -789,8 +799,7 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     const int64_t places = (int64_t)p.max_groups * p.group;
     p.pair_token = take(places * 4);
     p.pair_share = take(places * 4);
-    p.mid = take(places * inter * 2);
-    p.mid_rest = take(places * inter * 2);
+    p.mid = take(places * inter * 4);
     p.parts = take(p.few ? 0 : places * hidden * 4);
     p.bytes = at;
     return p;

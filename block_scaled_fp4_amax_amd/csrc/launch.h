@@ -405,7 +405,8 @@ struct MoeArgs {
     int32_t* place;            // of the pair among the groups'
     int32_t* pair_token;       // [max_groups * group] by place, -1: none
     float* pair_share;
-    uint16_t *mid, *mid_rest;  // bf16 [max_groups * group, inter]: the activations, and what they leave
+    uint16_t *mid, *mid_rest;  // bf16 [max_groups * group, inter]: the activations, and what they leave; or
+    float* mid32;              // binary32 [tokens * top_k, inter]
     float* parts;              // FP32 [max_groups * group, hidden]: W2's products
     int32_t few;               // 1: k_moe_few_up and k_moe_few_down
     int32_t group, max_groups; // pairs of a group at most, groups at most
@@ -413,7 +414,7 @@ struct MoeArgs {
 
 struct MoePlan {
     int32_t few, group, max_groups;
-    size_t groups, expert, share, place, pair_token, pair_share, mid, mid_rest, parts, bytes;
+    size_t groups, expert, share, place, pair_token, pair_share, mid, parts, bytes;
 };
 
 MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);

@@ -635,8 +635,7 @@ typedef struct {
  *            rows, codes 16-byte aligned, NVFP4's and AMD-FP4's scale bytes 2.  Outer scales: none, 2D of 64, 1D of a multiple of 64 (as in
  *            fp4_linear), or TENSORWISE with one FP32 scale for each expert ([experts]).
  * Each expert is read once for the tokens that it takes, 64 of the call's at a time.
- * W enters the products exactly, sums are binary32.  a_te act is rounded to bf16 before W2 (a
- * relative 2^-8); with FP32 y it enters as two such terms (2^-16).  Sums are joined in an order that the call's sizes
+ * W enters the products exactly, sums are binary32, and a_te act enters W2 with a relative 2^-16 or less.  Sums are joined in an order that the call's sizes
  * and the token's own choices give: equal calls give equal bits.
  * workspace: fp4q_moe_workspace_bytes() bytes, 16-byte aligned; no initial value, nothing kept.
  * Needs hidden % 32 == 0 and inter % 32 == 0, 1 <= top_k <= experts (FP4Q_ERR_SHAPE); tokens <= 1024, experts <= 512,
