@@ -826,10 +826,10 @@ int fp4_kv_append_rope(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp
     if (o.q && o.q == o.q_out && o.tokens > 1 && o.ld_q != o.ld_q_out) return FP4Q_ERR_SHAPE;
     if (o.tokens > kMaxKvRows || o.ld_k > ((int64_t)1 << 31) || o.ld_v > ((int64_t)1 << 31) || o.table_rows > ((int64_t)1 << 31))
         return FP4Q_ERR_UNSUPPORTED;
-    if (has_q && (o.ld_q > ((int64_t)1 << 31) || o.ld_q_out > ((int64_t)1 << 31) || o.q_heads > 65535))
+    if (has_q && (o.ld_q > ((int64_t)1 << 31) || o.ld_q_out > ((int64_t)1 << 31)))
         return FP4Q_ERR_UNSUPPORTED;
-    // units of heads are the launch's second dimension
-    if (2 * (int64_t)a.kv.heads + (has_q ? o.q_heads : 0) > 65535) return FP4Q_ERR_UNSUPPORTED;
+    // units of heads, two for each of them at most, are the launch's second dimension
+    if (2 * ((int64_t)a.kv.heads + (has_q ? o.q_heads : 0)) > 65535) return FP4Q_ERR_UNSUPPORTED;
     if (o.tokens == 0 || (a.kv.num_pages == 0 && !has_q)) return FP4Q_OK;
     if (!o.k || !o.v || !o.slots || !o.positions || (has_q && (!o.q || !o.q_out)) || (o.table_rows > 0 && (!o.cos || !o.sin)))
         return FP4Q_ERR_NULL;
@@ -1047,7 +1047,8 @@ bool is_dtype(int32_t d) { return d == FP4Q_DTYPE_BF16 || d == FP4Q_DTYPE_FP32; 
 int check_norm(int64_t rows, int64_t hidden)
 {
     if (rows < 0 || hidden < 8 || hidden % 8) return FP4Q_ERR_SHAPE;
-    if (hidden > 16384 || rows > ((int64_t)1 << 31) || rows * (hidden / 8) >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
+    // a row takes a wave at least, and a launch has fewer than 2^32 lanes
+    if (hidden > 16384 || rows >= ((int64_t)1 << 26) || rows * (hidden / 8) >= (int64_t)1 << 31) return FP4Q_ERR_UNSUPPORTED;
     return FP4Q_OK;
 }
 

@@ -506,7 +506,7 @@ typedef struct {
  * A position outside the tables marks padding: nothing of the token is written to the
  * cache, and its row of q_out is zeros.  Everything else (slots, padding, NaN and
  * infinities, alignments, limits) as in fp4_kv_append; q and q_out 16-byte aligned with pitches of
- * a whole number of 16 bytes (ignored for one token), q_heads <= 65535 (FP4Q_ERR_UNSUPPORTED).
+ * a whole number of 16 bytes (ignored for one token), kv_heads + q_heads <= 32767 (FP4Q_ERR_UNSUPPORTED).
  */
 int fp4_kv_append_rope(const fp4q_cfg* cfg, const fp4q_kv_cache* cache, const fp4q_kv_rope* rope, void* stream);
 
@@ -679,7 +679,7 @@ typedef struct {
  *   fp8_mode 2  amax / 448 for a row, in binary32, and the quotients rounded to binary32 first;
  * amax over the finite values of y before it is rounded to y_dtype.  Results do not depend on how
  * rows are shared among lanes, so equal rows give equal bits in every call.
- * Needs hidden % 8 == 0 (FP4Q_ERR_SHAPE), hidden <= 16384 and rows < 2^31 / (hidden / 8)
+ * Needs hidden % 8 == 0 (FP4Q_ERR_SHAPE), hidden <= 16384, rows < 2^26 and rows < 2^31 / (hidden / 8)
  * (FP4Q_ERR_UNSUPPORTED), all buffers but rstd and fp8_scales 16-byte aligned.
  */
 int fp4_add_rms_norm(const fp4q_add_rms_norm* norm, void* stream);

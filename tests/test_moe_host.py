@@ -70,3 +70,9 @@ def test_binding_refusals():
                           (dict(b1=z(8, 64, dtype=torch.float32)), "b1"), (dict(b2=z(8, 128, dtype=torch.bfloat16)), "b2")):
         with pytest.raises((ValueError, fq.Fp4Error), match=error):
             fq.fp4_moe(**{**good, **change})
+
+
+@pytest.mark.parametrize("experts,top_k", [(1, 1), (3, 1), (3, 3), (8, 2), (8, 4), (32, 4), (40, 5), (128, 8), (512, 32)])
+def test_a_workspace_of_more_tokens_serves_fewer(experts, top_k):
+    need = [fq.fp4q_moe_workspace_bytes(t, experts, top_k, 2880, 736) for t in range(0, 260)]
+    assert need[0] == 0 and all(a <= b for a, b in zip(need, need[1:]))

@@ -40,7 +40,8 @@ def rope(cfg=None, cache=None, **kw):
     (dict(rot_dim=80), fq.ERR_SHAPE), (dict(rot_dim=-16), fq.ERR_SHAPE), (dict(q_heads=0), fq.ERR_SHAPE),
     (dict(q_out=FAKE, ld_q_out=264), fq.ERR_SHAPE), (dict(interleaved=2), fq.ERR_MODE), (dict(tokens=1 << 28), fq.ERR_UNSUPPORTED),
     (dict(q_heads=65536, ld_q=1 << 23, ld_q_out=1 << 23), fq.ERR_UNSUPPORTED), (dict(table_rows=1 << 32), fq.ERR_UNSUPPORTED),
-    (dict(q_heads=65532, ld_q=1 << 23, ld_q_out=1 << 23), fq.ERR_UNSUPPORTED)])
+    (dict(q_heads=65532, ld_q=1 << 23, ld_q_out=1 << 23), fq.ERR_UNSUPPORTED),
+    (dict(q_heads=32766, ld_q=1 << 23, ld_q_out=1 << 23), fq.ERR_UNSUPPORTED)])   # with kv_heads, 2^15
 def test_rope_refusals(kw, st):
     assert rope(**kw) == st
 
@@ -74,7 +75,7 @@ def norm(**kw):
     (dict(rows=1 << 28), fq.ERR_UNSUPPORTED), (dict(rows=1 << 40), fq.ERR_UNSUPPORTED), (dict(x_dtype=1), fq.ERR_DTYPE),
     (dict(residual_dtype=3), fq.ERR_DTYPE), (dict(weight_dtype=-1), fq.ERR_DTYPE), (dict(y_dtype=1), fq.ERR_DTYPE),
     (dict(fp8_mode=3), fq.ERR_MODE), (dict(fp8_mode=-1), fq.ERR_MODE), (dict(eps=-1e-5), fq.ERR_MODE), (dict(eps=float("nan")), fq.ERR_MODE),
-    (dict(rows=0, x=None), fq.OK)])
+    (dict(rows=1 << 26), fq.ERR_UNSUPPORTED), (dict(rows=1 << 26, hidden=32), fq.ERR_UNSUPPORTED), (dict(rows=0, x=None), fq.OK)])
 def test_norm_refusals(kw, st):
     assert norm(**kw) == st
 
@@ -95,7 +96,7 @@ def grad(ws=FAKE, wsb=1 << 30, **kw):
     (dict(ld_dy=8), fq.ERR_SHAPE), (dict(ld_h=8), fq.ERR_SHAPE), (dict(ld_dresidual=8), fq.ERR_SHAPE), (dict(hidden=12), fq.ERR_SHAPE),
     (dict(rows=-2), fq.ERR_SHAPE), (dict(dy_dtype=1), fq.ERR_DTYPE), (dict(h_dtype=5), fq.ERR_DTYPE),
     (dict(ws=None), fq.ERR_WORKSPACE), (dict(wsb=16), fq.ERR_WORKSPACE), (dict(ws=MIS), fq.ERR_ALIGN),
-    (dict(rows=0, dweight=None, weight=None), fq.OK)])
+    (dict(rows=1 << 26), fq.ERR_UNSUPPORTED), (dict(rows=0, dweight=None, weight=None), fq.OK)])
 def test_norm_gradient_refusals(kw, st):
     assert grad(**kw) == st
 
