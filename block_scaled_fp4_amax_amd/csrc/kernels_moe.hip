@@ -14,8 +14,12 @@
 //   k_moe_join   adds a token's pairs in the order of its choices, so its result does not depend on
 //                which other tokens are there.  (W2's sums kept in LDS for all tokens, a workgroup
 //                going through all groups with no scratch, took 58 us for 48 tokens of 32 experts of
-//                2880 x 2880 where k_moe_down and k_moe_join take 44: parts of K a wave end at
-//                every group.)
+//                2880 x 2880 where k_moe_down and k_moe_join took 44, with activations of one bf16
+//                term: parts of K a wave end at every group.)
+// 48 tokens, 4 of 32 experts of 2880 x 2880 each (MXFP4, 423 MB of weights): 8 + 73 + 45 + 7 us, k_moe_up 3.9 TB/s.  Bound:
+// loads in flight.  A wave holds a unit of 64 bytes of 64 rows and the next one; four waves a SIMD instead of three
+// spill the second (81 us), loads past the caches fetch lines twice (85: two waves share each line), two units
+// of a line by one wave 76.
 // Up to kMoeFewPairs pairs take two launches instead, rows of W as they lie (below).
 //
 // Products as in kernels_linear.hip: v_mfma_f32_16x16x32_bf16 with rows of W decoded to bf16,
@@ -551,6 +555,9 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 // values in binary32: G[m] x is exact, each block of 16 is summed and its scales (inner times outer) multiply the
 // sum.  No product is wasted on tokens that are not there, a row is read in whole lines, and waves need neither
 // LDS nor a launch to join.  Each wave finds its token's experts itself.
+// One token, 4 of 32 experts of 2880 x 2880 (NVFP4, 2D outer scales, 56 MB): 14 + 11 us, where groups take 35 in all.
+// Bound: the trips one after another (logits, weights, the second launch, its logits, weights), about 7 us of each
+// launch, then memory.
 constexpr int kFewUpRows = 4, kFewDownRows = 8;          // of a wave: gate and up rows each, rows of W2
 constexpr int kFewWaves = 4;
 

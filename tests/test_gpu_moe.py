@@ -223,13 +223,14 @@ def test_more_tokens_than_a_launch_takes(T):
         assert torch.equal(y[at:at + 64], layer.run(x[at:at + 64], l[at:at + 64], 2))
 
 
-def test_infinities_and_nan_stay_with_their_tokens():
+@pytest.mark.parametrize("T", [12, 20])
+def test_infinities_and_nan_stay_with_their_tokens(T):
     rng = np.random.default_rng(3)
     layer = Layer("mxfp4", "none", 4, 96, 64)
-    x, l = tokens(rng, 20, 96), logits_of(rng, 20, 4)
+    x, l = tokens(rng, T, 96), logits_of(rng, T, 4)
     x[3, 5], x[11, 95] = float("inf"), float("nan")
     y = layer.run(x, l, 2).isnan().cpu().numpy()
-    others = np.ones(20, bool)
+    others = np.ones(T, bool)
     others[[3, 11]] = False
     assert y[11].all() and not y[others].any()
 
@@ -263,12 +264,13 @@ def test_views_given_outputs_and_workspace():
     assert layer.run(x[:0], l[:0], 2).shape == (0, 96)
 
 
-def test_replays_and_other_streams():
+@pytest.mark.parametrize("T", [1, 8, 12])
+def test_replays_and_other_streams(T):
     rng = np.random.default_rng(6)
     layer = Layer("nvfp4", "2d", 8, 256, 192)
-    x, l = tokens(rng, 12, 256).cuda(), d(logits_of(rng, 12, 8))
-    y = torch.empty(12, 256, dtype=torch.bfloat16, device="cuda")
-    ws = fq.fp4_moe_workspace(12, 8, 3, 256, 192)
+    x, l = tokens(rng, T, 256).cuda(), d(logits_of(rng, T, 8))
+    y = torch.empty(T, 256, dtype=torch.bfloat16, device="cuda")
+    ws = fq.fp4_moe_workspace(T, 8, 3, 256, 192)
     call = lambda **kw: fq.fp4_moe(x, l, layer.w1, layer.w2, layer.cfg, top_k=3, **kw)  # noqa: E731
     call(y=y, workspace=ws)
     torch.cuda.synchronize()
@@ -277,7 +279,7 @@ def test_replays_and_other_streams():
         call(y=y, workspace=ws)
     side = torch.cuda.Stream()
     for _ in range(4):
-        l.copy_(d(logits_of(rng, 12, 8)))
+        l.copy_(d(logits_of(rng, T, 8)))
         x.mul_(0.75)
         torch.cuda.synchronize()
         g.replay()
