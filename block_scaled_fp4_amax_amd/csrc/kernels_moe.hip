@@ -71,18 +71,25 @@ struct Choice {
     float share;
 };
 
-// The experts of a token and their shares, slot s in lane s.  PER: experts of a lane, expert j 64 + lane in place j.
+// A token's logits.  PER: experts of a lane, expert j 64 + lane in place j.
 template <int PER>
-__device__ __forceinline__ Choice choose(const MoeArgs& a, int t, int lane)
+__device__ __forceinline__ void load_logits(const MoeArgs& a, int t, int lane, float (&l)[PER])
 {
-    float l[PER];
-    uint32_t key[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = j * 64 + lane;
-        l[j] = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
-        key[j] = order_key(l[j]);
+        l[j] = e < a.experts && t < a.tokens ? a.logits[(int64_t)t * a.experts + e] : -__builtin_inff();
     }
+}
+
+// The experts of a token and their shares, slot s in lane s.
+template <int PER>
+__device__ __forceinline__ Choice choose(const MoeArgs& a, const float (&l)[PER])
+{
+    const int lane = (int)threadIdx.x & 63;
+    uint32_t key[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = order_key(l[j]);
     float top = 0.0f, mine = 0.0f;
     int chosen = -1;
 #pragma unroll 1
@@ -125,14 +132,23 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
 {
     __shared__ uint32_t member[PER * 64][kMoeMaxTokens / 32];
     __shared__ int first_group[PER * 64];
+    __shared__ Choice chosen[kMoeMaxTokens * kMoeMaxTopK];
+    constexpr int kTurns = kMoeMaxTokens * 64 / kRouteThreads;   // tokens of a wave
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    float l[kTurns][PER];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) load_logits<PER>(a, wave + i * (kRouteThreads / 64), lane, l[i]);
     for (int i = (int)threadIdx.x; i < PER * 64 * (kMoeMaxTokens / 32); i += kRouteThreads) (&member[0][0])[i] = 0;
     // places of the groups that no pair takes
     for (int i = (int)threadIdx.x; i < a.max_groups * a.group; i += kRouteThreads) a.pair_token[i] = -1;
     __syncthreads();
-    for (int t = wave; t < a.tokens; t += kRouteThreads / 64) {
-        const Choice c = choose<PER>(a, t, lane);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int t = wave + i * (kRouteThreads / 64);
+        if (t >= a.tokens) break;
+        const Choice c = choose<PER>(a, l[i]);
         if (lane < a.top_k) {
+            chosen[t * a.top_k + lane] = c;
             a.expert[t * a.top_k + lane] = c.expert;
             a.share[t * a.top_k + lane] = c.share;
             if (c.expert >= 0) atomicOr(&member[c.expert][t >> 5], 1u << (t & 31));
@@ -166,13 +182,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeArgs a)
     }
     __syncthreads();
     for (int p = (int)threadIdx.x; p < a.tokens * a.top_k; p += kRouteThreads) {
-        const int e = a.expert[p], t = p / a.top_k;      // written by this workgroup before the barriers
-        if (e < 0) continue;
+        const Choice c = chosen[p];
+        const int e = c.expert, t = p / a.top_k;
+        if (e < 0) {
+            a.place[p] = -1;
+            continue;
+        }
         int rank = __popc(member[e][t >> 5] & ((1u << (t & 31)) - 1));
         for (int w = 0; w < t >> 5; ++w) rank += __popc(member[e][w]);
         const int at = first_group[e] * a.group + rank;  // an expert's groups follow one another
         a.pair_token[at] = t;
-        a.pair_share[at] = a.share[p];
+        a.pair_share[at] = c.share;
         a.place[p] = at;
     }
 }
@@ -525,22 +545,31 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(MoeArgs a)
     });
 }
 
-// A token's sums over its experts in the order of its choices: four values of a row a lane.
+// A token's sums over its experts in the order of its choices: four values of a row a lane, four experts' on their
+// way together.
 __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 {
-    const int quads = a.hidden / 4, at = (int)blockIdx.x * 256 + (int)threadIdx.x;
-    if (at >= quads * a.tokens) return;
-    const int t = at / quads, n = (at - t * quads) * 4;
+    const int n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4, t = (int)blockIdx.y;
+    if (n >= a.hidden) return;
     f32x4_t v = {0, 0, 0, 0};
-    for (int s = 0; s < a.top_k; ++s) {
-        const int e = a.expert[t * a.top_k + s];
-        if (e < 0) break;
-        v += *(const f32x4_t*)(a.parts + (int64_t)a.place[t * a.top_k + s] * a.hidden + n);
-        if (!a.b2) continue;
-        const float share = a.share[t * a.top_k + s];
-        const float* b = a.b2 + (int64_t)e * a.hidden + n;
+    for (int s = 0; s < a.top_k; s += 4) {
+        int place[4];
+        f32x4_t part[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(share, b[i], v[i]);
+        for (int i = 0; i < 4; ++i) place[i] = s + i < a.top_k ? a.place[t * a.top_k + s + i] : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            part[i] = place[i] >= 0 ? *(const f32x4_t*)(a.parts + (int64_t)place[i] * a.hidden + n) : f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (place[i] < 0) break;                     // none from here on
+            v += part[i];
+            if (!a.b2) continue;
+            const float share = a.share[t * a.top_k + s + i];
+            const float* b = a.b2 + (int64_t)a.expert[t * a.top_k + s + i] * a.hidden + n;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(share, b[r], v[r]);
+        }
     }
     const int64_t to = (int64_t)t * a.ld_y + n;
 #pragma unroll
@@ -646,7 +675,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_up(MoeArgs a)
     const int pair = (int)blockIdx.y, t = pair / a.top_k, slot = pair - t * a.top_k;
     const int i0 = ((int)blockIdx.x * kFewWaves + wave) * kFewUpRows, K = a.hidden, N = 2 * a.inter;
     if (i0 >= a.inter) return;
-    const Choice mine = choose<PER>(a, t, lane);
+    float logits[PER];
+    load_logits<PER>(a, t, lane, logits);
+    const Choice mine = choose<PER>(a, logits);
     const int e = __builtin_amdgcn_readlane(mine.expert, slot);
     if (e < 0) return;
     int64_t rows[R];
@@ -687,7 +718,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
     __shared__ float join[kFewWaves][R];
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int t = (int)blockIdx.y, n0 = (int)blockIdx.x * R, K = a.inter;
-    const Choice mine = choose<PER>(a, t, lane);
+    float logits[PER];
+    load_logits<PER>(a, t, lane, logits);
+    const Choice mine = choose<PER>(a, logits);
     const int taken = __popcll(__ballot(mine.expert >= 0));   // slots 0 .. taken - 1
     const int of_slot = (K + 1023) / 1024, all = taken * of_slot;
     const int steps = wave < all ? (all - wave + kFewWaves - 1) / kFewWaves : 0;
@@ -743,7 +776,7 @@ hipError_t launch_products(const MoeArgs& a, hipStream_t s)
                        dim3(64 * kWaves), 0, s, a);
     hipLaunchKernelGGL((k_moe_down<BIAS, OUTER, MT>), dim3((uint32_t)((a.hidden + 63) / 64), (uint32_t)a.max_groups),
                        dim3(64 * kWaves), 0, s, a);
-    hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)(((int64_t)a.hidden / 4 * a.tokens + 255) / 256)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_moe_join, dim3((uint32_t)((a.hidden / 4 + 255) / 256), (uint32_t)a.tokens), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
