@@ -16,10 +16,10 @@
 //                going through all groups with no scratch, took 58 us for 48 tokens of 32 experts of
 //                2880 x 2880 where k_moe_down and k_moe_join took 44, with activations of one bf16
 //                term: parts of K a wave end at every group.)
-// 48 tokens, 4 of 32 experts of 2880 x 2880 each (MXFP4, 423 MB of weights): 8 + 73 + 45 + 7 us, k_moe_up 3.9 TB/s.  Bound:
+// 48 tokens, 4 of 32 experts of 2880 x 2880 each (MXFP4, 423 MB of weights): 7 + 73 + 45 + 5 us, k_moe_up 3.9 TB/s.  Bound:
 // loads in flight.  A wave holds a unit of 64 bytes of 64 rows and the next one; four waves a SIMD instead of three
 // spill the second (81 us), loads past the caches fetch lines twice (85: two waves share each line), two units
-// of a line by one wave 76.
+// of a line by one wave 76, 128 rows a workgroup 75.
 // Up to kMoeFewPairs pairs take two launches instead, rows of W as they lie (below).
 //
 // Products as in kernels_linear.hip: v_mfma_f32_16x16x32_bf16 with rows of W decoded to bf16,
