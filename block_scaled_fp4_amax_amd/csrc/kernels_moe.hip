@@ -487,6 +487,16 @@ __device__ __forceinline__ void rows64(const MoeWeight& weight, int expert, cons
     }
 }
 
+// y as a bf16 value and what it leaves: an infinity leaves nothing, and a number that would round to one is the
+// largest bf16 and the rest.
+__device__ __forceinline__ void two_terms(float y, float& hi, float& rest)
+{
+    constexpr float kMost = 3.38953139e38f;              // (2 - 2^-7) 2^127
+    const float near = bf16_lo(Dec<0>::round2(y, 0.0f)), size = fabsf(y);
+    hi = size > kMost && size < __builtin_inff() ? copysignf(kMost, y) : near;
+    rest = size == __builtin_inff() ? 0.0f : y - hi;
+}
+
 // 32 gate rows and the same 32 up rows of W1.
 template <int BIAS, int OUTER, int MT>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
@@ -516,10 +526,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_up(MoeArgs a)
             const float upper = v[4 + r] + (a.b1 ? a.b1[b + up] : 0.0f);
             y[r] = share * gated(a, gate, upper);
         }
-        const uint2 hi = make_uint2(Dec<0>::round2(y[0], y[1]), Dec<0>::round2(y[2], y[3]));
-        *(uint2*)(a.mid + (int64_t)pair * a.inter + i) = hi;
+        float hi[4], rest[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) two_terms(y[r], hi[r], rest[r]);
+        *(uint2*)(a.mid + (int64_t)pair * a.inter + i) = make_uint2(Dec<0>::round2(hi[0], hi[1]), Dec<0>::round2(hi[2], hi[3]));
         *(uint2*)(a.mid_rest + (int64_t)pair * a.inter + i) =
-            make_uint2(Dec<0>::rest2(y[0], y[1], hi.x), Dec<0>::rest2(y[2], y[3], hi.y));
+            make_uint2(Dec<0>::round2(rest[0], rest[1]), Dec<0>::round2(rest[2], rest[3]));
     });
 }
 

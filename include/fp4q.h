@@ -634,7 +634,8 @@ typedef struct {
  *   W1, W2   rowwise buffers as fp4_quantize or fp4_cast_transpose_grouped write them for the stacked
  *            rows, codes 16-byte aligned, NVFP4's and AMD-FP4's scale bytes 2.  Outer scales: none, 2D of 64, 1D of a multiple of 64 (as in
  *            fp4_linear), or TENSORWISE with one FP32 scale for each expert ([experts]).
- * Each expert is read once for the tokens that it takes, 64 of the call's at a time.
+ * Each expert is read once for the tokens that it takes, 64 of the call's at a time (calls of few tokens read it for
+ * each of them).
  * W enters the products exactly, sums are binary32, and a_te act enters W2 with a relative 2^-16 or less.  Sums are joined in an order that the call's sizes
  * and the token's own choices give: equal calls give equal bits.
  * workspace: fp4q_moe_workspace_bytes() bytes, 16-byte aligned; no initial value, nothing kept.

@@ -235,6 +235,46 @@ def test_infinities_and_nan_stay_with_their_tokens(T):
     assert y[11].all() and not y[others].any()
 
 
+@pytest.mark.parametrize("T", [3, 30])
+def test_an_infinite_activation_reaches_the_rows_that_weigh_it(T):
+    """An infinite bias of a gate makes one activation of one expert infinite: y is infinite where its weight
+    is not zero, with its sign, and NaN where it is."""
+    rng = np.random.default_rng(9)
+    layer = Layer("mxfp4", "none", 4, 96, 64, bias=True)
+    layer.b1[1, 7] = np.inf
+    x, l = tokens(rng, T, 96), logits_of(rng, T, 4)
+    l[0, 1], l[-1, 1] = 50.0, -50.0                      # the first token takes that expert, the last does not
+    y = layer.run(x, l, 2).double().cpu().numpy()
+    took = 0
+    for t in range(T):
+        if 1 not in [e for e, _, _ in layer.choices(l[t], 2, True)]:
+            assert np.isfinite(y[t]).all()
+            continue
+        took += 1
+        u = layer.v1[1][64 + 7] @ x[t].double().numpy() + layer.b1[1, 64 + 7]
+        want = layer.v2[1][:, 7] * u
+        assert np.array_equal(np.isnan(y[t]), want == 0) and (y[t][want > 0] == np.inf).all() and (y[t][want < 0] == -np.inf).all()
+    assert 0 < took < T
+
+
+def test_activations_beyond_the_largest_bf16():
+    """Activations of +-3.395e38, which round to infinity in bf16, weighed with 2^-6: y is finite."""
+    z = lambda *s: np.zeros(s, np.uint8)  # noqa: E731
+    E, H, I, T = 2, 32, 32, 40
+    c1, c2, s = z(E, 2 * I, H // 2), z(E, H, I // 2), np.full((E, 2 * I, 1), 127, np.uint8)
+    c2[:, :, 0] = 2                                      # the value 1 at place 0
+    w1, w2 = dict(codes=d(c1), scales=d(s), outer=None), dict(codes=d(c2), scales=d(np.full((E, H, 1), 121, np.uint8)), outer=None)
+    b1 = np.zeros((E, 2 * I), np.float32)
+    b1[:, 0], b1[0, I], b1[1, I] = 2.0 ** 64, np.float32(3.395e38) / 2.0 ** 64, -np.float32(3.395e38) / 2.0 ** 64
+    l = np.zeros((T, E), np.float32)
+    l[::2, 0] = l[1::2, 1] = 1.0
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    cfg = fq.make_cfg(format="mxfp4")
+    y = fq.fp4_moe(x, d(l), w1, w2, cfg, top_k=1, b1=d(b1), out_dtype=torch.float32).cpu().numpy()
+    want = np.where(np.arange(T) % 2 == 0, 1, -1)[:, None] * np.float64(np.float32(3.395e38)) * 2.0 ** -6
+    assert (np.abs(y - want) <= 2.0 ** -16 * np.abs(want)).all()
+
+
 def test_sizes_of_a_real_layer():
     rng = np.random.default_rng(4)
     for fmt, kind, T in (("nvfp4", "2d", 1), ("mxfp4", "none", 48), ("amdfp4", "1d192", 6)):
