@@ -61,7 +61,6 @@ constexpr int kWaves = 4;
 constexpr int kUnit = 128;                               // keys that a workgroup of few rows takes at once
 constexpr int kMinShare = 4;                             // units of a workgroup's share, at least
 constexpr int kFewRows = 32;
-constexpr int kMinRounds = 4;                            // rounds of a part of a tree's keys, at least
 constexpr int kStep = 32;                                // keys of a step
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.4028235e38f;                 // m of a row that has seen no key
@@ -867,8 +866,6 @@ __device__ __forceinline__ int share_of(int total, const AttnArgs& a)
     return max((total + parts - 1) / parts, kMinShare);
 }
 
-__device__ __forceinline__ int parts_of(int units, int share) { return (units + share - 1) / share; }
-
 template <int D, int BIAS, int QT, bool FINE, bool TREE>
 __global__ __launch_bounds__(64 * kWaves, QT == 1 && D == 64 ? 4 : D == 256 && QT == 2 ? 1 : 2) void k_attn_few(AttnArgs a)
 {
@@ -1194,24 +1191,21 @@ __device__ __forceinline__ TreeSeq tree_seq(const AttnArgs& a, int b)
     if (b >= a.batch) return TreeSeq{0, 0};
     const QueryRange qr = queries_of(a, b);
     const int kv = kv_length(a.kv_lens[b], a.max_kv, a.table_cols, a.kv.page_size, a.kv.num_pages);
-    const int lo = tree_context(kv, qr.count, a.window, 0).lo / kv_round(D) * kv_round(D);
-    return TreeSeq{max(1, (kv - lo + kv_round(D) - 1) / kv_round(D)), (qr.count * a.group + kTileRows - 1) / kTileRows};
+    return TreeSeq{tree_rounds(kv, qr.count, a.window, kv_round(D)), tile_count(qr.count * a.group)};
 }
 
-// Rounds of a part: with `slots` workgroups at once and half a part lost a tile.
+// tree_share of all sequences (first: of the first 64).
 template <int D>
-__device__ __forceinline__ int tree_share(const AttnArgs& a, const TreeSeq& first, int lane)
+__device__ __forceinline__ int share_of_trees(const AttnArgs& a, const TreeSeq& first, int lane)
 {
-    int total = __builtin_amdgcn_readlane(lane_sums(first.units * first.tiles), 63);
-    int items = __builtin_amdgcn_readlane(lane_sums(first.tiles), 63);
+    int rounds = __builtin_amdgcn_readlane(lane_sums(first.units * first.tiles), 63);
+    int tiles = __builtin_amdgcn_readlane(lane_sums(first.tiles), 63);
     for (int b = 64; b < a.batch; b += 64) {
         const TreeSeq s = tree_seq<D>(a, b + lane);
-        total += __builtin_amdgcn_readlane(lane_sums(s.units * s.tiles), 63);
-        items += __builtin_amdgcn_readlane(lane_sums(s.tiles), 63);
+        rounds += __builtin_amdgcn_readlane(lane_sums(s.units * s.tiles), 63);
+        tiles += __builtin_amdgcn_readlane(lane_sums(s.tiles), 63);
     }
-    const int per_head = max(1, a.slots / a.kv.heads);
-    const int parts = max(per_head - items / 2, (per_head + 3) / 4);
-    return max((total + parts - 1) / parts, kMinRounds);
+    return tree_share(rounds, tiles, a.slots, a.kv.heads);
 }
 
 struct TreePlace {
@@ -1220,16 +1214,12 @@ struct TreePlace {
     int tiles;
 };
 
-// Workgroup `place` of a head: the parts of sequence after sequence, tiles side by side in each.
+// Workgroup `place` of a head where keys are cut: the parts of sequence after sequence, tiles side by side in each.
 template <int D>
 __device__ __forceinline__ TreePlace tree_place(const AttnArgs& a, int place, int lane)
 {
-    if (a.slots == 0) {                                  // one workgroup a tile
-        const int tiles = (a.max_q * a.group + kTileRows - 1) / kTileRows;
-        return TreePlace{place / tiles, place % tiles, 0, 1, 0, tiles};
-    }
     TreeSeq mine = tree_seq<D>(a, lane);
-    const int share = tree_share<D>(a, mine, lane);
+    const int share = share_of_trees<D>(a, mine, lane);
     int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         if (b0) mine = tree_seq<D>(a, b0 + lane);
@@ -1260,7 +1250,7 @@ __global__ __launch_bounds__(256) void k_attn_tree_join(AttnArgs a, float unshif
     const int rows = qr.count * a.group;
     if ((int)blockIdx.x * 16 >= rows) return;
     TreeSeq mine = tree_seq<D>(a, lane);
-    const int share = tree_share<D>(a, mine, lane);
+    const int share = share_of_trees<D>(a, mine, lane);
     int first = 0;                                       // parts of a head before this sequence's
     for (int b0 = 0; b0 + 64 <= seq; b0 += 64) {
         first += __builtin_amdgcn_readlane(lane_sums(mine.tiles ? parts_of(mine.units, share) * mine.tiles : 0), 63);
@@ -1340,10 +1330,14 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int head, b, split, block, parts = 1;
     if constexpr (TREE) {
-        head = (int)blockIdx.x % a.kv.heads;
-        const TreePlace p = tree_place<D>(a, (int)blockIdx.x / a.kv.heads, lane);
-        if (p.parts == 0) return;
-        b = p.seq, block = p.tile, split = p.part, parts = p.parts;
+        if (a.slots == 0) {                              // one workgroup a tile
+            head = (int)blockIdx.x, block = (int)blockIdx.y, b = (int)blockIdx.z, split = 0;
+        } else {
+            head = (int)blockIdx.x % a.kv.heads;
+            const TreePlace p = tree_place<D>(a, (int)blockIdx.x / a.kv.heads, lane);
+            if (p.parts == 0) return;
+            b = p.seq, block = p.tile, split = p.part, parts = p.parts;
+        }
     } else {
         head = (int)blockIdx.x;
         b = (int)blockIdx.z % a.batch, split = (int)blockIdx.z / a.batch;
@@ -1516,7 +1510,8 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
         AttnArgs t = a;
         t.part_o = a.few_o;
         t.part_ml = a.few_ml;
-        hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), dim3((uint32_t)a.groups), dim3(64 * T::kWaves), T::kLds, s, t);
+        const TreeGrid g = tree_grid(TreePlan{a.slots, a.slots ? a.groups / a.kv.heads : 0}, a.batch, a.kv.heads, rows);
+        hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), dim3(g.x, g.y, g.z), dim3(64 * T::kWaves), T::kLds, s, t);
         if (a.slots)
             hipLaunchKernelGGL((k_attn_tree_join<D>), dim3((uint32_t)((rows + 15) / 16), (uint32_t)a.kv.heads, (uint32_t)a.batch),
                                dim3(256), 0, s, t, Dec<BIAS>::kUnshift);

@@ -51,18 +51,9 @@ AttnPlan plan_attn(const KvView& kv, int64_t batch, int64_t total_q, int64_t q_h
 // Trees of more rows than a wave's (k_attn_tiles with TREE).
 static void plan_trees(AttnPlan& p, const KvView& kv, int64_t batch, int64_t rows, int64_t keys)
 {
-    // workgroups that the chip holds at once, by their LDS.  Keys are not cut where every sequence is
-    // short or the tiles alone fill the chip twice.
-    const int64_t slots = kv.dim == 256 ? 256 : 512, round = kv_round(kv.dim);
-    const int64_t tiles = batch * ((rows + kTileRows - 1) / kTileRows), units = keys / round + 2;
-    p.groups = (int32_t)(tiles * kv.heads);
-    if (keys <= round * kMinRounds || tiles * kv.heads >= 2 * slots) return;
-    if (tiles * units >= (int64_t)1 << 30) return;               // rounds are counted in 32 bits
-    // no share makes more parts than these: a part is a share, or the last of its tile
-    const int64_t per_head = slots / kv.heads > 0 ? slots / kv.heads : 1;
-    const int64_t parts = std::min(per_head + tiles, tiles * (units / kMinRounds + 1));
-    p.slots = (int32_t)slots;
-    p.groups = (int32_t)(parts * kv.heads);
+    const TreePlan t = plan_tree(batch, kv.heads, rows, keys, kv.dim);
+    p.slots = t.slots;
+    p.groups = t.parts * kv.heads;
     const size_t n = (size_t)p.groups * kTileRows;
     p.few_ml = n * 2 * sizeof(float);
     p.few_o = n * kv.dim * sizeof(float);

@@ -161,16 +161,6 @@ FP4Q_HD KeyRange tile_part(const KeyRange& first, const KeyRange& last, int32_t 
     return KeyRange{lo, last.hi < lo + chunk ? last.hi : lo + chunk};
 }
 
-// The same for part `part` of `parts` even ones, in whole rounds.
-FP4Q_HD KeyRange tree_part(const KeyRange& first, const KeyRange& last, int32_t round, int32_t part, int32_t parts)
-{
-    const int32_t lo = first.lo / round * round;
-    const int64_t units = (last.hi - lo + round - 1) / round;
-    const int32_t from = lo + (int32_t)(units * part / parts) * round;
-    const int64_t to = lo + units * (part + 1) / parts * round;
-    return KeyRange{from, to < last.hi ? (int32_t)to : last.hi};
-}
-
 struct TilePlan {
     int32_t splits, chunk;
 };
@@ -194,6 +184,76 @@ inline TilePlan plan_tiles(int64_t batch, int64_t heads, int64_t group, int64_t 
     p.splits = (int32_t)want;
     p.chunk = (int32_t)((keys + want * 128 - 1) / (want * 128) * 128);
     return p;
+}
+
+// ---------------------------------------------------------------- keys of trees
+// The rows of a sequence of drafted tokens and a head are tiles of kTileRows, each of which walks the sequence's
+// keys in rounds.  Where that leaves compute units idle, the rounds of every tile are cut into parts, one a workgroup: as
+// many as rounds of `share` give, which follows from all sequences' lengths (read on the device).
+constexpr int kMinRounds = 4;            // rounds of a part, at least
+
+FP4Q_HD int32_t tile_count(int32_t rows) { return (rows + kTileRows - 1) / kTileRows; }
+
+// Parts of `units` where one has `share` at most.
+FP4Q_HD int32_t parts_of(int32_t units, int32_t share) { return (units + share - 1) / share; }
+
+// Rounds that a tile of n drafted tokens after kv - n keys walks, one at least.
+FP4Q_HD int32_t tree_rounds(int32_t kv, int32_t n, int32_t window, int32_t round)
+{
+    const int32_t lo = tree_context(kv, n, window, 0).lo / round * round;
+    return kv - lo > round ? parts_of(kv - lo, round) : 1;
+}
+
+// Rounds of a part: `rounds` of `tiles` tiles of a head, with `slots` workgroups at once and half a part lost a
+// tile.
+FP4Q_HD int32_t tree_share(int32_t rounds, int32_t tiles, int32_t slots, int32_t heads)
+{
+    const int32_t per_head = slots / heads > 1 ? slots / heads : 1;
+    const int32_t most = per_head - tiles / 2, least = (per_head + 3) / 4;
+    const int32_t share = parts_of(rounds, most > least ? most : least);
+    return share > kMinRounds ? share : kMinRounds;
+}
+
+// The keys of part `part` of `parts` even ones, in whole rounds; hi <= lo where it has none.
+FP4Q_HD KeyRange tree_part(const KeyRange& first, const KeyRange& last, int32_t round, int32_t part, int32_t parts)
+{
+    const int32_t lo = first.lo / round * round;
+    const int64_t units = (last.hi - lo + round - 1) / round;
+    const int32_t from = lo + (int32_t)(units * part / parts) * round;
+    const int64_t to = lo + units * (part + 1) / parts * round;
+    return KeyRange{from, to < last.hi ? (int32_t)to : last.hi};
+}
+
+struct TreePlan {
+    int32_t slots;                       // workgroups that the chip holds at once; 0: keys are not cut
+    int32_t parts;                       // of a head's tiles, at most
+};
+
+// For sequences of up to `rows` rows and `keys` keys.
+inline TreePlan plan_tree(int64_t batch, int64_t heads, int64_t rows, int64_t keys, int head_dim)
+{
+    // workgroups at once by their LDS.  Keys are not cut where every sequence is short or the tiles alone fill the
+    // chip twice.
+    const int64_t slots = head_dim == 256 ? 256 : 512, round = kv_round(head_dim);
+    const int64_t tiles = batch * tile_count((int32_t)rows), units = keys / round + 2;
+    if (keys <= round * kMinRounds || tiles * heads >= 2 * slots) return TreePlan{0, 0};
+    if (tiles * units >= (int64_t)1 << 30) return TreePlan{0, 0};   // rounds are counted in 32 bits
+    // no share makes more parts than these: a part is a share, or the last of its tile
+    const int64_t per_head = slots / heads > 0 ? slots / heads : 1;
+    const int64_t by_share = per_head + tiles, by_rounds = tiles * (units / kMinRounds + 1);
+    return TreePlan{(int32_t)slots, (int32_t)(by_share < by_rounds ? by_share : by_rounds)};
+}
+
+// Workgroups of a launch by dimension: parts of the heads, or where keys are not cut heads, tiles and sequences, whose
+// product may pass 32 bits.
+struct TreeGrid {
+    uint32_t x, y, z;
+};
+
+inline TreeGrid tree_grid(const TreePlan& p, int64_t batch, int64_t heads, int64_t rows)
+{
+    if (p.slots) return TreeGrid{(uint32_t)(p.parts * heads), 1, 1};
+    return TreeGrid{(uint32_t)heads, (uint32_t)tile_count((int32_t)rows), (uint32_t)batch};
 }
 
 }  // namespace fp4q

@@ -284,7 +284,7 @@ struct AttnArgs {
     float *few_o, *few_ml;   // few rows: [groups][16 or 32]
     float scale;
     int32_t batch, total_q, q_heads, group, table_cols, max_q, max_kv, causal, window;
-    int32_t slots, groups;   // few rows, trees: workgroups that the chip holds (0: keys are not cut), workgroups
+    int32_t slots, groups;   // few rows, trees: workgroups that the chip holds (0: keys are not cut), workgroups (trees: if cut)
     int32_t splits, chunk;   // many rows: parts of a sequence's keys and the keys of one (a multiple of 128)
     int32_t out_f32;
     const uint8_t* tree;     // fp4_attn_tree: [total_q, tree_cols], drafted keys that a query sees
