@@ -18,6 +18,20 @@ def _need_gpu():
     fq.lib()
 
 
+@pytest.mark.parametrize("fmt,D,batch,window", [("mxfp4", 64, 70, 0), ("nvfp4", 128, 130, 0), ("nvfp4", 64, 130, 700)])
+def test_more_sequences_than_lanes(fmt, D, batch, window):
+    """Ragged trees whose keys are cut, empty ones and ones without a context among them."""
+    rng = np.random.default_rng(batch)
+    ql = rng.integers(1, 7, batch)
+    kv = rng.integers(1, 1700, batch)
+    ql[[0, 63, 64, 69]], ql[[5, 40]] = 6, 0
+    kv[[0, 63, 64, 65, batch - 1]], kv[[7, 66]], kv[68] = 1700, 3, 0
+    s = Setup(fmt, D, 1, 7, 16, [int(n) for n in kv], [int(n) for n in ql], outer=fmt == "nvfp4").device()
+    tree = trees(rng, [int(n) for n in ql], 6)
+    assert fq.fp4_attn_workspace(s.cache, len(tree), 7, batch, max_q=6, max_kv=1700, window=window) is not None
+    check(s, tree, window=window, max_q=6, max_kv=1700)
+
+
 def test_more_workgroups_than_a_dimension_takes():
     """512 sequences of 8 heads with a bound of 2^18 nodes: 2^23 workgroups of 512 lanes."""
     rng = np.random.default_rng(2)
