@@ -857,10 +857,12 @@ def fp4_kv_read(cache, slots, *, dtype=None, stream=None, out=None):
     return k, v
 
 
-def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=None, table_cols=None, window=0):
+def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=None, table_cols=None, window=0, trees=None):
     """Scratch for fp4_attn and fp4_attn_tree calls of this size (None if they need none), to keep
     between calls.  max_q, max_kv, window and table_cols as in the call; without
-    table_cols, the columns that max_kv needs."""
+    table_cols, the columns that max_kv needs.  trees: False sizes it for fp4_attn alone and True for
+    fp4_attn_tree alone, which cuts keys that fp4_attn does not (a prompt of 1024 tokens, 64 / 8 heads of 128: None
+    and 68 MB); None for both."""
     torch = _torch()
     if max_kv is None and table_cols is None:
         raise ValueError("give max_kv or table_cols")
@@ -871,8 +873,8 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
     _ints32("fp4_attn_workspace", *n)
     a = _Attn(batch=n[0], total_q=n[1], q_heads=n[2], table_cols=n[3], max_q=n[4], max_kv=n[5], causal=1, window=n[6],
               scale=1.0, ld_q=n[2] * cache.head_dim, q_starts=16)
-    n = max(f(ct.byref(cache.cfg), cache._ref, ct.byref(a))
-            for f in (lib().fp4q_attn_workspace_bytes, lib().fp4q_attn_tree_workspace_bytes))
+    sizes = {False: lib().fp4q_attn_workspace_bytes, True: lib().fp4q_attn_tree_workspace_bytes}
+    n = max(f(ct.byref(cache.cfg), cache._ref, ct.byref(a)) for t, f in sizes.items() if trees is None or t == bool(trees))
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
 
