@@ -878,21 +878,9 @@ def fp4_attn_workspace(cache, total_q, q_heads, batch, *, max_q=None, max_kv=Non
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
 
-def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv=None, scale=None, causal=True, window=0,
-             sinks=None, out=None, out_dtype=None, with_lse=False, workspace=None, stream=None, _tree=None):
-    """Attention of q (bf16 [tokens, q_heads, head_dim]) over the cache (see
-    include/fp4q.h for masks, limits and rounding).
-
-    page_table   int32 [batch, cols], kv_lens int32 [batch] on the device.
-    q_starts     int32 [batch + 1]: sequence b's queries are q[q_starts[b]:
-                 q_starts[b + 1]]; None: one query each.
-    max_q, max_kv  bounds of the sequences' query and key counts (default: all of q,
-                 all that the page table can name); tight ones make better launches.
-    scale        of q . k, default head_dim ** -0.5.
-    window       > 0: each query sees at most that many keys, up to its own.
-    sinks        float32 [q_heads]: a logit that joins each row's softmax.
-    Returns out (bf16, or out_dtype float32, which also keeps twice the bits of the
-    weights), or (out, lse) with with_lse."""
+def _attention(tree, q, cache, page_table, kv_lens, q_starts, max_q, max_kv, scale, causal, window, sinks, out, out_dtype, with_lse,
+               workspace, stream):
+    """fp4_attn, or fp4_attn_tree with its (checked) mask."""
     torch = _torch()
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, head_dim]")
@@ -931,21 +919,41 @@ def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv
                        D ** -0.5 if scale is None else scale, batch, T, Hq, cols, max_q, max_kv, 1 if causal else 0,
                        window))
     if workspace is None:
-        need = (lib().fp4q_attn_workspace_bytes if _tree is None else lib().fp4q_attn_tree_workspace_bytes)(cfg, cache._ref, a)
+        need = (lib().fp4q_attn_workspace_bytes if tree is None else lib().fp4q_attn_tree_workspace_bytes)(cfg, cache._ref, a)
         if need:
             workspace = _new(need, torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on %s" % dev)
     size, scratch = (0, None) if workspace is None else (workspace.nbytes, workspace.data_ptr())
-    if _tree is None:
+    if tree is None:
         _launch("fp4_attn", lib().fp4_attn, dev, cfg, cache._ref, a, scratch, size, _raw_stream(stream, dev))
     else:
-        _launch("fp4_attn_tree", lib().fp4_attn_tree, dev, cfg, cache._ref, a, _tree.data_ptr(), _tree.shape[1], scratch,
+        _launch("fp4_attn_tree", lib().fp4_attn_tree, dev, cfg, cache._ref, a, tree.data_ptr(), tree.shape[1], scratch,
                 size, _raw_stream(stream, dev))
     return (out, lse) if with_lse else out
 
 
-def fp4_attn_tree(q, cache, page_table, kv_lens, q_starts, tree, **kw):
+def fp4_attn(q, cache, page_table, kv_lens, q_starts=None, *, max_q=None, max_kv=None, scale=None, causal=True, window=0,
+             sinks=None, out=None, out_dtype=None, with_lse=False, workspace=None, stream=None):
+    """Attention of q (bf16 [tokens, q_heads, head_dim]) over the cache (see
+    include/fp4q.h for masks, limits and rounding).
+
+    page_table   int32 [batch, cols], kv_lens int32 [batch] on the device.
+    q_starts     int32 [batch + 1]: sequence b's queries are q[q_starts[b]:
+                 q_starts[b + 1]]; None: one query each.
+    max_q, max_kv  bounds of the sequences' query and key counts (default: all of q,
+                 all that the page table can name); tight ones make better launches.
+    scale        of q . k, default head_dim ** -0.5.
+    window       > 0: each query sees at most that many keys, up to its own.
+    sinks        float32 [q_heads]: a logit that joins each row's softmax.
+    Returns out (bf16, or out_dtype float32, which also keeps twice the bits of the
+    weights), or (out, lse) with with_lse."""
+    return _attention(None, q, cache, page_table, kv_lens, q_starts, max_q, max_kv, scale, causal, window, sinks, out, out_dtype,
+                      with_lse, workspace, stream)
+
+
+def fp4_attn_tree(q, cache, page_table, kv_lens, q_starts, tree, *, max_q=None, max_kv=None, scale=None, window=0, sinks=None,
+                  out=None, out_dtype=None, with_lse=False, workspace=None, stream=None):
     """fp4_attn of trees of drafted tokens: each sequence's queries are the nodes of its tree, and
     their keys are the last of its kv_lens.
 
@@ -958,10 +966,9 @@ def fp4_attn_tree(q, cache, page_table, kv_lens, q_starts, tree, **kw):
         raise ValueError("tree must be bool or uint8 [%d, cols], got %s %s" % (q.shape[0], tree.dtype, list(tree.shape)))
     if not tree.is_contiguous() or tree.device != cache.device:
         raise ValueError("tree must be contiguous and on %s" % cache.device)
-    if "causal" in kw:
-        raise TypeError("fp4_attn_tree takes no causal")
     _ints32("fp4_attn_tree", tree.shape[1])
-    return fp4_attn(q, cache, page_table, kv_lens, q_starts, _tree=tree, **kw)
+    return _attention(tree, q, cache, page_table, kv_lens, q_starts, max_q, max_kv, scale, True, window, sinks, out, out_dtype,
+                      with_lse, workspace, stream)
 
 
 # ------------------------------------------------------------------ mixture of experts
