@@ -1515,13 +1515,13 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s)
         if (a.slots)
             hipLaunchKernelGGL((k_attn_tree_join<D>), dim3((uint32_t)((rows + 15) / 16), (uint32_t)a.kv.heads, (uint32_t)a.batch),
                                dim3(256), 0, s, t, Dec<BIAS>::kUnshift);
-        return hipGetLastError();
-    }
-    const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
-    hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
-    if (a.splits > 1) {
-        const int64_t all = (int64_t)a.total_q * a.q_heads;
-        hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
+    } else {
+        const dim3 grid((uint32_t)a.kv.heads, (uint32_t)((rows + kTileRows - 1) / kTileRows), (uint32_t)(a.batch * a.splits));
+        hipLaunchKernelGGL((k_attn_tiles<D, BIAS, FINE, TREE>), grid, dim3(64 * T::kWaves), T::kLds, s, a);
+        if (a.splits > 1) {
+            const int64_t all = (int64_t)a.total_q * a.q_heads;
+            hipLaunchKernelGGL((k_attn_join<D>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a, Dec<BIAS>::kUnshift);
+        }
     }
     return hipGetLastError();
 }
