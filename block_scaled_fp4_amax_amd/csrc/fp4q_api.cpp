@@ -1075,6 +1075,8 @@ int fp4_add_rms_norm(const fp4q_add_rms_norm* norm, void* stream)
         (o.fp8_mode == 2 && misaligned(o.fp8_scales, 4)) || bad_pitch(o.rows, o.ld_x, o.x_dtype) ||
         (o.residual && bad_pitch(o.rows, o.ld_residual, o.residual_dtype)))
         return FP4Q_ERR_ALIGN;
+    // h's contiguous rows would overwrite rows of a pitched residual that are still to be read
+    if (o.residual && o.residual == o.residual_out && o.rows > 1 && o.ld_residual != o.hidden) return FP4Q_ERR_SHAPE;
     NormArgs a;
     a.x = o.x;
     a.residual = o.residual;
@@ -1117,6 +1119,7 @@ int fp4_add_rms_norm_backward(const fp4q_rms_norm_grad* grad, void* workspace, s
         misaligned(o.rstd, 4) || misaligned(o.dx, 16) || misaligned(o.dweight, 16) || bad_pitch(o.rows, o.ld_dy, o.dy_dtype) ||
         bad_pitch(o.rows, o.ld_h, o.h_dtype) || (o.dresidual && bad_pitch(o.rows, o.ld_dresidual, o.h_dtype)))
         return FP4Q_ERR_ALIGN;
+    if (o.dresidual && o.dresidual == o.dx && o.rows > 1 && o.ld_dresidual != o.hidden) return FP4Q_ERR_SHAPE;   // as above
     const NormGradPlan p = plan_rms_norm_backward(o.rows, o.hidden);
     if (o.dweight && p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return FP4Q_ERR_WORKSPACE;
     if (o.dweight && p.bytes > 0 && misaligned(workspace, 16)) return FP4Q_ERR_ALIGN;

@@ -655,7 +655,8 @@ typedef struct {
     int64_t ld_x, ld_residual;
     const void* weight;        /* [hidden]                                                      */
     void* residual_out;        /* h [rows, hidden] in the residual's type, written; may be residual
-                                  itself where that is contiguous; NULL without a residual       */
+                                  itself where that is contiguous (FP4Q_ERR_SHAPE: with a pitch);
+                                  NULL without a residual                                       */
     float* rstd;               /* r [rows] or NULL                                              */
     void* y;                   /* [rows, hidden] or NULL                                        */
     uint8_t* fp8;              /* E4M3 codes of y [rows, hidden] (fp8_mode)                      */
@@ -695,7 +696,8 @@ typedef struct {
     const void* weight;        /* [hidden]                                                      */
     const float* rstd;         /* [rows] of the forward call                                    */
     void* dx;                  /* [rows, hidden], h's type: the gradient of x and of residual, written;
-                                  may be dresidual itself where that is contiguous               */
+                                  may be dresidual itself where that is contiguous (FP4Q_ERR_SHAPE:
+                                  with a pitch)                                                 */
     float* dweight;            /* FP32 [hidden] or NULL, written                                 */
     int64_t rows, hidden;
     int32_t dy_dtype, h_dtype, weight_dtype, reserved;
