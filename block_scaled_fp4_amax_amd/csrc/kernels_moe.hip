@@ -593,8 +593,7 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a)
 
 // ---------------------------------------------------------------- a few tokens
 // A wave takes rows of W as they lie, 16 values a lane and 1024 a pass, and multiplies them with its token's
-// values in binary32: G[m] x is exact, each block of 16 is summed and its scales (inner times outer) multiply the
-// sum.  No product is wasted on tokens that are not there, a row is read in whole lines, and waves need neither
+// values in binary32: each 16 products are summed and their scales (inner times outer) multiply the sum.  No product is wasted on tokens that are not there, a row is read in whole lines, and waves need neither
 // LDS nor a launch to join.  Each wave finds its token's experts itself.
 // One token, 4 of 32 experts of 2880 x 2880 (NVFP4, 2D outer scales, 56 MB): 14 + 11 us, where groups take 35 in all.
 // Bound: the trips one after another (logits, weights, the second launch, its logits, weights), about 7 us of each
@@ -607,6 +606,9 @@ constexpr int kFewWaves = 4;
 template <int BIAS, int OUTER, int R, int RUN, bool X32>
 struct Pass {
     static constexpr int B = Dec<BIAS>::kBlock;
+    // Codes enter as 2^-7 of their values (MXFP4: of their scaled values), since sixteen products of up to 6 x may pass binary32
+    // where a scale brings them back; NVFP4's and AMD-FP4's sums of rows are multiplied by kBack.
+    static constexpr float kBack = BIAS == 0 ? 1.0f : 0x1p7f;
     uint2 c[R];
     uint32_t s[R];
     float o[OUTER == kPerTile ? R / RUN : OUTER == kPerRow ? R : 1];
@@ -643,20 +645,23 @@ struct Pass {
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            // MXFP4's 2^k enters with the codes as 2^(k - 7) and with the sum as the rest (the conversion reads the
+            // exponent alone: byte 0 is 2^-127, 0xFF NaN); others' scales multiply the sum
+            const uint32_t part = s[r] == 0xFFu ? 0xFFu : s[r] > 7 ? s[r] - 7 : 0;
+            const float with_codes = BIAS == 0 ? __uint_as_float(part << 23) : 1.0f / kBack;
+            float d;
+            if constexpr (BIAS == 0) d = __uint_as_float((min(s[r], 7u) + 127) << 23);
+            else d = DecBf16<BIAS>::scale(s[r]) * (OUTER == kInnerOnly ? whole : o[OUTER == kPerTile ? r / RUN : r]);
             float sum = 0.0f;
             const auto eight = [&](uint32_t code, const float* p) {
                 const auto two = [&](auto g, const float* q) { sum = __builtin_fmaf(g[1], q[1], __builtin_fmaf(g[0], q[0], sum)); };
-                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 0), p);
-                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 1), p + 2);
-                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 2), p + 4);
-                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.0f, 3), p + 6);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, with_codes, 0), p);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, with_codes, 1), p + 2);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, with_codes, 2), p + 4);
+                two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, with_codes, 3), p + 6);
             };
             eight(c[r].x, v);
             eight(c[r].y, v + 8);
-            // MXFP4's byte 0 is 2^-127, 0xFF NaN
-            float d = BIAS != 0 ? DecBf16<BIAS>::scale(s[r])
-                                : s[r] == 0 ? 0x1p-127f : s[r] == 0xFFu ? __builtin_nanf("") : __uint_as_float(s[r] << 23);
-            d *= OUTER == kInnerOnly ? whole : o[OUTER == kPerTile ? r / RUN : r];
             acc[r] = __builtin_fmaf(sum, d, acc[r]);
         }
     }
@@ -711,7 +716,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_up(MoeArgs a)
     float g = 0.0f, u = 0.0f;
 #pragma unroll
     for (int r = 0; r < kFewUpRows; ++r) {
-        const float gr = wave_sum(acc[r]), ur = wave_sum(acc[kFewUpRows + r]);
+        const float gr = wave_sum(acc[r]) * P::kBack, ur = wave_sum(acc[kFewUpRows + r]) * P::kBack;
         g = lane == r ? gr : g;
         u = lane == r ? ur : u;
     }
@@ -762,7 +767,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_moe_few_down(MoeArgs a)
     float y = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float v = wave_sum(acc[r]);
+        const float v = wave_sum(acc[r]) * P::kBack;
         y = lane == r ? v : y;
     }
     if (lane < R) join[wave][lane] = y;

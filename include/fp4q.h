@@ -636,8 +636,10 @@ typedef struct {
  *            fp4_linear), or TENSORWISE with one FP32 scale for each expert ([experts]).
  * Each expert is read once for the tokens that it takes, 64 of the call's at a time (calls of few tokens read it for
  * each of them).
- * W enters the products exactly, sums are binary32, and a_te act enters W2 with a relative 2^-16 or less.  Sums are joined in an order that the call's sizes
- * and the token's own choices give: equal calls give equal bits.
+ * W enters the products exactly, sums are binary32, and a_te act enters W2 with a relative 2^-16 or less.  Outer scales in 1D or
+ * 2D multiply sums of up to 64 products, which pass binary32's range where x or a_te act is beyond 2^102 (y may be infinite or NaN);
+ * MXFP4 values of 2^128 and more (scale bytes 253 and 254) may count as infinite.  Sums are joined in an order that the
+ * call's sizes and the token's own choices give: equal calls give equal bits.
  * workspace: fp4q_moe_workspace_bytes() bytes, 16-byte aligned; no initial value, nothing kept.
  * Needs hidden % 32 == 0 and inter % 32 == 0, 1 <= top_k <= experts (FP4Q_ERR_SHAPE); tokens <= 1024, experts <= 512,
  * top_k <= 32, hidden and inter <= 2^16, ld_x <= 2^22 (FP4Q_ERR_UNSUPPORTED).
