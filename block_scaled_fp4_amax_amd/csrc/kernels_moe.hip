@@ -29,6 +29,8 @@
 // Rounding.  a act enters W2 as two bf16 terms (good to 2^-16), which lie side by side in the
 // registers while a unit of W2 is decoded once for both; one term would add its 2^-8 to that of y.  A few tokens' a act
 // stays binary32.
+#include <algorithm>
+
 #include "fp4q_device.h"
 #include "launch.h"
 #include "lds_load.h"
@@ -816,8 +818,7 @@ hipError_t launch_outer(const MoeArgs& a, hipStream_t s)
     else if (a.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), dim3(1), dim3(kRouteThreads), 0, s, a);
     else hipLaunchKernelGGL((k_moe_route<8>), dim3(1), dim3(kRouteThreads), 0, s, a);
     if (a.group == 16) return launch_products<BIAS, OUTER, 1>(a, s);
-    if (a.group == 32) return launch_products<BIAS, OUTER, 2>(a, s);
-    return launch_products<BIAS, OUTER, 4>(a, s);
+    return launch_products<BIAS, OUTER, 2>(a, s);
 }
 
 template <int BIAS>
@@ -842,18 +843,24 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     // (NVFP4) 24 : 35, 16 65 : 70, 24 91 : 87, 48 156 : 115; 9 pairs of 20 experts of 2048 x 736
     // (AMD-FP4) 15 : 21, 21 22 : 27, 30 30 : 28.
     p.few = pairs <= kMoeFewPairs ? 1 : 0;
-    // Pairs of a group: an expert of more is read again for each further group (from the caches), one of
-    // fewer pays for tiles of tokens that it has not.  An expert's pairs are at most the tokens.
-    p.group = tokens <= 16 || pairs <= 8 * experts ? 16 : tokens <= 32 || pairs <= 20 * experts ? 32 : 64;
+    // Pairs of a group: an expert of more is read again for each further group (from the caches), one of fewer pays for
+    // tiles of tokens that it has not.  Groups of 32 where most experts have more than 16 pairs and at most 32.  Groups of 16
+    // against 32, us, 8 experts of 2880 x 2880, 4 a token (NVFP4): 16 pairs an expert 65 : 74 (2D outer), 17 65 : 68, 19 74 : 69, 24
+    // 78 : 72, 28 83 : 77, 32 88 : 89, 4 experts of 64 each 83 : 84 (2D); 16 of 2048 x 1024, 8 a token (AMD-FP4, 1D): 18
+    // 60 : 51, 26 64 : 57, 32 77 : 78.  (Groups of 64 were slower everywhere: 64 pairs an expert 98, 24 136.)
+    const bool more = tokens > 32 && pairs > 17 * experts;
+    p.group = more && pairs <= 30 * experts ? 32 : 16;
     const int64_t reached = experts < pairs ? experts : pairs;
-    p.max_groups = (int32_t)(reached + (tokens > p.group ? pairs / p.group : 0));
+    const auto groups_of = [&](int64_t group, int64_t n) { return reached + (tokens > group ? n / group : 0); };
+    p.max_groups = (int32_t)groups_of(p.group, pairs);
+    // room for either, so that scratch of more tokens serves fewer
+    const int64_t places = std::max(groups_of(16, pairs) * 16, more ? groups_of(32, std::min(pairs, 30 * experts)) * 32 : 0);
     size_t at = 0;
     const auto take = [&at](size_t n) { const size_t here = at; at += padded(n); return here; };
-    p.groups = take(p.max_groups * sizeof(MoeGroup));
+    p.groups = take(places / 16 * sizeof(MoeGroup));
     p.expert = take(pairs * 4);
     p.share = take(pairs * 4);
     p.place = take(pairs * 4);
-    const int64_t places = (int64_t)p.max_groups * p.group;
     p.pair_token = take(places * 4);
     p.pair_share = take(places * 4);
     p.mid = take(places * inter * 4);

@@ -1,5 +1,5 @@
 """GPU tests of fp4_moe's further paths against the same binary64 layer and bounds as tests/test_gpu_moe.py: rows of
-more than one chunk of 4096 values, whose scale bytes are laid into LDS chunk by chunk, in groups of 16, 32 and 64 pairs and row by
+more than one chunk of 4096 values, whose scale bytes are laid into LDS chunk by chunk, in groups of 16 and 32 pairs and row by
 row; and tokens whose experts are excluded in calls of few pairs."""
 import numpy as np
 import pytest
@@ -22,14 +22,26 @@ def _need_gpu():
     ("mxfp4", "none", 4128, 64), ("mxfp4", "none", 64, 4128), ("mxfp4", "none", 8256, 64), ("nvfp4", "none", 4096, 32),
     ("nvfp4", "2d", 4160, 64), ("nvfp4", "2d", 64, 8256), ("nvfp4", "1d64", 4160, 128), ("nvfp4", "tensor", 96, 8224),
     ("amdfp4", "none", 8224, 96), ("amdfp4", "1d192", 8256, 192), ("amdfp4", "1d192", 192, 4224), ("amdfp4", "2d", 4160, 4160)])
-@pytest.mark.parametrize("T", [2, 16, 30, 50])
-def test_rows_of_several_chunks(fmt, kind, H, I, T):
-    """2 experts, both taken: 4 pairs row by row, then groups of 16 (up to 16 tokens), 32 and 64 (more than 8 and 20 pairs an
-    expert)."""
+@pytest.mark.parametrize("T,E", [(2, 2), (16, 2), (30, 2), (40, 4)])
+def test_rows_of_several_chunks(fmt, kind, H, I, T, E):
+    """4 pairs row by row, groups of 16 (one and more an expert), and of 32 (20 pairs an expert)."""
     rng = np.random.default_rng(H + I + T)
-    layer = Layer(fmt, kind, 2, H, I, bias=T == 30)
-    x, l = tokens(rng, T, H), logits_of(rng, T, 2)
+    layer = Layer(fmt, kind, E, H, I, bias=T == 30)
+    x, l = tokens(rng, T, H), logits_of(rng, T, E)
     layer.check(x, l, 2, interleaved=T == 16, out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("T,E,k", [(33, 2, 1), (34, 6, 3), (64, 7, 2), (64, 10, 3), (35, 2, 2), (64, 4, 2), (61, 4, 2)])
+def test_groups_around_their_bounds(T, E, k):
+    """Pairs an expert at and beside 17 and 30, where groups are of 16 or 32, evenly and all of the same experts."""
+    rng = np.random.default_rng(T + E)
+    layer = Layer("nvfp4", "1d64", E, 192, 128, bias=True)
+    x, l = tokens(rng, T, 192), logits_of(rng, T, E)
+    y = layer.check(x, l, k)
+    ws = fq.fp4_moe_workspace(64, E, k, 192, 128)        # of more tokens
+    assert torch.equal(layer.run(x, l, k, workspace=ws), y)
+    l[:, :k] += 50
+    layer.check(x, l, k)
 
 
 @pytest.mark.parametrize("k", [1, 2, 3])
