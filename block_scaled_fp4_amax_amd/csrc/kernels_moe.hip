@@ -3,11 +3,11 @@
 //   y_t = sum over the k experts e with token t's largest logits of
 //         a_te (W2_e act(W1_e x_t + b1_e) + b2_e),   a_te the softmax of the logits
 //
-// Every expert that a token reached is read once, which is what bounds the layer: 4 bits
-// and a scale's share a weight, for few tokens each.  Four launches:
+// Reading every expert that a token reached is what bounds the layer: 4 bits and a scale's share a
+// weight, for few tokens each.  Four launches:
 //   k_moe_route  one workgroup: each token's experts and their shares, then the (token, expert)
-//                pairs in the order of the experts and their groups of up to 16 MT
-//                pairs of one expert;
+//                pairs in the order of the experts and their groups of up to 16 MT (MT 1 or 2)
+//                pairs of one expert, for each of which the expert is read (plan_moe);
 //   k_moe_up     a workgroup takes 32 gate and 32 up rows of W1 for one group; its waves share K
 //                and join through LDS; a times the activation goes to the scratch;
 //   k_moe_down   the same for 64 rows of W2; each pair's products go to the scratch in binary32;
@@ -16,19 +16,23 @@
 //                going through all groups with no scratch, took 58 us for 48 tokens of 32 experts of
 //                2880 x 2880 where k_moe_down and k_moe_join took 44, with activations of one bf16
 //                term: parts of K a wave end at every group.)
-// 48 tokens, 4 of 32 experts of 2880 x 2880 each (MXFP4, 423 MB of weights): 7 + 73 + 45 + 5 us, k_moe_up 3.9 TB/s.  Bound:
-// loads in flight.  A wave holds a unit of 64 bytes of 64 rows and the next one; four waves a SIMD instead of three
-// spill the second (81 us), loads past the caches fetch lines twice (85: two waves share each line), two units
-// of a line by one wave 76, 128 rows a workgroup 75.
+// 48 tokens, 4 of 32 experts of 2880 x 2880 each (MXFP4, 423 MB of weights): 7 + 73 + 45 + 5 us, k_moe_up 3.9 TB/s; NVFP4 with
+// 2D outer scales (448 MB) 7 + 85 + 53 + 5; 64 tokens, 8 of those, 11 + 116 + 76 + 6.  Bound: loads in flight.  A wave holds a unit
+// of 64 bytes of 64 rows and the next one, in registers.  Waves a SIMD by those: three in k_moe_up for all formats and in k_moe_down for MXFP4;
+// two in k_moe_down for NVFP4 and AMD-FP4 (172 registers with 2D outer scales, 230 without), and with MT = 2.  Tried with MXFP4, k_moe_up:
+// four waves spill the second unit (81 us), loads past the caches fetch lines twice (85: two waves share each line), two units
+// of a line by one wave 76, 128 rows a workgroup 75.  Not tried: units that wait in LDS, which loads straight to it
+// (lds_load.h) would hold without registers.
 // Up to kMoeFewPairs pairs take two launches instead, rows of W as they lie (below).
 //
 // Products as in kernels_linear.hip: v_mfma_f32_16x16x32_bf16 with rows of W decoded to bf16,
 // exactly, as the A operand and tokens as the B operand; a unit is 128 values of K, of which
 // lane l loads 32 (l / 16) .. + 31 of row l % 16.  Sums are binary32.
 //
-// Rounding.  a act enters W2 as two bf16 terms (good to 2^-16), which lie side by side in the
-// registers while a unit of W2 is decoded once for both; one term would add its 2^-8 to that of y.  A few tokens' a act
-// stays binary32.
+// Rounding.  a act enters W2 as two bf16 terms (good to 2^-16); one term would add its 2^-8 to that of y.  With MT = 1 the terms lie
+// side by side in the registers while a unit of W2 is decoded once for both; with MT = 2 there is no room for that
+// (rows64), and each 4096 values of W2 are loaded (again from the caches) and decoded for one term, then for the other.  A few
+// tokens' a act stays binary32.
 #include <algorithm>
 
 #include "fp4q_device.h"

@@ -634,7 +634,7 @@ typedef struct {
  *   W1, W2   rowwise buffers as fp4_quantize or fp4_cast_transpose_grouped write them for the stacked
  *            rows, codes 16-byte aligned, NVFP4's and AMD-FP4's scale bytes 2.  Outer scales: none, 2D of 64, 1D of a multiple of 64 (as in
  *            fp4_linear), or TENSORWISE with one FP32 scale for each expert ([experts]).
- * Each expert is read once for the tokens that it takes, 64 of the call's at a time (calls of few tokens read it for
+ * An expert is read for up to 16 or 32 of its tokens together, among 64 of the call's at a time (calls of few tokens read it for
  * each of them).
  * W enters the products exactly, sums are binary32, and a_te act enters W2 with a relative 2^-16 or less.  Outer scales in 1D or
  * 2D multiply sums of up to 64 products, which pass binary32's range where x or a_te act is beyond 2^102 (y may be infinite or NaN);
@@ -681,7 +681,8 @@ typedef struct {
  *   fp8_mode 1  the scale of fp4_mx_project_fp8's mx8_row: 2^E for 32 values, E = floor(log2 amax) - 8
  *               within [-127, 127] (byte 0 where there is no finite nonzero value); hidden % 32 == 0;
  *   fp8_mode 2  amax / 448 for a row, in binary32, and the quotients rounded to binary32 first;
- * amax over the finite values of y before it is rounded to y_dtype.  Results do not depend on how
+ * amax over the finite values of y before it is rounded to y_dtype (a row's scale of 0 makes its infinities NaN
+ * codes).  Results do not depend on how
  * rows are shared among lanes, so equal rows give equal bits in every call.
  * Needs hidden % 8 == 0 (FP4Q_ERR_SHAPE), hidden <= 16384, rows < 2^26 and rows < 2^31 / (hidden / 8)
  * (FP4Q_ERR_UNSUPPORTED), all buffers but rstd and fp8_scales 16-byte aligned.
