@@ -1214,10 +1214,13 @@ struct TreePlace {
     int tiles;
 };
 
-// Workgroup `place` of a head where keys are cut: the parts of sequence after sequence, tiles side by side in each.
+// Workgroup `place` of a head: the parts of sequence after sequence, tiles side by side in each.
+// (Calls whose keys are not cut return here too: a branch around this in the kernel reloaded two more spilled registers a
+// round at head_dim 128, and 4 trees of 26 after up to 131072 keys took 302 us for 271.)
 template <int D>
 __device__ __forceinline__ TreePlace tree_place(const AttnArgs& a, int place, int lane)
 {
+    if (a.slots == 0) return TreePlace{(int)blockIdx.z, (int)blockIdx.y, 0, 1, 0, 0};   // one workgroup a tile (tree_grid)
     TreeSeq mine = tree_seq<D>(a, lane);
     const int share = share_of_trees<D>(a, mine, lane);
     int before = 0;
@@ -1330,14 +1333,10 @@ __global__ __launch_bounds__(512, D == 256 ? 2 : 4) void k_attn_tiles(AttnArgs a
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     int head, b, split, block, parts = 1;
     if constexpr (TREE) {
-        if (a.slots == 0) {                              // one workgroup a tile
-            head = (int)blockIdx.x, block = (int)blockIdx.y, b = (int)blockIdx.z, split = 0;
-        } else {
-            head = (int)blockIdx.x % a.kv.heads;
-            const TreePlace p = tree_place<D>(a, (int)blockIdx.x / a.kv.heads, lane);
-            if (p.parts == 0) return;
-            b = p.seq, block = p.tile, split = p.part, parts = p.parts;
-        }
+        head = (int)blockIdx.x % a.kv.heads;
+        const TreePlace p = tree_place<D>(a, (int)blockIdx.x / a.kv.heads, lane);
+        if (p.parts == 0) return;
+        b = p.seq, block = p.tile, split = p.part, parts = p.parts;
     } else {
         head = (int)blockIdx.x;
         b = (int)blockIdx.z % a.batch, split = (int)blockIdx.z / a.batch;
