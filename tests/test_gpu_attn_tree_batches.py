@@ -1,5 +1,6 @@
-"""GPU tests of fp4_attn_tree in batches of more sequences than a wave has lanes, and in launches of more workgroups than
-one dimension takes, against the same binary64 reference and bounds as tests/test_gpu_attn_tree.py."""
+"""GPU tests of fp4_attn_tree in batches of more sequences than a wave has lanes, of several tiles whose keys are not cut, and
+in launches of more workgroups than one dimension takes, against the same binary64 reference and bounds as
+tests/test_gpu_attn_tree.py."""
 import numpy as np
 import pytest
 import torch
@@ -16,6 +17,15 @@ def _need_gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     fq.lib()
+
+
+@pytest.mark.parametrize("fmt,D", [("mxfp4", 64), ("nvfp4", 128), ("amdfp4", 256)])
+def test_several_tiles_of_keys_that_are_not_cut(fmt, D):
+    """Up to 528 rows of a sequence and head, five tiles, and at most 256 keys, four rounds."""
+    ql = [66, 40, 0, 66, 5, 17]
+    s = Setup(fmt, D, 2, 8, 16, [250, 200, 30, 66, 256, 9], ql, outer=fmt == "nvfp4").device()
+    assert fq.fp4_attn_workspace(s.cache, sum(ql), 16, len(ql), max_q=66, max_kv=256, trees=True) is None
+    check(s, trees(np.random.default_rng(D), ql, 66), max_q=66, max_kv=256)
 
 
 @pytest.mark.parametrize("fmt,D,batch,window", [("mxfp4", 64, 70, 0), ("nvfp4", 128, 130, 0), ("nvfp4", 64, 130, 700)])
