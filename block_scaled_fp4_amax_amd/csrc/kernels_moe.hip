@@ -848,17 +848,19 @@ MoePlan plan_moe(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     // (AMD-FP4) 15 : 21, 21 22 : 27, 30 30 : 28.
     p.few = pairs <= kMoeFewPairs ? 1 : 0;
     // Pairs of a group: an expert of more is read again for each further group (from the caches), one of fewer pays for
-    // tiles of tokens that it has not.  Groups of 32 where most experts have more than 16 pairs and at most 32.  Groups of 16
-    // against 32, us, 8 experts of 2880 x 2880, 4 a token (NVFP4): 16 pairs an expert 65 : 74 (2D outer), 17 65 : 68, 19 74 : 69, 24
-    // 78 : 72, 28 83 : 77, 32 88 : 89, 4 experts of 64 each 83 : 84 (2D); 16 of 2048 x 1024, 8 a token (AMD-FP4, 1D): 18
-    // 60 : 51, 26 64 : 57, 32 77 : 78.  (Groups of 64 were slower everywhere: 64 pairs an expert 98, 24 136.)
-    const bool more = tokens > 32 && pairs > 17 * experts;
-    p.group = more && pairs <= 30 * experts ? 32 : 16;
+    // tiles of tokens that it has not, and with few experts more groups fill the chip better.  Groups of 16 against
+    // 32, us, by pairs an expert: 8 experts of 2880 x 2880, 4 a token (NVFP4) 16 65 : 74, 17 65 : 68, 19 74 : 69, 24 78 : 72, 28
+    // 83 : 77, 32 88 : 89; all 8 a token (MXFP4) 20 67 : 63, 32 71 : 73, 33 91 : 103, 48 101 : 107, 49 113 : 107, 64 124 : 115; 16 of
+    // 2048 x 1024, 8 a token (AMD-FP4, 1D) 18 60 : 51, 26 64 : 57, 32 77 : 78; 2 of 2880 x 2880 (NVFP4, 2D) 20
+    // 40 : 46, 40 51 : 55, 64 56 : 58.  Groups of 64 (one wave a SIMD but for MXFP4) gain at most 5 % on the better of
+    // these (49 of each of the 8, MXFP4, 102) and lose up to 70 % (24 of each of 8, 4 a token, NVFP4, 2D, 136 for 79).
+    const bool most = experts >= 4 && pairs > 17 * experts;
+    p.group = most && (pairs <= 30 * experts || pairs > 48 * experts) ? 32 : 16;
     const int64_t reached = experts < pairs ? experts : pairs;
-    const auto groups_of = [&](int64_t group, int64_t n) { return reached + (tokens > group ? n / group : 0); };
-    p.max_groups = (int32_t)groups_of(p.group, pairs);
+    const auto groups_of = [&](int64_t group) { return reached + (tokens > group ? pairs / group : 0); };
+    p.max_groups = (int32_t)groups_of(p.group);
     // room for either, so that scratch of more tokens serves fewer
-    const int64_t places = std::max(groups_of(16, pairs) * 16, more ? groups_of(32, std::min(pairs, 30 * experts)) * 32 : 0);
+    const int64_t places = std::max(groups_of(16) * 16, most ? groups_of(32) * 32 : 0);
     size_t at = 0;
     const auto take = [&at](size_t n) { const size_t here = at; at += padded(n); return here; };
     p.groups = take(places / 16 * sizeof(MoeGroup));

@@ -31,9 +31,10 @@ def test_rows_of_several_chunks(fmt, kind, H, I, T, E):
     layer.check(x, l, 2, interleaved=T == 16, out_dtype=torch.float32)
 
 
-@pytest.mark.parametrize("T,E,k", [(33, 2, 1), (34, 6, 3), (64, 7, 2), (64, 10, 3), (35, 2, 2), (64, 4, 2), (61, 4, 2)])
+@pytest.mark.parametrize("T,E,k", [(34, 4, 2), (35, 4, 2), (60, 4, 2), (61, 4, 2), (48, 4, 4), (49, 4, 4), (64, 7, 7), (18, 5, 5), (32, 6, 6),
+                                   (64, 3, 2), (64, 10, 3)])
 def test_groups_around_their_bounds(T, E, k):
-    """Pairs an expert at and beside 17 and 30, where groups are of 16 or 32, evenly and all of the same experts."""
+    """Pairs an expert at and beside 17, 30 and 48, where groups are of 16 or 32, evenly and all of the same experts."""
     rng = np.random.default_rng(T + E)
     layer = Layer("nvfp4", "1d64", E, 192, 128, bias=True)
     x, l = tokens(rng, T, 192), logits_of(rng, T, E)
